@@ -24,7 +24,10 @@ EXPORTS = ("engram_status_string", "engram_plan_create", "engram_plan_destroy", 
            "engram_cache_observe", "engram_cache_build", "engram_stage_a_cached", "engram_cache_stats",
            "engram_cache_set_dedup", "engram_quantize_fp8", "engram_plan_set_sm_limit", "engram_plan_host_gather_sms", "engram_plan_set_host_gather_sms",
            "engram_sm_split_create", "engram_sm_split_sms", "engram_sm_split_stream", "engram_sm_split_destroy",
-           "engram_forward_split", "engram_stage_a_e4m3", "engram_stage_a_layers_e4m3", "engram_stage_b_e4m3")
+           "engram_forward_split", "engram_stage_a_e4m3", "engram_stage_a_layers_e4m3", "engram_stage_b_e4m3",
+           "engram_attn_plan_create", "engram_attn_plan_destroy", "engram_attn_get_error", "engram_attn_workspace_bytes",
+           "engram_kv_cache_create", "engram_kv_cache_destroy", "engram_qk_norm_rope", "engram_kv_append",
+           "engram_paged_attention", "engram_verify_drafts")
 
 
 class Config(ctypes.Structure):
@@ -42,6 +45,22 @@ class Weights(ctypes.Structure):
 
 class State(ctypes.Structure):
     _fields_ = [("prev_ids", ctypes.c_void_p), ("u_ring", ctypes.c_void_p), ("pos", ctypes.c_void_p)]
+
+
+class AttnConfig(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int), ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int), ("page", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("rope_adjacent", ctypes.c_int),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class HeadsView(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Sequences(ctypes.Structure):
+    _fields_ = [("start", ctypes.c_void_p), ("length", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("table_pages", ctypes.c_int), ("tokens", ctypes.c_int64),
+                ("max_new", ctypes.c_int)]
 
 
 class EngramError(RuntimeError):
@@ -110,6 +129,17 @@ def _lib() -> ctypes.CDLL:
                                             ctypes.POINTER(State), vp, sz, vp]
         lib.engram_plan_set_fused_decode.argtypes = [vp, i32]
         lib.engram_plan_kernel_times.argtypes = [vp, ctypes.POINTER(ctypes.c_float), i32, ctypes.POINTER(i32)]
+        lib.engram_attn_plan_create.argtypes = [ctypes.POINTER(AttnConfig), ctypes.POINTER(vp)]
+        lib.engram_attn_plan_destroy.argtypes = [vp]
+        lib.engram_attn_get_error.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
+        lib.engram_attn_workspace_bytes.argtypes = [vp, ctypes.POINTER(sz)]
+        lib.engram_kv_cache_create.argtypes = [vp, vp, vp, i64, ctypes.POINTER(vp)]
+        lib.engram_kv_cache_destroy.argtypes = [vp]
+        # pointers to views and sequences as plain addresses (byref), which the front end keeps filled
+        lib.engram_qk_norm_rope.argtypes = [vp, vp, vp, i64, vp, vp, i32, vp, vp, vp, vp, vp]
+        lib.engram_kv_append.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp]
+        lib.engram_paged_attention.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+        lib.engram_verify_drafts.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]
         for name in EXPORTS:
             if name not in ("engram_status_string", "engram_sm_split_stream"):   # those two return pointers
                 getattr(lib, name).restype = i32

@@ -1,0 +1,259 @@
+"""Python front end of the attention sub-block's C ABI (include/engram_attention.h).
+
+Argument marshalling only, as in engram.py: every step runs in the library's
+CUDA kernels on the current stream, tensors are passed by pointer.  Outputs are
+allocated unless given.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from .engram import _ACT_DTYPES, _dev, _stream
+
+_ROPE_STYLES = {"halves": 0, "adjacent": 1}
+
+
+def _view(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, head_dim: int,
+          tokens: Optional[int] = None) -> _lib.HeadsView:
+    """A [tokens, heads, head_dim] device tensor whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or (tokens is not None and shape[0] != tokens):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected "
+                         f"({'tokens' if tokens is None else tokens}, {heads}, {head_dim})")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and shape[0]:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    # the stride of a dimension of one element is never used and may be anything
+    return _lib.HeadsView(t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if heads > 1 else 0)
+
+
+def _norm_weight(g: Optional[torch.Tensor], name: str, head_dim: int) -> int:
+    return 0 if g is None else _dev(g, name, torch.float32, (head_dim,))
+
+
+class AttentionPlan:
+    """A validated attention shape bound to the current CUDA device.
+
+    ``rotary_dim`` elements of each head are rotated (default: all); ``rope_style``
+    pairs element i with i + rotary_dim/2 ("halves") or 2i with 2i+1 ("adjacent").
+    ``scale`` multiplies q.k (default 1/sqrt(head_dim))."""
+
+    def __init__(self, *, heads: int, heads_kv: int, head_dim: int, page: int = 64, dtype: str = "bf16",
+                 rotary_dim: Optional[int] = None, rope_style: str = "halves", eps: float = 1e-6,
+                 scale: Optional[float] = None):
+        if rope_style not in _ROPE_STYLES:
+            raise ValueError(f"rope_style: {rope_style!r}, expected one of {sorted(_ROPE_STYLES)}")
+        if dtype not in _ACT_DTYPES:
+            raise ValueError(f"dtype: {dtype!r}, expected one of {sorted(_ACT_DTYPES)}")
+        if scale is not None and not scale > 0:
+            raise ValueError("scale: must be positive")
+        self.heads, self.heads_kv, self.head_dim, self.page = heads, heads_kv, head_dim, page
+        self.dtype, self.rope_style, self.eps, self.scale = dtype, rope_style, eps, scale
+        self.rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        self.torch_dtype = _ACT_DTYPES[dtype][1]
+        cfg = _lib.AttnConfig(heads, heads_kv, head_dim, page, _ACT_DTYPES[dtype][0], self.rotary_dim,
+                              _ROPE_STYLES[rope_style], eps, 0.0 if scale is None else scale)
+        self._lib = _lib._lib()
+        self._h = ctypes.c_void_p()
+        self._workspaces = {}
+        torch.cuda.current_device()   # make sure a context exists on the current device
+        _lib.check(self._lib.engram_attn_plan_create(ctypes.byref(cfg), ctypes.byref(self._h)),
+                   "engram_attn_plan_create")
+        n = ctypes.c_size_t()
+        _lib.check(self._lib.engram_attn_workspace_bytes(self._h, ctypes.byref(n)), "engram_attn_workspace_bytes")
+        self.workspace_bytes = n.value
+
+    def new_workspace(self, device="cuda") -> torch.Tensor:
+        """A workspace for attention calls; calls that may run at the same time need one each."""
+        return torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
+
+    def _workspace(self, stream: int) -> torch.Tensor:
+        """The plan's own workspace of a stream (calls on one stream run one after another)."""
+        ws = self._workspaces.get(stream)
+        if ws is None:
+            ws = self._workspaces[stream] = self.new_workspace()
+        return ws
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) and self._h.value:
+            self._lib.engram_attn_plan_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def get_error(self) -> Tuple[int, int]:
+        """(status, error bits) after synchronising the current stream; clears the bits."""
+        flags = ctypes.c_uint32()
+        st = self._lib.engram_attn_get_error(self._h, _stream(), ctypes.byref(flags))
+        return st, flags.value
+
+    def rope_table(self, length: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+        """float32 [length, rotary_dim]: cosines, then sines, of position / theta^(2i/rotary_dim)."""
+        r = self.rotary_dim
+        inv = float(theta) ** (-torch.arange(0, r, 2, dtype=torch.float64, device=device) / r)
+        angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * inv
+        return torch.cat((angle.cos(), angle.sin()), 1).float().contiguous()
+
+    def _rope(self, rope: Optional[torch.Tensor]) -> Tuple[int, int]:
+        if rope is None:
+            return 0, 0
+        if rope.dim() != 2 or rope.shape[1] != self.rotary_dim:
+            raise ValueError(f"rope: shape {tuple(rope.shape)}, expected (length, {self.rotary_dim})")
+        return _dev(rope, "rope", torch.float32), rope.shape[0]
+
+    def qk_norm_rope(self, q: torch.Tensor, k: Optional[torch.Tensor] = None,
+                     positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None, *,
+                     g_q: Optional[torch.Tensor] = None, g_k: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None
+                     ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+        """Per-head norm (where a weight is given) and rotation of q [T, heads, D] and k
+        [T, heads_kv, D] in one launch (engram_qk_norm_rope): dense outputs (q, k)."""
+        D, dt = self.head_dim, self.torch_dtype
+        T = q.shape[0]
+        vq = _view(q, "q", dt, self.heads, D)
+        if q_out is None:
+            q_out = torch.empty(T, self.heads, D, dtype=dt, device=q.device)
+        vk, k_ptr = None, 0
+        if k is not None:
+            vk = ctypes.byref(_view(k, "k", dt, self.heads_kv, D, T))
+            if k_out is None:
+                k_out = torch.empty(T, self.heads_kv, D, dtype=dt, device=q.device)
+            k_ptr = _dev(k_out, "k_out", dt, (T, self.heads_kv, D))
+        rope_ptr, rope_len = self._rope(rope)
+        pos = 0 if positions is None else _dev(positions, "positions", torch.int32, (T,))
+        _lib.check(self._lib.engram_qk_norm_rope(
+            self._h, ctypes.byref(vq), vk, T, pos, rope_ptr, rope_len, _norm_weight(g_q, "g_q", D),
+            _norm_weight(g_k, "g_k", D), _dev(q_out, "q_out", dt, (T, self.heads, D)), k_ptr, _stream()),
+            "engram_qk_norm_rope")
+        return q_out, k_out
+
+
+class SequenceBatch:
+    """The sequences of a step (engram_sequences_t): ``start`` int32 [B+1] rows of the packed
+    new tokens, ``length`` int32 [B] tokens in the cache once they are appended, ``table``
+    int32 [B, pages] page ids.  ``max_new``: the most new tokens of a sequence, a launch hint.
+    ``tokens``: rows of the packed arrays, where it is known (else the arrays' own)."""
+
+    def __init__(self, start: torch.Tensor, length: torch.Tensor, table: torch.Tensor, max_new: int = 0):
+        if length.dim() != 1 or table.dim() != 2:
+            raise ValueError("length: expected [B]; table: expected [B, pages]")
+        B = length.shape[0]
+        self.start, self.length, self.table, self.max_new = start, length, table, int(max_new)
+        self._s = _lib.Sequences(_dev(start, "start", torch.int32, (B + 1,)),
+                                 _dev(length, "length", torch.int32, (B,)),
+                                 _dev(table, "table", torch.int32, (B, table.shape[1])), B, table.shape[1], 0,
+                                 self.max_new)
+
+    def _struct(self, tokens: int):
+        self._s.tokens = tokens
+        return ctypes.byref(self._s)
+
+
+class PagedCache:
+    """One layer's keys and values in pages: ``k`` and ``v`` [pages, heads_kv, page, head_dim]
+    in the plan's type, owned by the caller, updated in place."""
+
+    def __init__(self, plan: AttentionPlan, k: torch.Tensor, v: torch.Tensor):
+        shape = (k.shape[0], plan.heads_kv, plan.page, plan.head_dim)
+        self.plan, self.k, self.v = plan, k, v
+        self._lib = plan._lib
+        self._h = ctypes.c_void_p()
+        _lib.check(self._lib.engram_kv_cache_create(plan._h, _dev(k, "k", plan.torch_dtype, shape),
+                                                    _dev(v, "v", plan.torch_dtype, shape), k.shape[0],
+                                                    ctypes.byref(self._h)), "engram_kv_cache_create")
+
+    @classmethod
+    def empty(cls, plan: AttentionPlan, pages: int, device="cuda") -> "PagedCache":
+        shape = (pages, plan.heads_kv, plan.page, plan.head_dim)
+        return cls(plan, torch.empty(shape, dtype=plan.torch_dtype, device=device),
+                   torch.empty(shape, dtype=plan.torch_dtype, device=device))
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) and self._h.value:
+            self._lib.engram_kv_cache_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def append(self, batch: SequenceBatch, k: torch.Tensor, v: torch.Tensor, rope: Optional[torch.Tensor] = None, *,
+               g_k: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+               g_q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+        """Append the new tokens' k (normed where g_k is given, rotated where rope is) and v
+        [tokens, heads_kv, D]; with q, also its norm and rotation in the same launch
+        (engram_kv_append).  Returns the queries, or None."""
+        p = self.plan
+        D, dt, T = p.head_dim, p.torch_dtype, k.shape[0]
+        vk, vv = _view(k, "k", dt, p.heads_kv, D), _view(v, "v", dt, p.heads_kv, D, T)
+        vq, q_ptr = None, 0
+        if q is not None:
+            vq = ctypes.byref(_view(q, "q", dt, p.heads, D, T))
+            if q_out is None:
+                q_out = torch.empty(T, p.heads, D, dtype=dt, device=q.device)
+            q_ptr = _dev(q_out, "q_out", dt, (T, p.heads, D))
+        rope_ptr, rope_len = p._rope(rope)
+        _lib.check(self._lib.engram_kv_append(
+            self._h, batch._struct(T), ctypes.byref(vk), ctypes.byref(vv), rope_ptr, rope_len,
+            _norm_weight(g_k, "g_k", D), vq, _norm_weight(g_q, "g_q", D), q_ptr, _stream()), "engram_kv_append")
+        return q_out if q is not None else None
+
+    def attend(self, batch: SequenceBatch, q: torch.Tensor, *, causal: bool = True, window: int = 0,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Attention of the queries [tokens, heads, D] over the cache (engram_paged_attention):
+        (out, lse float32 [tokens, heads]).  Without a ``workspace`` the plan keeps one per stream."""
+        p = self.plan
+        D, dt, T = p.head_dim, p.torch_dtype, q.shape[0]
+        vq = _view(q, "q", dt, p.heads, D)
+        if out is None:
+            out = torch.empty(T, p.heads, D, dtype=dt, device=q.device)
+        if lse is None:
+            lse = torch.empty(T, p.heads, dtype=torch.float32, device=q.device)
+        s = _stream()
+        ws = p._workspace(s.value or 0) if workspace is None else workspace
+        _lib.check(self._lib.engram_paged_attention(
+            self._h, batch._struct(T), ctypes.byref(vq), int(causal), int(window),
+            _dev(out, "out", dt, (T, p.heads, D)), _dev(lse, "lse", torch.float32, (T, p.heads)),
+            _dev(ws, "workspace"), ws.numel(), s), "engram_paged_attention")
+        return out, lse
+
+
+def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, u: torch.Tensor, *,
+                  draft_probs: Optional[torch.Tensor] = None, n_drafts: Optional[torch.Tensor] = None,
+                  tokens: Optional[torch.Tensor] = None, accepted: Optional[torch.Tensor] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Check drafted tokens int32 [B, S] against the target's probabilities [B, S+1, V] with the
+    random numbers u [B, S+1] (engram_verify_drafts).  ``draft_probs`` [B, S, V], or None where
+    each draft is certain; ``n_drafts`` int32 [B], or None for S each.  Returns (tokens int32
+    [B, S+1], accepted int32 [B])."""
+    if target.dim() != 3 or target.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("target: expected float32 or bfloat16 [B, S+1, V]")
+    B, S, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    if tokens is None:
+        tokens = torch.empty(B, S + 1, dtype=torch.int32, device=target.device)
+    if accepted is None:
+        accepted = torch.empty(B, dtype=torch.int32, device=target.device)
+    _lib.check(_lib._lib().engram_verify_drafts(
+        _dev(target, "target"), 0 if draft_probs is None else _dev(draft_probs, "draft_probs", target.dtype, (B, S, V)),
+        _lib.F32 if target.dtype == torch.float32 else _lib.BF16, _dev(drafts, "drafts", torch.int32, (B, S)),
+        0 if n_drafts is None else _dev(n_drafts, "n_drafts", torch.int32, (B,)),
+        _dev(u, "u", torch.float32, (B, S + 1)), B, S, V, _dev(tokens, "tokens", torch.int32, (B, S + 1)),
+        _dev(accepted, "accepted", torch.int32, (B,)), _stream()), "engram_verify_drafts")
+    return tokens, accepted

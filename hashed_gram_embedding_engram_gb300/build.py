@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libengram_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]
-SOURCES = ["api.cu", "hash.cu", "gather.cu", "gemm.cu", "gemm_pair.cu", "fusion.cu", "tma.cu", "noalloc.cu", "cache.cu", "stage_b.cu", "decode.cu", "quant.cu", "smsplit.cu"]
+SOURCES = ["api.cu", "hash.cu", "gather.cu", "gemm.cu", "gemm_pair.cu", "fusion.cu", "tma.cu", "noalloc.cu", "cache.cu", "stage_b.cu", "decode.cu", "quant.cu", "smsplit.cu",
+           "attention.cu", "rope.cu", "attn_simt.cu", "verify.cu"]
 
 
 def nvcc() -> str:
@@ -40,7 +41,7 @@ def _newer(target: str, deps) -> bool:
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(ROOT, "include", "engram.h"))
+    headers += [os.path.join(ROOT, "include", f) for f in ("engram.h", "engram_attention.h")]
     nv = nvcc()
 
     def compile_one(src: str) -> str:

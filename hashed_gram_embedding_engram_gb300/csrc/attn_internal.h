@@ -1,0 +1,98 @@
+// Internal declarations of the attention sub-block: the plan and the cache
+// handles, the kernels' arguments and the launchers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/engram_attention.h"
+#include "engram_internal.h"
+
+struct engram_attn_plan {
+  engram_attn_config_t cfg;
+  int group;                  // heads / heads_kv
+  int page_shift;             // log2(page)
+  float scale;
+  int device;
+  int num_sms;
+  uint32_t* err;              // device error word
+};
+
+struct engram_kv_cache {
+  const engram_attn_plan* plan;
+  void* k;
+  void* v;
+  int64_t pages;
+};
+
+namespace engram {
+
+// A [tokens, heads, head_dim] view; strides in elements.
+struct HeadsView {
+  const void* ptr;
+  int64_t ts;
+  int64_t hs;
+};
+
+// The sequences of a call, as the kernels read them.
+struct SeqArgs {
+  const int32_t* start;
+  const int32_t* length;
+  const int32_t* table;
+  int B;
+  int table_pages;
+  int page_shift;
+  int tokens;
+};
+
+struct RopeArgs {
+  HeadsView q, k, v;          // ptr null: not there (v: append only)
+  void* q_out;                // dense [tokens, heads, D]
+  void* k_out;                // dense [tokens, heads_kv, D], or null when appending
+  void* k_pages;              // cache, or null
+  void* v_pages;
+  int64_t pages;
+  const int32_t* positions;   // null when appending
+  const float* rope;          // [rope_len, rotary] or null
+  const float* g_q;
+  const float* g_k;
+  SeqArgs seq;
+  int tokens;
+  int heads, heads_kv, D, rotary, rope_len;
+  float eps;
+  uint32_t* err;
+};
+
+struct AttnArgs {
+  HeadsView q;
+  const void* k;              // [pages, heads_kv, page, D]
+  const void* v;
+  int64_t pages;
+  void* out;                  // dense [tokens, heads, D]
+  float* lse;                 // [tokens, heads] or null
+  SeqArgs seq;
+  int heads, heads_kv, group, D;
+  int causal, window;
+  float scale_log2;           // scale * log2(e): scores in powers of two
+  uint32_t* counters;         // kAttnCounters words, zero between calls
+  float* parts;               // partial tiles (attn_sched.cuh)
+  uint32_t* err;
+};
+
+constexpr int kAttnCounters = 4096;      // at least the blocks of any attention grid
+constexpr int kAttnPartRows = 256;       // rows of partial tiles per SM, twice (workspace bound)
+
+inline size_t attn_workspace_bytes(const engram_attn_plan* p) {
+  return kAttnCounters * 4 +
+         static_cast<size_t>(p->num_sms) * 2 * kAttnPartRows * (static_cast<size_t>(p->cfg.head_dim) + 2) * 4;
+}
+
+cudaError_t launch_rope(const engram_attn_plan* p, const RopeArgs& a, cudaStream_t s);
+// Attention on the CUDA cores: every type and head size.
+cudaError_t launch_attention_simt(const engram_attn_plan* p, const AttnArgs& a, int max_new, cudaStream_t s);
+cudaError_t launch_verify(const void* target, const void* draft, bool is_f32, const int32_t* drafts,
+                          const int32_t* n_drafts, const float* u, int B, int S, int V, int32_t* tokens,
+                          int32_t* accepted, cudaStream_t s);
+
+}  // namespace engram
