@@ -133,6 +133,19 @@ engram_status_t engram_kv_cache_create(const engram_attn_plan_t* plan, void* k, 
   c->k = k;
   c->v = v;
   c->pages = pages;
+  const int D = plan->cfg.head_dim;
+  c->maps = plan->cfg.dtype == ENGRAM_BF16 && (D == 64 || D == 128);
+  if (c->maps) {
+    const uint64_t rows = static_cast<uint64_t>(pages) * plan->cfg.heads_kv << plan->page_shift;
+    auto map = [&](CUtensorMap* m, const void* base, int most) {
+      const uint32_t box = static_cast<uint32_t>(plan->cfg.page < most ? plan->cfg.page : most);
+      return engram::make_tensor_map_2d(m, base, false, D, rows, static_cast<uint64_t>(D) * 2, 64, box, true);
+    };
+    if (!map(&c->k64, k, 64) || !map(&c->v64, v, 64)) {
+      delete c;
+      return ENGRAM_ERR_CUDA;
+    }
+  }
   *out = c;
   return ENGRAM_OK;
 }
@@ -242,6 +255,9 @@ engram_status_t engram_paged_attention(const engram_kv_cache_t* cache, const eng
   a.err = plan->err;
   int64_t max_new = seq->max_new > 0 ? seq->max_new : seq->tokens;
   if (max_new > seq->tokens) max_new = seq->tokens;
+  const int64_t rows = max_new * plan->group;
+  if (engram::attention_rows_applies(cache, rows))
+    return cuda_status(engram::launch_attention_rows(cache, a, rows, (cudaStream_t)stream));
   return cuda_status(engram::launch_attention_simt(plan, a, static_cast<int>(max_new), (cudaStream_t)stream));
 }
 

@@ -568,3 +568,22 @@ def test_refusals_of_the_front_end():
         verify_drafts(p, d.long(), u)
     with pytest.raises(EngramError, match="INVALID_ARG"):
         verify_drafts(p[:, :1].contiguous(), d[:, :0].contiguous(), u[:, :1].contiguous())
+
+
+@pytest.mark.parametrize("hint", [1, 5, 40, 0, 10 ** 6])
+def test_max_new_is_a_hint_only(hint):
+    """Whatever launch the hint picks, every row is computed."""
+    c = Case(seed=14, new=(3, 200, 1), length=(40, 333, 1000), heads=8, heads_kv=2, D=128, page=32)
+    c.batch = SequenceBatch(c.batch.start, c.batch.length, c.batch.table, max_new=hint)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("hint", [1, 2, 200])
+def test_pages_outside_a_window_are_not_looked_at(hint):
+    """Table entries of pages that no query sees may hold anything (an engine frees them)."""
+    c = Case(seed=15, new=(2, 1), length=(600, 131), heads=8, heads_kv=2, D=128, page=16, window=100)
+    c.batch = SequenceBatch(c.batch.start, c.batch.length, c.batch.table, max_new=hint)
+    table = c.batch.table
+    table[0, :(600 - 2 - 100) // 16] = 2 ** 30
+    table[1, :(131 - 1 - 99) // 16] = -3
+    c.check(*c.run())
