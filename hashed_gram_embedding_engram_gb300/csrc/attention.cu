@@ -141,7 +141,7 @@ engram_status_t engram_kv_cache_create(const engram_attn_plan_t* plan, void* k, 
       const uint32_t box = static_cast<uint32_t>(plan->cfg.page < most ? plan->cfg.page : most);
       return engram::make_tensor_map_2d(m, base, false, D, rows, static_cast<uint64_t>(D) * 2, 64, box, true);
     };
-    if (!map(&c->k64, k, 64) || !map(&c->v64, v, 64)) {
+    if (!map(&c->k64, k, 64) || !map(&c->v64, v, 64) || !map(&c->k128, k, 128) || !map(&c->v128, v, 128)) {
       delete c;
       return ENGRAM_ERR_CUDA;
     }
@@ -258,6 +258,7 @@ engram_status_t engram_paged_attention(const engram_kv_cache_t* cache, const eng
   const int64_t rows = max_new * plan->group;
   if (engram::attention_rows_applies(cache, rows))
     return cuda_status(engram::launch_attention_rows(cache, a, rows, (cudaStream_t)stream));
+  if (cache->maps) return cuda_status(engram::launch_attention_tiles(cache, a, (cudaStream_t)stream));
   return cuda_status(engram::launch_attention_simt(plan, a, static_cast<int>(max_new), (cudaStream_t)stream));
 }
 

@@ -26,6 +26,7 @@ struct engram_kv_cache {
   int64_t pages;
   bool maps;                  // bf16 with D 64 or 128: tensor maps for the tensor-core kernels,
   CUtensorMap k64, v64;       // boxes of min(page, 64) rows x 64 columns
+  CUtensorMap k128, v128;     // boxes of min(page, 128) rows x 64 columns
 };
 
 namespace engram {
@@ -97,6 +98,8 @@ cudaError_t launch_attention_simt(const engram_attn_plan* p, const AttnArgs& a, 
 // the tensor cores, where the cache has tensor maps; more rows make more tiles.
 bool attention_rows_applies(const engram_kv_cache* c, int64_t rows);
 cudaError_t launch_attention_rows(const engram_kv_cache* c, const AttnArgs& a, int64_t rows, cudaStream_t s);
+// Attention of longer chunks on the tensor cores, 256 rows a tile.
+cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const void* target, const void* draft, bool is_f32, const int32_t* drafts,
                           const int32_t* n_drafts, const float* u, int B, int S, int V, int32_t* tokens,
                           int32_t* accepted, cudaStream_t s);

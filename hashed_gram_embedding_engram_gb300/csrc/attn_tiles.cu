@@ -1,0 +1,425 @@
+// Attention of chunks of new tokens over the paged cache on the fifth-
+// generation tensor cores: bf16, head size 64 or 128.
+//
+//   S = Q K^T,  P = 2^(scale log2(e) S - m),  l = sum P,  O = P V
+//
+// A block has 256 rows (two tiles of 128) and takes 128 keys a step:
+//   warp 8      TMA: keys and values of a step into rings of their own, one
+//               box a page and 64 columns, 128-byte swizzle.
+//   warp 9      one elected lane issues tcgen05.mma: S = Q K^T (both operands
+//               from shared memory) and O += P V (P from TMEM, V as it lies in
+//               the cache, the head dimension contiguous: an MN-major operand).
+//   warps 0-3   softmax of tile 0, 4-7 of tile 1: one thread a row reads its
+//               128 scores from TMEM, writes its weights (bf16) over them.
+// While one tile's scores are in the softmax, the tensor core works on the
+// other's, so the two alternate: PV(0), S(0), PV(1), S(1), ...  TMEM is full:
+// two S/P tiles of 128 columns and two accumulators of D.
+// The accumulator is brought to a new maximum only when that exceeds the one
+// in use by 2^8 (weights then are at most 2^8, far inside bf16 and float), so
+// the round trip of O through the registers is rare.
+// Slots past a length hold anything: their scores are replaced by -inf, and
+// the issuing warp zeroes their values in shared memory (0 * NaN is NaN).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "attn_sched.cuh"
+#include "attn_tma.cuh"
+#include "ptx.cuh"
+
+namespace engram {
+namespace {
+
+using namespace at;
+
+constexpr int kRT = 256;
+constexpr int kKT = 128;
+constexpr int kNT = 320;
+constexpr float kSlack = 8.f;      // powers of two a row's maximum may grow before O is rescaled
+
+template <int D>
+struct Cfg {
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kTile = kKT * D * 2;                // bytes of 128 rows of K, V or Q
+  static constexpr int kSmem = 1024 + (2 + 2 * kStages) * kTile;
+};
+
+struct Shared {
+  uint64_t full_k[4], empty_k[4], full_v[4], empty_v[4];
+  uint64_t q_full[2];   // queries of a tile are in shared memory
+  uint64_t s_full[2];   // scores of a step are in TMEM
+  uint64_t p_full[2];   // weights of a step are in TMEM, O is at the step's maximum
+  uint64_t o_full[2];   // the step's PV is done
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  int flag;
+  Range range;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The 32 rows of a warp of tile t, from global memory to the swizzled tile.
+template <int D>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Walk& w, uint8_t* tile, int t, int warp4,
+                                             int lane) {
+  constexpr int kLanes = D / 8;             // 16-byte pieces of a row
+  const int n_rows = w.q.n * a.group;
+  const int piece = lane % kLanes;
+#pragma unroll 8
+  for (int i = 0; i < kLanes; ++i) {
+    const int row = warp4 * 32 + i * (32 / kLanes) + lane / kLanes;
+    const int rr = w.r * kRT + t * 128 + row;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (rr < n_rows)
+      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.ptr) +
+                                               (w.q.row0 + rr / a.group) * a.q.ts +
+                                               (w.h * a.group + rr % a.group) * a.q.hs + piece * 8));
+    *reinterpret_cast<uint4*>(tile + (piece >> 3) * (128 * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = x;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kNT, 1)
+    attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v) {
+  constexpr int kStages = Cfg<D>::kStages;
+  constexpr int kTile = Cfg<D>::kTile;
+  constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, kKT);
+  constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(128, D) | (1u << 16);   // B (the values) MN-major
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = smem;
+  uint8_t* sk = smem + 2 * kTile;
+  uint8_t* sv = sk + kStages * kTile;
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&sh.full_k[s], 1);
+      ptx::mbar_init(&sh.full_v[s], 1);
+      ptx::mbar_init(&sh.empty_k[s], 1);
+      ptx::mbar_init(&sh.empty_v[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(&sh.q_full[t], 4);
+      ptx::mbar_init(&sh.s_full[t], 1);
+      ptx::mbar_init(&sh.p_full[t], 4);
+      ptx::mbar_init(&sh.o_full[t], 1);
+    }
+    ptx::mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&map_k);
+    ptx::tma_prefetch_desc(&map_v);
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(&sh.tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  ptx::tc_fence_before();
+  find_range<kNT, kRT, kKT>(a, &sh.range);   // ends with a block barrier
+  ptx::tc_fence_after();
+  const Range range = sh.range;
+  const uint32_t tmem = sh.tmem;
+
+  if (range.u0 < range.u1) {
+    Walk w = walk_begin<kRT, kKT>(a, range);
+    int64_t u = range.u0, tile_u0 = range.tile_u0;
+    if (warp == 8) {
+      // -------------------------------------------------------------- TMA
+      int stage = 0, filled = 0;
+      uint32_t phase = 0;
+      while (true) {
+        const int ua = static_cast<int>(u - tile_u0);
+        const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+        for (int un = ua; un < ub && w.k.hi > 0; ++un) {
+          const int j0 = (w.k.lo / kKT + un) * kKT;
+          const int32_t row = page_row<kKT>(a, w, j0, lane);
+          wait_bounded(&sh.empty_k[stage], phase ^ 1, &sh.abort, a.err);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full_k[stage], kTile);
+          __syncwarp();
+          load_boxes<kKT, D>(a, &map_k, sk + stage * kTile, &sh.full_k[stage], row, j0, lane);
+          wait_bounded(&sh.empty_v[stage], phase ^ 1, &sh.abort, a.err);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full_v[stage], kTile);
+          __syncwarp();
+          load_boxes<kKT, D>(a, &map_v, sv + stage * kTile, &sh.full_v[stage], row, j0, lane);
+          if (filled < kStages) ++filled;
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+        u = tile_u0 + ub;
+        if (u >= range.u1) break;
+        tile_u0 = u;
+        walk_next<kRT, kKT>(a, w);
+      }
+      if (*reinterpret_cast<volatile int*>(&sh.abort)) {     // copies in flight land before the block ends
+        for (int i = 0; i < filled; ++i) {
+          stage = stage == 0 ? kStages - 1 : stage - 1;
+          if (stage == kStages - 1) phase ^= 1;
+          drain_bounded(&sh.full_k[stage], phase);
+          drain_bounded(&sh.full_v[stage], phase);
+        }
+      }
+    } else if (warp == 9) {
+      // -------------------------------------------------------------- MMA
+      int ks = 0, vs = 0;                       // ring stages
+      uint32_t kp = 0, vp = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
+      auto scores = [&](int t) {                // S(t) = Q(t) K^T of stage ks
+        if (lane == 0) {
+          const uint32_t qa = ptx::smem_u32(sq + t * kTile), ka = ptx::smem_u32(sk + ks * kTile);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
+            ptx::mma_bf16(tmem + t * 128, ptx::sdesc_kmajor_sw128(qa + off), ptx::sdesc_kmajor_sw128(ka + off), kIdescS,
+                          k > 0);
+          }
+          ptx::mma_commit(&sh.s_full[t]);
+        }
+        __syncwarp();
+      };
+      auto next_k = [&] {
+        if (lane == 0) ptx::mma_commit(&sh.empty_k[ks]);
+        __syncwarp();
+        if (++ks == kStages) ks = 0, kp ^= 1;
+      };
+      while (true) {
+        const int ua = static_cast<int>(u - tile_u0);
+        const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+        if (w.k.hi > 0) {
+          const int nt = w.q.n * a.group - w.r * kRT > 128 ? 2 : 1;
+          for (int t = 0; t < nt; ++t) {
+            wait_bounded(&sh.q_full[t], qp[t], &sh.abort, a.err);
+            qp[t] ^= 1;
+            if (t == 0) wait_bounded(&sh.full_k[ks], kp, &sh.abort, a.err);
+            ptx::tc_fence_after();
+            scores(t);
+          }
+          next_k();
+          for (int un = ua; un < ub; ++un) {
+            for (int t = 0; t < nt; ++t) {
+              if (t == 0) {
+                wait_bounded(&sh.full_v[vs], vp, &sh.abort, a.err);
+                const int j0 = (w.k.lo / kKT + un) * kKT;
+                if (j0 < w.k.lo || j0 + kKT > w.k.hi) {
+                  zero_rows<kKT, D>(sv + vs * kTile, w.k.lo - j0, w.k.hi - j0, lane, 32);
+                  ptx::fence_proxy_async_smem();
+                  __syncwarp();
+                }
+              }
+              wait_bounded(&sh.p_full[t], pp[t], &sh.abort, a.err);
+              pp[t] ^= 1;
+              ptx::tc_fence_after();
+              if (lane == 0) {
+                const uint32_t va = ptx::smem_u32(sv + vs * kTile);
+#pragma unroll
+                for (int k = 0; k < kKT / 16; ++k)
+                  ptx::mma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
+                                   ptx::sdesc_mnmajor_sw128(va + k * 2048, 128 * 128), kIdescO, un > ua || k > 0);
+                ptx::mma_commit(&sh.o_full[t]);
+              }
+              __syncwarp();
+              if (un + 1 < ub) {
+                if (t == 0) {
+                  wait_bounded(&sh.full_k[ks], kp, &sh.abort, a.err);
+                  ptx::tc_fence_after();
+                }
+                scores(t);
+              }
+            }
+            if (lane == 0) ptx::mma_commit(&sh.empty_v[vs]);
+            __syncwarp();
+            if (++vs == kStages) vs = 0, vp ^= 1;
+            if (un + 1 < ub) next_k();
+          }
+        }
+        u = tile_u0 + ub;
+        if (u >= range.u1) break;
+        tile_u0 = u;
+        walk_next<kRT, kKT>(a, w);
+      }
+      if (lane == 0) ptx::mma_commit(&sh.drain);
+      __syncwarp();
+      drain_bounded(&sh.drain, 0);
+    } else {
+      // -------------------------------------------------------------- softmax
+      const int t = warp >> 2, warp4 = warp & 3;
+      const uint32_t ts = tmem + t * 128 + (static_cast<uint32_t>(warp4 * 32) << 16);
+      const uint32_t to = tmem + 256 + t * 128 + (static_cast<uint32_t>(warp4 * 32) << 16);
+      uint32_t sp = 0, op = 0;
+      while (true) {
+        const int ua = static_cast<int>(u - tile_u0);
+        const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+        const int n_rows = w.q.n * a.group;
+        const int row = t * 128 + warp4 * 32 + lane, rr = w.r * kRT + row;
+        const bool live = rr < n_rows;
+        const bool work = w.k.hi > 0 && n_rows - w.r * kRT > t * 128;   // of the tile: same in all its warps
+        const int p = w.q.len - w.q.n + rr / a.group;
+        const int hi = !live || p < 0 ? 0 : (a.causal ? p + 1 : w.q.len);
+        const int lo = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
+        float m = -INFINITY, l = 0.f;
+        if (work) {
+          load_queries<D>(a, w, sq + t * kTile, t, warp4, lane);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.q_full[t]);
+          for (int un = ua; un < ub; ++un) {
+            const int j0 = (w.k.lo / kKT + un) * kKT;
+            wait_bounded(&sh.s_full[t], sp, &sh.abort, a.err);
+            sp ^= 1;
+            ptx::tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(ts + c * 32, s[c]);
+            ptx::tmem_ld_wait();
+            if (__any_sync(~0u, j0 < lo || j0 + kKT > hi)) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const int j = j0 + c * 32 + i;
+                  if (j < lo || j >= hi) s[c][i] = 0xFF800000u;      // -inf
+                }
+            }
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(s[c][i]));
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
+            // m stays unless it is more than kSlack behind (or unset)
+            float f = 1.f;
+            if (top > m + kSlack || (m == -INFINITY && top > m)) {
+              f = ex2(m - top);
+              m = top;
+            }
+            if (un > ua && __any_sync(~0u, f != 1.f)) {
+              l *= f;
+              wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);   // the step before has been added
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                ptx::tmem_ld_32x32b_x32(to + c, o);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                ptx::tmem_st_32x32b_x32(to + c, o);
+              }
+            }
+            op ^= 1;
+            const float base = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float x0 = __uint_as_float(s[h * 2 + i / 16][(i % 16) * 2]);
+                const float x1 = __uint_as_float(s[h * 2 + i / 16][(i % 16) * 2 + 1]);
+                const float p0 = ex2(fmaf(x0, a.scale_log2, -base)), p1 = ex2(fmaf(x1, a.scale_log2, -base));
+                sum[(i & 1) * 2] += p0;
+                sum[(i & 1) * 2 + 1] += p1;
+                const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+                pk[i] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+              ptx::tmem_st_32x32b_x32(ts + h * 32, pk);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
+          }
+          wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);
+          ptx::tc_fence_after();
+        }
+        const bool whole = ua == 0 && ub == w.units;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
+        float* part = part_slot<kRT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          if (work) {
+            ptx::tmem_ld_32x32b_x32(to + c, o);
+            ptx::tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+          if (live && whole) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * D + c;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[i + 2 * k]) * inv,
+                                                               __uint_as_float(o[i + 2 * k + 1]) * inv);
+                x[k] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+              *reinterpret_cast<uint4*>(out + i) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(part + row * D + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        __syncwarp();
+        ptx::tc_fence_before();       // O is read: the next tile's first weights let it be overwritten
+        if (live) {
+          if (whole) {
+            if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          } else {
+            part[kRT * D + row] = m;
+            part[kRT * D + kRT + row] = l;
+          }
+        }
+        if (!whole) {
+          const int cf = block_of(range, tile_u0), cl = block_of(range, tile_u0 + w.units - 1);
+          if (arrive_last<256>(a, cf, cl, &sh.flag, tid, 1)) join_tile<__nv_bfloat16, 256, kRT>(a, w, cf, cl, tid);
+        }
+        u = tile_u0 + ub;
+        if (u >= range.u1) break;
+        tile_u0 = u;
+        walk_next<kRT, kKT>(a, w);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
+  constexpr int smem = Cfg<D>::kSmem;
+  static bool attr_set = false;   // per template instance; idempotent if raced
+  if (!attr_set) {
+    cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_set = true;
+  }
+  return launch_pdl(attn_tiles_kernel<D>, dim3(p->num_sms), dim3(kNT), smem, s, a, c->k128, c->v128);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
+  return a.D == 64 ? run<64>(c->plan, c, a, s) : run<128>(c->plan, c, a, s);
+}
+
+}  // namespace engram
