@@ -53,16 +53,6 @@ class AttnConfig(ctypes.Structure):
                 ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
-class HeadsView(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
-class Sequences(ctypes.Structure):
-    _fields_ = [("start", ctypes.c_void_p), ("length", ctypes.c_void_p), ("table", ctypes.c_void_p),
-                ("B", ctypes.c_int), ("table_pages", ctypes.c_int), ("tokens", ctypes.c_int64),
-                ("max_new", ctypes.c_int)]
-
-
 class EngramError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -135,7 +125,7 @@ def _lib() -> ctypes.CDLL:
         lib.engram_attn_workspace_bytes.argtypes = [vp, ctypes.POINTER(sz)]
         lib.engram_kv_cache_create.argtypes = [vp, vp, vp, i64, ctypes.POINTER(vp)]
         lib.engram_kv_cache_destroy.argtypes = [vp]
-        # pointers to views and sequences as plain addresses (byref), which the front end keeps filled
+        # views and sequences as bytes that the front end packs
         lib.engram_qk_norm_rope.argtypes = [vp, vp, vp, i64, vp, vp, i32, vp, vp, vp, vp, vp]
         lib.engram_kv_append.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp]
         lib.engram_paged_attention.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]

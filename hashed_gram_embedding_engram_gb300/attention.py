@@ -7,6 +7,7 @@ allocated unless given.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -16,15 +17,34 @@ from .engram import _ACT_DTYPES, _dev, _stream
 
 _ROPE_STYLES = {"halves": 0, "adjacent": 1}
 
+# engram_heads_view_t and engram_sequences_t as bytes of the call's own: a step's calls take a few
+# microseconds on the device, so the front end must not take longer (a ctypes structure costs three times this)
+_pack_view = struct.Struct("@Pqq").pack
+_pack_sequences = struct.Struct("@PPPiiqi4x").pack
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(device: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
+    """_dev with its checks in one test where all hold."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, dtype, shape)
+
 
 def _view(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, head_dim: int,
-          tokens: Optional[int] = None) -> _lib.HeadsView:
+          tokens: Optional[int] = None) -> bytes:
     """A [tokens, heads, head_dim] device tensor whose last dimension is dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or (tokens is not None and shape[0] != tokens):
@@ -34,11 +54,11 @@ def _view(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, head_dim: 
     if s2 != 1 and shape[0]:
         raise ValueError(f"{name}: the last dimension must be dense")
     # the stride of a dimension of one element is never used and may be anything
-    return _lib.HeadsView(t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if heads > 1 else 0)
+    return _pack_view(t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if heads > 1 else 0)
 
 
 def _norm_weight(g: Optional[torch.Tensor], name: str, head_dim: int) -> int:
-    return 0 if g is None else _dev(g, name, torch.float32, (head_dim,))
+    return 0 if g is None else _ptr(g, name, torch.float32, (head_dim,))
 
 
 class AttentionPlan:
@@ -66,7 +86,7 @@ class AttentionPlan:
         self._lib = _lib._lib()
         self._h = ctypes.c_void_p()
         self._workspaces = {}
-        torch.cuda.current_device()   # make sure a context exists on the current device
+        self.device = torch.cuda.current_device()   # also makes sure a context exists
         _lib.check(self._lib.engram_attn_plan_create(ctypes.byref(cfg), ctypes.byref(self._h)),
                    "engram_attn_plan_create")
         n = ctypes.c_size_t()
@@ -111,9 +131,9 @@ class AttentionPlan:
     def _rope(self, rope: Optional[torch.Tensor]) -> Tuple[int, int]:
         if rope is None:
             return 0, 0
-        if rope.dim() != 2 or rope.shape[1] != self.rotary_dim:
-            raise ValueError(f"rope: shape {tuple(rope.shape)}, expected (length, {self.rotary_dim})")
-        return _dev(rope, "rope", torch.float32), rope.shape[0]
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2 or rope.shape[1] != self.rotary_dim:
+            raise ValueError(f"rope: expected a tensor of shape (length, {self.rotary_dim})")
+        return _ptr(rope, "rope", torch.float32, rope.shape), rope.shape[0]
 
     def qk_norm_rope(self, q: torch.Tensor, k: Optional[torch.Tensor] = None,
                      positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None, *,
@@ -129,16 +149,15 @@ class AttentionPlan:
             q_out = torch.empty(T, self.heads, D, dtype=dt, device=q.device)
         vk, k_ptr = None, 0
         if k is not None:
-            vk = ctypes.byref(_view(k, "k", dt, self.heads_kv, D, T))
+            vk = _view(k, "k", dt, self.heads_kv, D, T)
             if k_out is None:
                 k_out = torch.empty(T, self.heads_kv, D, dtype=dt, device=q.device)
-            k_ptr = _dev(k_out, "k_out", dt, (T, self.heads_kv, D))
+            k_ptr = _ptr(k_out, "k_out", dt, (T, self.heads_kv, D))
         rope_ptr, rope_len = self._rope(rope)
-        pos = 0 if positions is None else _dev(positions, "positions", torch.int32, (T,))
+        pos = 0 if positions is None else _ptr(positions, "positions", torch.int32, (T,))
         _lib.check(self._lib.engram_qk_norm_rope(
-            self._h, ctypes.byref(vq), vk, T, pos, rope_ptr, rope_len, _norm_weight(g_q, "g_q", D),
-            _norm_weight(g_k, "g_k", D), _dev(q_out, "q_out", dt, (T, self.heads, D)), k_ptr, _stream()),
-            "engram_qk_norm_rope")
+            self._h, vq, vk, T, pos, rope_ptr, rope_len, _norm_weight(g_q, "g_q", D), _norm_weight(g_k, "g_k", D),
+            _ptr(q_out, "q_out", dt, (T, self.heads, D)), k_ptr, _current_stream(self.device)), "engram_qk_norm_rope")
         return q_out, k_out
 
 
@@ -153,14 +172,11 @@ class SequenceBatch:
             raise ValueError("length: expected [B]; table: expected [B, pages]")
         B = length.shape[0]
         self.start, self.length, self.table, self.max_new = start, length, table, int(max_new)
-        self._s = _lib.Sequences(_dev(start, "start", torch.int32, (B + 1,)),
-                                 _dev(length, "length", torch.int32, (B,)),
-                                 _dev(table, "table", torch.int32, (B, table.shape[1])), B, table.shape[1], 0,
-                                 self.max_new)
+        self._fixed = (_dev(start, "start", torch.int32, (B + 1,)), _dev(length, "length", torch.int32, (B,)),
+                       _dev(table, "table", torch.int32, (B, table.shape[1])), B, table.shape[1])
 
-    def _struct(self, tokens: int):
-        self._s.tokens = tokens
-        return ctypes.byref(self._s)
+    def _struct(self, tokens: int) -> bytes:
+        return _pack_sequences(*self._fixed, tokens, self.max_new)
 
 
 class PagedCache:
@@ -204,14 +220,14 @@ class PagedCache:
         vk, vv = _view(k, "k", dt, p.heads_kv, D), _view(v, "v", dt, p.heads_kv, D, T)
         vq, q_ptr = None, 0
         if q is not None:
-            vq = ctypes.byref(_view(q, "q", dt, p.heads, D, T))
+            vq = _view(q, "q", dt, p.heads, D, T)
             if q_out is None:
                 q_out = torch.empty(T, p.heads, D, dtype=dt, device=q.device)
-            q_ptr = _dev(q_out, "q_out", dt, (T, p.heads, D))
+            q_ptr = _ptr(q_out, "q_out", dt, (T, p.heads, D))
         rope_ptr, rope_len = p._rope(rope)
         _lib.check(self._lib.engram_kv_append(
-            self._h, batch._struct(T), ctypes.byref(vk), ctypes.byref(vv), rope_ptr, rope_len,
-            _norm_weight(g_k, "g_k", D), vq, _norm_weight(g_q, "g_q", D), q_ptr, _stream()), "engram_kv_append")
+            self._h, batch._struct(T), vk, vv, rope_ptr, rope_len, _norm_weight(g_k, "g_k", D), vq,
+            _norm_weight(g_q, "g_q", D), q_ptr, _current_stream(p.device)), "engram_kv_append")
         return q_out if q is not None else None
 
     def attend(self, batch: SequenceBatch, q: torch.Tensor, *, causal: bool = True, window: int = 0,
@@ -226,12 +242,14 @@ class PagedCache:
             out = torch.empty(T, p.heads, D, dtype=dt, device=q.device)
         if lse is None:
             lse = torch.empty(T, p.heads, dtype=torch.float32, device=q.device)
-        s = _stream()
-        ws = p._workspace(s.value or 0) if workspace is None else workspace
+        s = _current_stream(p.device)
+        if workspace is None:
+            ws_ptr, ws_bytes = p._workspace(s).data_ptr(), p.workspace_bytes
+        else:
+            ws_ptr, ws_bytes = _dev(workspace, "workspace", torch.uint8), workspace.numel()
         _lib.check(self._lib.engram_paged_attention(
-            self._h, batch._struct(T), ctypes.byref(vq), int(causal), int(window),
-            _dev(out, "out", dt, (T, p.heads, D)), _dev(lse, "lse", torch.float32, (T, p.heads)),
-            _dev(ws, "workspace"), ws.numel(), s), "engram_paged_attention")
+            self._h, batch._struct(T), vq, int(causal), int(window), _ptr(out, "out", dt, (T, p.heads, D)),
+            _ptr(lse, "lse", torch.float32, (T, p.heads)), ws_ptr, ws_bytes, s), "engram_paged_attention")
         return out, lse
 
 
@@ -243,17 +261,20 @@ def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, u: torch.Tensor, *
     random numbers u [B, S+1] (engram_verify_drafts).  ``draft_probs`` [B, S, V], or None where
     each draft is certain; ``n_drafts`` int32 [B], or None for S each.  Returns (tokens int32
     [B, S+1], accepted int32 [B])."""
-    if target.dim() != 3 or target.dtype not in (torch.float32, torch.bfloat16):
+    if not isinstance(target, torch.Tensor) or target.dtype not in (torch.float32, torch.bfloat16) or target.dim() != 3:
         raise ValueError("target: expected float32 or bfloat16 [B, S+1, V]")
-    B, S, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    B, S1, V = target.shape
+    S = S1 - 1
     if tokens is None:
-        tokens = torch.empty(B, S + 1, dtype=torch.int32, device=target.device)
+        tokens = torch.empty(B, S1, dtype=torch.int32, device=target.device)
     if accepted is None:
         accepted = torch.empty(B, dtype=torch.int32, device=target.device)
+    i32 = torch.int32
     _lib.check(_lib._lib().engram_verify_drafts(
-        _dev(target, "target"), 0 if draft_probs is None else _dev(draft_probs, "draft_probs", target.dtype, (B, S, V)),
-        _lib.F32 if target.dtype == torch.float32 else _lib.BF16, _dev(drafts, "drafts", torch.int32, (B, S)),
-        0 if n_drafts is None else _dev(n_drafts, "n_drafts", torch.int32, (B,)),
-        _dev(u, "u", torch.float32, (B, S + 1)), B, S, V, _dev(tokens, "tokens", torch.int32, (B, S + 1)),
-        _dev(accepted, "accepted", torch.int32, (B,)), _stream()), "engram_verify_drafts")
+        _ptr(target, "target", target.dtype, target.shape),
+        0 if draft_probs is None else _ptr(draft_probs, "draft_probs", target.dtype, (B, S, V)),
+        _lib.F32 if target.dtype is torch.float32 else _lib.BF16, _ptr(drafts, "drafts", i32, (B, S)),
+        0 if n_drafts is None else _ptr(n_drafts, "n_drafts", i32, (B,)), _ptr(u, "u", torch.float32, (B, S1)), B, S, V,
+        _ptr(tokens, "tokens", i32, (B, S1)), _ptr(accepted, "accepted", i32, (B,)),
+        _current_stream(target.device.index)), "engram_verify_drafts")
     return tokens, accepted

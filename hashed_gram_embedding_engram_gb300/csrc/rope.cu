@@ -20,24 +20,36 @@ namespace engram {
 namespace {
 
 constexpr int kNT = 256;
+constexpr int64_t kManyHeads = 65536;   // from here a group takes four heads of a token, below one
+
+// Eight elements as they lie in memory (one or two 16-byte words), and as floats.
+template <typename T>
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+};
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+
+__device__ __forceinline__ void to_float(const Raw<float>& r, float (&x)[8]) {
+  const uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void to_float(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(u[i] << 16);
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) { to_float(load_raw(p), x); }
 
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -69,16 +81,16 @@ __global__ void __launch_bounds__(kNT) rope_kernel(const __grid_constant__ RopeA
   const int nq = a.q.ptr ? a.heads : 0, nk = a.k.ptr ? a.heads_kv : 0, nv = kAppend ? a.heads_kv : 0;
 
   // heads of this group: queries, then keys, then values
-  float x[HB][8];
+  Raw<T> raw[HB];
 #pragma unroll
   for (int j = 0; j < HB; ++j) {
     const int hh = h0 + j;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) raw[j].w[i] = make_uint4(0, 0, 0, 0);
     if (!live || !mine || hh >= nq + nk + nv) continue;
     const HeadsView& view = hh < nq ? a.q : (hh < nq + nk ? a.k : a.v);
     const int h = hh < nq ? hh : (hh < nq + nk ? hh - nq : hh - nq - nk);
-    load8<T>(static_cast<const T*>(view.ptr) + token * view.ts + h * view.hs + lane * 8, x[j]);
+    raw[j] = load_raw(static_cast<const T*>(view.ptr) + token * view.ts + h * view.hs + lane * 8);
   }
 
   int pos = -1;
@@ -143,8 +155,8 @@ __global__ void __launch_bounds__(kNT) rope_kernel(const __grid_constant__ RopeA
       sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
     } else {
       const int at = lane * 8 < half ? lane * 8 : lane * 8 - half;
-      load8<float>(row + at, cs);
-      load8<float>(row + half + at, sn);
+      load8(row + at, cs);
+      load8(row + half + at, sn);
     }
   }
 
@@ -155,25 +167,27 @@ __global__ void __launch_bounds__(kNT) rope_kernel(const __grid_constant__ RopeA
     const float* g = is_v ? nullptr : (hh < nq ? a.g_q : a.g_k);
     const bool turned = rotated && !is_v;
     // the groups of a warp may hold different kinds of heads: all lanes take part in every shuffle
+    float x[8];
+    to_float(raw[j], x);
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[j][i], x[j][i], ss);
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
     for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
     if (g && mine) {
       const float inv = 1.f / sqrtf(ss / a.D + a.eps);
       float gw[8];
-      load8<float>(g + lane * 8, gw);
+      load8(g + lane * 8, gw);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = x[j][i] * inv * gw[i];
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * gw[i];
     }
     if (adjacent) {
       if (turned) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float lo = x[j][2 * i], hi = x[j][2 * i + 1];
-          x[j][2 * i] = lo * cs[i] - hi * sn[i];
-          x[j][2 * i + 1] = lo * sn[i] + hi * cs[i];
+          const float lo = x[2 * i], hi = x[2 * i + 1];
+          x[2 * i] = lo * cs[i] - hi * sn[i];
+          x[2 * i + 1] = lo * sn[i] + hi * cs[i];
         }
       }
     } else {
@@ -182,21 +196,21 @@ __global__ void __launch_bounds__(kNT) rope_kernel(const __grid_constant__ RopeA
       const int from = low ? lane + step : lane - step;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_sync(~0u, x[j][i], from & (LG - 1), LG);
-        if (turned) x[j][i] = low ? x[j][i] * cs[i] - other * sn[i] : other * sn[i] + x[j][i] * cs[i];
+        const float other = __shfl_sync(~0u, x[i], from & (LG - 1), LG);
+        if (turned) x[i] = low ? x[i] * cs[i] - other * sn[i] : other * sn[i] + x[i] * cs[i];
       }
     }
     if (!live || !mine || hh >= nq + nk + nv) continue;
     if (hh < nq) {
-      store8(static_cast<T*>(a.q_out) + (static_cast<int64_t>(token) * a.heads + hh) * a.D + lane * 8, x[j]);
+      store8(static_cast<T*>(a.q_out) + (static_cast<int64_t>(token) * a.heads + hh) * a.D + lane * 8, x);
     } else if constexpr (kAppend) {
       if (slot >= 0) {
         const int h = is_v ? hh - nq - nk : hh - nq;
         T* pages = static_cast<T*>(is_v ? a.v_pages : a.k_pages);
-        store8(pages + (slot + (static_cast<int64_t>(h) << a.seq.page_shift)) * a.D + lane * 8, x[j]);
+        store8(pages + (slot + (static_cast<int64_t>(h) << a.seq.page_shift)) * a.D + lane * 8, x);
       }
     } else {
-      store8(static_cast<T*>(a.k_out) + (static_cast<int64_t>(token) * a.heads_kv + hh - nq) * a.D + lane * 8, x[j]);
+      store8(static_cast<T*>(a.k_out) + (static_cast<int64_t>(token) * a.heads_kv + hh - nq) * a.D + lane * 8, x);
     }
   }
 }
@@ -228,6 +242,10 @@ cudaError_t pick_lanes(const RopeArgs& a, bool adjacent, cudaStream_t s) {
 cudaError_t launch_rope(const engram_attn_plan* p, const RopeArgs& a, cudaStream_t s) {
   const bool adjacent = p->cfg.rope_adjacent != 0;
   const bool f32 = p->cfg.dtype == ENGRAM_F32;
+  const int64_t heads = static_cast<int64_t>(a.tokens) *
+                        ((a.q.ptr ? a.heads : 0) + (a.k.ptr ? a.heads_kv : 0) + (a.k_pages ? a.heads_kv : 0));
+  if (heads >= kManyHeads)
+    return f32 ? pick_lanes<float, 4>(a, adjacent, s) : pick_lanes<__nv_bfloat16, 4>(a, adjacent, s);
   return f32 ? pick_lanes<float, 1>(a, adjacent, s) : pick_lanes<__nv_bfloat16, 1>(a, adjacent, s);
 }
 
