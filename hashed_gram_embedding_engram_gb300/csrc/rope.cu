@@ -5,11 +5,15 @@
 // the row of the token's position in a float table.
 //
 // One group of 8, 16 or 32 lanes holds one head of one token, 8 elements a
-// lane, so a head is read once in 16-byte loads, its sum of squares is a
-// shuffle tree and its pairs are in one lane (adjacent) or two (halves).  All
-// arithmetic is float; the outputs are rounded once.  What bounds it: device
-// memory on long inputs, the launch and three dependent loads (sequence,
-// page, row of the table) on a decode step.
+// lane: four from each half of the rotated part (pairs i, i + rotary/2) or
+// eight that follow one another (adjacent pairs, and what is not rotated).  So
+// both elements of a pair, and the four cosines and sines that they need, are
+// in one lane; only the sum of squares crosses lanes.  A block has heads of
+// one kind (queries, keys or values): its pointers, strides and norm weights
+// are the same for all its lanes.  All arithmetic is float; the outputs are
+// rounded once.  What bounds it: device memory on long inputs, the launch and
+// the chain of dependent loads (sequence, page, row of the table) on a decode
+// step.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,233 +24,261 @@ namespace engram {
 namespace {
 
 constexpr int kNT = 256;
-constexpr int64_t kManyHeads = 65536;   // from here a group takes four heads of a token, below one
+constexpr int kBlocksPerSm = 6;
 
-// Eight elements as they lie in memory (one or two 16-byte words), and as floats.
+// Two runs of four elements as they lie in memory, and as floats.
 template <typename T>
-struct Raw {
-  uint4 w[sizeof(T) / 2];
+struct Raw;
+template <>
+struct Raw<float> {
+  uint4 lo, hi;
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 lo, hi;
 };
 
-template <typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p) {
-  Raw<T> r;
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
-  return r;
-}
-
 __device__ __forceinline__ void to_float(const Raw<float>& r, float (&x)[8]) {
-  const uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+  x[0] = __uint_as_float(r.lo.x), x[1] = __uint_as_float(r.lo.y), x[2] = __uint_as_float(r.lo.z);
+  x[3] = __uint_as_float(r.lo.w), x[4] = __uint_as_float(r.hi.x), x[5] = __uint_as_float(r.hi.y);
+  x[6] = __uint_as_float(r.hi.z), x[7] = __uint_as_float(r.hi.w);
 }
 __device__ __forceinline__ void to_float(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
-  const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+  const uint32_t u[4] = {r.lo.x, r.lo.y, r.hi.x, r.hi.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(u[i] << 16);
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) { to_float(load_raw(p), x); }
-
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ Raw<float> from_float(const float (&x)[8], float) {
+  return {make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])),
+          make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]))};
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+__device__ __forceinline__ Raw<__nv_bfloat16> from_float(const float (&x)[8], __nv_bfloat16) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     u[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  return {make_uint2(u[0], u[1]), make_uint2(u[2], u[3])};
 }
 
-// LG lanes a head; HB heads of a token in turn by one group (their loads in
-// flight together).  kAppend: positions from the sequences, k and v to pages.
-template <typename T, int LG, int HB, bool kAppend>
-__global__ void __launch_bounds__(kNT) rope_kernel(const __grid_constant__ RopeArgs a, int blocks_per_token, bool adjacent) {
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
-  constexpr int kGroups = kNT / LG;
-  const int lane = threadIdx.x % LG;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LG;
-  const int token = static_cast<int>(item / blocks_per_token);
-  const int h0 = static_cast<int>(item - static_cast<int64_t>(token) * blocks_per_token) * HB;
-  const bool live = token < a.tokens;
-  const bool mine = lane * 8 < a.D;
-  const int nq = a.q.ptr ? a.heads : 0, nk = a.k.ptr ? a.heads_kv : 0, nv = kAppend ? a.heads_kv : 0;
+// Where a token's keys and values go.
+struct Place {
+  int64_t slot;    // cache row of head 0 of its token ((page id * heads_kv) * page + slot), or -1
+  int pos;         // row of the table, or -1: not rotated
+};
 
-  // heads of this group: queries, then keys, then values
-  Raw<T> raw[HB];
-#pragma unroll
-  for (int j = 0; j < HB; ++j) {
-    const int hh = h0 + j;
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) raw[j].w[i] = make_uint4(0, 0, 0, 0);
-    if (!live || !mine || hh >= nq + nk + nv) continue;
-    const HeadsView& view = hh < nq ? a.q : (hh < nq + nk ? a.k : a.v);
-    const int h = hh < nq ? hh : (hh < nq + nk ? hh - nq : hh - nq - nk);
-    raw[j] = load_raw(static_cast<const T*>(view.ptr) + token * view.ts + h * view.hs + lane * 8);
-  }
-
-  int pos = -1;
-  int64_t slot = -1;    // cache row of head 0 of this token: ((page id * heads_kv) * page + slot)
+// The place of token `token`; `first`: sequence of the block's first token.
+template <bool kAppend>
+__device__ __forceinline__ Place find_place(const RopeArgs& a, int token, int b) {
+  Place x{-1, -1};
   bool bad = false;
   if constexpr (kAppend) {
-    // the sequence of the block's first token by a count over start[1..B]; then a walk
-    const int first = static_cast<int>(static_cast<int64_t>(blockIdx.x) * kGroups / blocks_per_token);
-    int b = 0;
-    for (int base = 1; base <= a.seq.B; base += kNT) {
-      const int i = base + threadIdx.x;
-      b += __syncthreads_count(i <= a.seq.B && __ldg(a.seq.start + i) <= first);
+    while (b < a.seq.B && __ldg(a.seq.start + b + 1) <= token) ++b;
+    if (b >= a.seq.B) {
+      bad = true;          // a row that no sequence has
+    } else {
+      const int begin = __ldg(a.seq.start + b), end = __ldg(a.seq.start + b + 1), len = __ldg(a.seq.length + b);
+      const int64_t room = static_cast<int64_t>(a.seq.table_pages) << a.seq.page_shift;
+      bad = begin < 0 || begin > token || end > a.tokens || len < 0 || len > room;
+      if (!bad) x.pos = max(len - end + token, -1);
     }
-    if (live) {
-      while (b < a.seq.B && __ldg(a.seq.start + b + 1) <= token) ++b;
-      const int begin = b < a.seq.B ? __ldg(a.seq.start + b) : 0;
-      if (b >= a.seq.B || begin < 0 || begin > token || __ldg(a.seq.start + b + 1) > a.tokens) {
-        bad = true;        // a row that no sequence has
-      } else {
-        const int len = __ldg(a.seq.length + b);
-        const int64_t room = static_cast<int64_t>(a.seq.table_pages) << a.seq.page_shift;
-        pos = len - __ldg(a.seq.start + b + 1) + token;
-        if (len < 0 || len > room) {
-          bad = true;
-          pos = -1;
-        }
-      }
-      if (pos >= 0 && !bad && h0 + HB > nq) {
-        const int pid = __ldg(a.seq.table + static_cast<int64_t>(b) * a.seq.table_pages + (pos >> a.seq.page_shift));
-        if (pid < 0 || pid >= a.pages) {
-          bad = true;
-        } else {
-          slot = (static_cast<int64_t>(pid) * a.heads_kv << a.seq.page_shift) +
-                 (pos & ((1 << a.seq.page_shift) - 1));
-        }
-      }
+    if (x.pos >= 0) {
+      const int pid = __ldg(a.seq.table + static_cast<int64_t>(b) * a.seq.table_pages + (x.pos >> a.seq.page_shift));
+      if (pid < 0 || pid >= a.pages)
+        bad = true;
+      else
+        x.slot = (static_cast<int64_t>(pid) * a.heads_kv << a.seq.page_shift) +
+                 (x.pos & ((1 << a.seq.page_shift) - 1));
+    }
+  } else if (a.positions) {
+    x.pos = __ldg(a.positions + token);
+    bad = x.pos < 0;
+  }
+  if (a.rope && a.rotary > 0) {
+    if (x.pos >= a.rope_len) {
+      bad = true;
+      x.pos = -1;
     }
   } else {
-    if (live && a.positions) {
-      pos = __ldg(a.positions + token);
-      bad = pos < 0;
+    x.pos = -1;
+  }
+  if (bad) atomicOr(a.err, kErrIndexRange);
+  return x;
+}
+
+enum Kind { kQueries, kKeys, kValues };
+
+// A block takes rounds * kGroups heads of one kind that follow one another (the
+// heads of token 0, of token 1, ..), a group one at a time; each group's next
+// head is on its way while it works on the current one.  With more rounds than
+// one, the places of the block's tokens are found once, by a thread each.
+// kAppend: places from the sequences, k and v to pages; else from positions.
+template <typename T, int LG, bool kAppend>
+__global__ void __launch_bounds__(kNT)
+    rope_kernel(const __grid_constant__ RopeArgs a, int blocks_q, int blocks_k, int rounds, bool adjacent) {
+  constexpr int kGroups = kNT / LG;
+  using R = Raw<T>;
+  using V = decltype(R::lo);
+  __shared__ Place places[kNT];
+  const int lane = threadIdx.x % LG, group = threadIdx.x / LG;
+  int block = static_cast<int>(blockIdx.x);
+  Kind kind = kQueries;
+  if (block >= blocks_q) {
+    block -= blocks_q, kind = kKeys;
+    if (kAppend && block >= blocks_k) block -= blocks_k, kind = kValues;
+  }
+  const HeadsView view = kind == kQueries ? a.q : (kind == kKeys ? a.k : a.v);
+  const int heads = kind == kQueries ? a.heads : a.heads_kv;
+  const float* g = kind == kQueries ? a.g_q : (kind == kKeys ? a.g_k : nullptr);
+  const int64_t items = static_cast<int64_t>(a.tokens) * heads;
+  const int64_t first = static_cast<int64_t>(block) * rounds * kGroups;
+  const int n = static_cast<int>(min(items - first, static_cast<int64_t>(rounds * kGroups)));
+  const int t0 = static_cast<int>(first / heads);
+
+  // this lane's two runs of a head, and the angles of its pairs
+  const bool mine = lane * 8 < a.D;
+  const bool in_rotary = kind != kValues && lane * 8 < a.rotary;
+  const bool split = in_rotary && !adjacent;
+  const int at_lo = split ? lane * 4 : lane * 8, at_hi = split ? a.rotary / 2 + lane * 4 : lane * 8 + 4;
+
+  // the group's head, and the steps to its next one
+  int t = static_cast<int>((first + group) / heads), h = static_cast<int>((first + group) - static_cast<int64_t>(t) * heads);
+  const int step_t = kGroups / heads, step_h = kGroups - step_t * heads;
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  auto load = [&](int t, int h, bool live) {
+    R r{};
+    if (live && mine) {
+      const T* p = static_cast<const T*>(view.ptr) + t * view.ts + h * view.hs;
+      r.lo = *reinterpret_cast<const V*>(p + at_lo);
+      r.hi = *reinterpret_cast<const V*>(p + at_hi);
+    }
+    return r;
+  };
+  R now = load(t, h, group < n);
+  float gw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) gw[i] = 1.f;
+  if (g && mine) {
+    const float4 lo = __ldg(reinterpret_cast<const float4*>(g + at_lo)), hi = __ldg(reinterpret_cast<const float4*>(g + at_hi));
+    gw[0] = lo.x, gw[1] = lo.y, gw[2] = lo.z, gw[3] = lo.w, gw[4] = hi.x, gw[5] = hi.y, gw[6] = hi.z, gw[7] = hi.w;
+  }
+
+  int b = 0;
+  if constexpr (kAppend) {       // the sequence of the first token, by a count over start[1..B]
+    for (int base = 1; base <= a.seq.B; base += kNT) {
+      const int i = base + threadIdx.x;
+      b += __syncthreads_count(i <= a.seq.B && __ldg(a.seq.start + i) <= t0);
     }
   }
-  bool turn = pos >= 0 && a.rope != nullptr && a.rotary > 0;
-  if (turn && pos >= a.rope_len) {
-    bad = true;
-    turn = false;
-  }
-  if (bad && live && lane == 0) atomicOr(a.err, kErrIndexRange);
-
-  float cs[8], sn[8];
-  const int half = a.rotary / 2;
-  const bool rotated = turn && lane * 8 < a.rotary;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-  if (rotated) {
-    const float* row = a.rope + static_cast<int64_t>(pos) * a.rotary;
-    if (adjacent) {
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + lane * 4));
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + half + lane * 4));
-      cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
-      sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
-    } else {
-      const int at = lane * 8 < half ? lane * 8 : lane * 8 - half;
-      load8(row + at, cs);
-      load8(row + half + at, sn);
-    }
+  const bool once = rounds == 1;
+  if (!once) {
+    const int t1 = static_cast<int>((first + n - 1) / heads);     // at most kNT tokens: a block has at most kNT heads
+    if (t0 + static_cast<int>(threadIdx.x) <= t1) places[threadIdx.x] = find_place<kAppend>(a, t0 + threadIdx.x, b);
+    __syncthreads();
   }
 
-#pragma unroll
-  for (int j = 0; j < HB; ++j) {
-    const int hh = h0 + j;
-    const bool is_v = kAppend && hh >= nq + nk;
-    const float* g = is_v ? nullptr : (hh < nq ? a.g_q : a.g_k);
-    const bool turned = rotated && !is_v;
-    // the groups of a warp may hold different kinds of heads: all lanes take part in every shuffle
+  // every group makes the same number of turns: all lanes of a warp take part in the shuffles
+  for (int i0 = 0; i0 < n; i0 += kGroups) {
+    const bool live = i0 + group < n;
+    int next_t = t + step_t, next_h = h + step_h;
+    if (next_h >= heads) next_h -= heads, ++next_t;
+    const R next = load(next_t, next_h, i0 + kGroups + group < n);
+    Place place{-1, -1};
+    if (live) place = once ? find_place<kAppend>(a, t, b) : places[t - t0];
     float x[8];
-    to_float(raw[j], x);
-    float ss = 0.f;
+    to_float(now, x);
+    if (kind != kValues) {       // the same in the whole block
+      float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in_rotary && place.pos >= 0) {
+        const float* row = a.rope + static_cast<int64_t>(place.pos) * a.rotary + lane * 4;
+        c4 = __ldg(reinterpret_cast<const float4*>(row));
+        s4 = __ldg(reinterpret_cast<const float4*>(row + a.rotary / 2));
+      }
+      if (g) {
+        float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-    for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-    if (g && mine) {
-      const float inv = 1.f / sqrtf(ss / a.D + a.eps);
-      float gw[8];
-      load8(g + lane * 8, gw);
+        for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+        const float inv = rsqrtf(ss / a.D + a.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * gw[i];
-    }
-    if (adjacent) {
-      if (turned) {
+        for (int i = 0; i < 8; ++i) x[i] *= inv * gw[i];
+      }
+      const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+      if (adjacent) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float lo = x[2 * i], hi = x[2 * i + 1];
           x[2 * i] = lo * cs[i] - hi * sn[i];
           x[2 * i + 1] = lo * sn[i] + hi * cs[i];
         }
-      }
-    } else {
-      const int step = a.rotary / 16;                  // lanes between the halves
-      const bool low = lane * 8 < half;
-      const int from = low ? lane + step : lane - step;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_sync(~0u, x[i], from & (LG - 1), LG);
-        if (turned) x[i] = low ? x[i] * cs[i] - other * sn[i] : other * sn[i] + x[i] * cs[i];
+        for (int i = 0; i < 4; ++i) {
+          const float lo = x[i], hi = x[4 + i];
+          x[i] = lo * cs[i] - hi * sn[i];
+          x[4 + i] = lo * sn[i] + hi * cs[i];
+        }
       }
     }
-    if (!live || !mine || hh >= nq + nk + nv) continue;
-    if (hh < nq) {
-      store8(static_cast<T*>(a.q_out) + (static_cast<int64_t>(token) * a.heads + hh) * a.D + lane * 8, x);
-    } else if constexpr (kAppend) {
-      if (slot >= 0) {
-        const int h = is_v ? hh - nq - nk : hh - nq;
-        T* pages = static_cast<T*>(is_v ? a.v_pages : a.k_pages);
-        store8(pages + (slot + (static_cast<int64_t>(h) << a.seq.page_shift)) * a.D + lane * 8, x);
+    if (live && mine) {
+      T* to = nullptr;
+      if (kind == kQueries)
+        to = static_cast<T*>(a.q_out) + (static_cast<int64_t>(t) * heads + h) * a.D;
+      else if constexpr (!kAppend)
+        to = static_cast<T*>(a.k_out) + (static_cast<int64_t>(t) * heads + h) * a.D;
+      else if (place.slot >= 0)
+        to = static_cast<T*>(kind == kKeys ? a.k_pages : a.v_pages) +
+             (place.slot + (static_cast<int64_t>(h) << a.seq.page_shift)) * a.D;
+      if (to) {
+        const R r = from_float(x, T());
+        *reinterpret_cast<V*>(to + at_lo) = r.lo;
+        *reinterpret_cast<V*>(to + at_hi) = r.hi;
       }
-    } else {
-      store8(static_cast<T*>(a.k_out) + (static_cast<int64_t>(token) * a.heads_kv + hh - nq) * a.D + lane * 8, x);
     }
+    __syncwarp();
+    now = next, t = next_t, h = next_h;
   }
 }
 
-template <typename T, int LG, int HB>
-cudaError_t run(const RopeArgs& a, bool adjacent, cudaStream_t s) {
-  const bool append = a.k_pages != nullptr;
-  const int heads = (a.q.ptr ? a.heads : 0) + (a.k.ptr ? a.heads_kv : 0) + (append ? a.heads_kv : 0);
-  const int per = (heads + HB - 1) / HB;
-  const int64_t items = static_cast<int64_t>(a.tokens) * per;
-  const int64_t grid = (items + kNT / LG - 1) / (kNT / LG);
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  if (append)
-    return launch_pdl(rope_kernel<T, LG, HB, true>, dim3(static_cast<unsigned>(grid)), dim3(kNT), 0, s, a, per,
+template <typename T, int LG>
+cudaError_t run(const RopeArgs& a, bool adjacent, int num_sms, cudaStream_t s) {
+  constexpr int kGroups = kNT / LG;
+  const int64_t q = a.q.ptr ? static_cast<int64_t>(a.tokens) * a.heads : 0;
+  const int64_t k = a.k.ptr ? static_cast<int64_t>(a.tokens) * a.heads_kv : 0, v = a.k_pages ? k : 0;
+  // heads of a group: one while that leaves the SMs less than kBlocksPerSm blocks each, then more,
+  // so that the chain of loads that finds the places is paid for several at once
+  int64_t rounds = (q + k + v) / (static_cast<int64_t>(kGroups) * num_sms * kBlocksPerSm);
+  rounds = rounds < 1 ? 1 : (rounds > LG ? LG : rounds);          // at most LG * kGroups = kNT heads a block
+  const auto blocks = [&](int64_t n) { return (n + rounds * kGroups - 1) / (rounds * kGroups); };
+  if (blocks(q) + blocks(k) + blocks(v) > INT32_MAX) return cudaErrorInvalidValue;
+  const int bq = static_cast<int>(blocks(q)), bk = static_cast<int>(blocks(k));
+  const unsigned grid = static_cast<unsigned>(bq + bk + blocks(v));
+  if (a.k_pages)
+    return launch_pdl(rope_kernel<T, LG, true>, dim3(grid), dim3(kNT), 0, s, a, bq, bk, static_cast<int>(rounds),
                       adjacent);
-  return launch_pdl(rope_kernel<T, LG, HB, false>, dim3(static_cast<unsigned>(grid)), dim3(kNT), 0, s, a, per,
+  return launch_pdl(rope_kernel<T, LG, false>, dim3(grid), dim3(kNT), 0, s, a, bq, bk, static_cast<int>(rounds),
                     adjacent);
 }
 
-template <typename T, int HB>
-cudaError_t pick_lanes(const RopeArgs& a, bool adjacent, cudaStream_t s) {
-  if (a.D <= 64) return run<T, 8, HB>(a, adjacent, s);
-  if (a.D <= 128) return run<T, 16, HB>(a, adjacent, s);
-  return run<T, 32, HB>(a, adjacent, s);
+template <typename T>
+cudaError_t pick_lanes(const RopeArgs& a, bool adjacent, int num_sms, cudaStream_t s) {
+  if (a.D <= 64) return run<T, 8>(a, adjacent, num_sms, s);
+  if (a.D <= 128) return run<T, 16>(a, adjacent, num_sms, s);
+  return run<T, 32>(a, adjacent, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const engram_attn_plan* p, const RopeArgs& a, cudaStream_t s) {
   const bool adjacent = p->cfg.rope_adjacent != 0;
-  const bool f32 = p->cfg.dtype == ENGRAM_F32;
-  const int64_t heads = static_cast<int64_t>(a.tokens) *
-                        ((a.q.ptr ? a.heads : 0) + (a.k.ptr ? a.heads_kv : 0) + (a.k_pages ? a.heads_kv : 0));
-  if (heads >= kManyHeads)
-    return f32 ? pick_lanes<float, 4>(a, adjacent, s) : pick_lanes<__nv_bfloat16, 4>(a, adjacent, s);
-  return f32 ? pick_lanes<float, 1>(a, adjacent, s) : pick_lanes<__nv_bfloat16, 1>(a, adjacent, s);
+  return p->cfg.dtype == ENGRAM_F32 ? pick_lanes<float>(a, adjacent, p->num_sms, s)
+                                    : pick_lanes<__nv_bfloat16>(a, adjacent, p->num_sms, s);
 }
 
 }  // namespace engram
