@@ -184,6 +184,7 @@ engram_status_t engram_qk_norm_rope(const engram_attn_plan_t* plan, const engram
   a.D = plan->cfg.head_dim;
   a.rotary = plan->cfg.rotary_dim;
   a.eps = plan->cfg.eps;
+  a.inv_D = 1.f / static_cast<float>(plan->cfg.head_dim);
   a.err = plan->err;
   return cuda_status(engram::launch_rope(plan, a, (cudaStream_t)stream));
 }
@@ -220,6 +221,7 @@ engram_status_t engram_kv_append(engram_kv_cache_t* cache, const engram_sequence
   a.D = plan->cfg.head_dim;
   a.rotary = rope ? plan->cfg.rotary_dim : 0;
   a.eps = plan->cfg.eps;
+  a.inv_D = 1.f / static_cast<float>(plan->cfg.head_dim);
   a.err = plan->err;
   return cuda_status(engram::launch_rope(plan, a, (cudaStream_t)stream));
 }

@@ -63,7 +63,7 @@ struct RopeArgs {
   SeqArgs seq;
   int tokens;
   int heads, heads_kv, D, rotary, rope_len;
-  float eps;
+  float eps, inv_D;
   uint32_t* err;
 };
 

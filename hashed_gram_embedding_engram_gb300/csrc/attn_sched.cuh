@@ -117,17 +117,32 @@ __device__ __forceinline__ void walk_next(const AttnArgs& a, Walk& w) {
 }
 
 // All threads of the block (NT of them): the block's range.  Every block reads
-// all lengths; the sums are whole numbers, so all blocks agree.
+// all lengths; the sums are whole numbers, so all blocks agree.  A thread has a
+// sequence; one with several row tiles is summed by the lanes of its warp (as a
+// loop of the one thread, 64 tiles took 80 us).
 template <int NT, int RT, int KT>
 __device__ void find_range(const AttnArgs& a, Range* out) {
   __shared__ int64_t warp_sum[NT / 32];
+  __shared__ int64_t rest;     // units before u0 in its sequence
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto tile_units = [&](const Seq& q, int r) {
+    return units_of<KT>(key_range<RT>(q, a.group, r, a.causal, a.window));
+  };
   auto units_per_head = [&](int b, uint32_t* err) -> int64_t {
-    if (b >= a.seq.B) return 0;
-    const Seq q = load_seq(a.seq, b, err);
+    Seq q{0, 0, 0};
+    if (b < a.seq.B) q = load_seq(a.seq, b, err);
     const int tiles = row_tiles<RT>(q, a.group);
-    int64_t n = 0;
-    for (int r = 0; r < tiles; ++r) n += units_of<KT>(key_range<RT>(q, a.group, r, a.causal, a.window));
+    int64_t n = tiles == 1 ? tile_units(q, 0) : 0;
+    for (uint32_t many = __ballot_sync(~0u, tiles > 1); many; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      const Seq p{0, __shfl_sync(~0u, q.n, src), __shfl_sync(~0u, q.len, src)};
+      const int p_tiles = __shfl_sync(~0u, tiles, src);
+      int64_t sum = 0;
+      for (int r = lane; r < p_tiles; r += 32) sum += tile_units(p, r);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      if (lane == src) n = sum;
+    }
     return n;
   };
   auto scan = [&](int64_t v, int64_t& total) -> int64_t {   // inclusive, over the block
@@ -164,33 +179,43 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
     out->u0 = u0;
     out->u1 = u1;
   }
-  if (u0 >= u1) {
-    __syncthreads();
-    return;
-  }
-  int64_t before = 0;
-  for (int base = 0; base < a.seq.B; base += NT) {
-    int64_t total = U;
-    if (a.seq.B > NT) {
-      mine = units_per_head(base + tid, nullptr) * a.heads_kv;
-      upto = scan(mine, total);
-    }
-    if (before + upto - mine <= u0 && u0 < before + upto) {   // one thread: sequence base + tid
-      const int64_t rest = u0 - (before + upto - mine), per = mine / a.heads_kv;
-      out->b = base + tid;
-      out->h = static_cast<int>(rest / per);
-      const Seq q = load_seq(a.seq, base + tid, nullptr);
-      int64_t left = rest % per;
-      int r = 0;
-      for (;; ++r) {
-        const int n = units_of<KT>(key_range<RT>(q, a.group, r, a.causal, a.window));
-        if (left < n) break;
-        left -= n;
+  if (u0 < u1) {
+    int64_t before = 0;
+    for (int base = 0; base < a.seq.B; base += NT) {
+      int64_t total = U;
+      if (a.seq.B > NT) {
+        mine = units_per_head(base + tid, nullptr) * a.heads_kv;
+        upto = scan(mine, total);
       }
-      out->r = r;
-      out->tile_u0 = u0 - left;
+      if (before + upto - mine <= u0 && u0 < before + upto) {   // one thread: sequence base + tid
+        const int64_t in = u0 - (before + upto - mine), per = mine / a.heads_kv;
+        out->b = base + tid;
+        out->h = static_cast<int>(in / per);
+        rest = in % per;
+      }
+      before += total;
     }
-    before += total;
+    __syncthreads();
+    if (warp == 0) {                       // the row tile that holds it
+      const Seq q = load_seq(a.seq, out->b, nullptr);
+      const int tiles = row_tiles<RT>(q, a.group);
+      int64_t at = 0;
+      for (int r0 = 0; r0 < tiles; r0 += 32) {
+        const int64_t n = r0 + lane < tiles ? tile_units(q, r0 + lane) : 0;
+        int64_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t t = __shfl_up_sync(~0u, inc, o);
+          if (lane >= o) inc += t;
+        }
+        const int64_t left = rest - at - (inc - n);
+        if (left >= 0 && left < n) {       // one lane
+          out->r = r0 + lane;
+          out->tile_u0 = u0 - left;
+        }
+        at += __shfl_sync(~0u, inc, 31);
+      }
+    }
   }
   __syncthreads();
 }
@@ -238,36 +263,108 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 
 constexpr float kLn2 = 0.69314718055994531f;
 
-// Join the partials of blocks cf..cl for the tile's `rows` valid rows and write
-// the output.  A row without keys has maximum -inf and total 0 in every part.
-template <typename T, int NT, int RT>
-__device__ void join_tile(const AttnArgs& a, const Walk& w, int cf, int cl, int tid) {
-  const int rows = min(RT, w.q.n * a.group - w.r * RT);
+// Weighted sums of the parts for kEach 4-element vectors a thread, kParts parts' loads in flight.
+template <typename T, int NT, int RT, int kEach, int kParts, typename Place>
+__device__ __forceinline__ void join_sums(const AttnArgs& a, const float* first, int n, int rows, int tid,
+                                          const Place& place) {
+  const int64_t slot = RT * (a.D + 2);
   const int vecs = a.D / 4;
-  for (int x = tid; x < rows * vecs; x += NT) {
-    const int row = x / vecs, d = (x - row * vecs) * 4;
-    float top = -INFINITY;
-    for (int c = cf; c <= cl; ++c) top = fmaxf(top, __ldcg(part_slot<RT>(a, 2 * c + (c == cf)) + RT * a.D + row));
-    float total = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = cf; c <= cl; ++c) {
-      const float* s = part_slot<RT>(a, 2 * c + (c == cf));
-      const float m = __ldcg(s + RT * a.D + row);
-      if (m == -INFINITY) continue;
-      const float f = exp2f(m - top);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * a.D + d));
-      total = fmaf(f, __ldcg(s + RT * a.D + RT + row), total);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
+  for (int x0 = tid; x0 < rows * vecs; x0 += NT * kEach) {
+    int row[kEach], d[kEach];
+    float4 o[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int x = min(x0 + i * NT, rows * vecs - 1);
+      row[i] = x / vecs;
+      d[i] = (x - row[i] * vecs) * 4;
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const int rr = w.r * RT + row;
-    const int64_t at = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
-    store4(static_cast<T*>(a.out) + at * a.D + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (d == 0 && a.lse) a.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+    for (int c0 = 0; c0 < n; c0 += kParts) {
+      float f[kParts][kEach];
+      float4 v[kParts][kEach];
+#pragma unroll
+      for (int c = 0; c < kParts; ++c)
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const float* s = first + (c0 + c == 0 ? 0 : (2 * (c0 + c) - 1) * slot);
+          const bool in = c0 + c < n;
+          f[c][i] = in ? __ldcg(s + RT * a.D + row[i]) : 0.f;
+          v[c][i] = in ? __ldcg(reinterpret_cast<const float4*>(s + row[i] * a.D + d[i])) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int c = 0; c < kParts; ++c)
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          o[i].x = fmaf(f[c][i], v[c][i].x, o[i].x);
+          o[i].y = fmaf(f[c][i], v[c][i].y, o[i].y);
+          o[i].z = fmaf(f[c][i], v[c][i].z, o[i].z);
+          o[i].w = fmaf(f[c][i], v[c][i].w, o[i].w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (x0 + i * NT < rows * vecs) store4(static_cast<T*>(a.out) + place(row[i]) * a.D + d[i], o[i]);
   }
+}
+
+// Join the partials of blocks cf..cl for the tile's valid rows and write the
+// output.  A row without keys has maximum -inf and total 0 in every part.
+// First the parts' factors 2^(m - top) / total, in place of their maxima: a
+// thread a row where the parts are few, else a warp a row and a lane a part;
+// then the weighted sums.  Loads go out together in both: one after another,
+// two parts of 256 rows took 66 us.
+template <typename T, int NT, int RT>
+__device__ void join_tile(const AttnArgs& a, const Walk& w, int cf, int cl, int tid, uint32_t bar) {
+  const int rows = min(RT, w.q.n * a.group - w.r * RT), n = cl - cf + 1;
+  const int64_t slot = RT * (a.D + 2);
+  float* const first = part_slot<RT>(a, 2 * cf + 1);       // then the slots 2c of the later blocks
+  auto stats = [&](int c, int row) { return first + (c == 0 ? 0 : (2 * c - 1) * slot) + RT * a.D + row; };
+  auto place = [&](int row) {
+    const int rr = w.r * RT + row;
+    return (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
+  };
+  auto write_lse = [&](int row, float top, float total) {
+    if (a.lse) a.lse[place(row)] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+  };
+  if (n <= 4) {
+    for (int row = tid; row < rows; row += NT) {
+      float m[4], l[4], top = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        m[c] = c < n ? __ldcg(stats(c, row)) : -INFINITY;
+        l[c] = c < n ? __ldcg(stats(c, row) + RT) : 0.f;
+        top = fmaxf(top, m[c]);
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) total = fmaf(exp2f(m[c] - base), l[c], total);
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) __stcg(stats(c, row), exp2f(m[c] - base) * inv);
+      write_lse(row, top, total);
+    }
+  } else {
+    const int lane = tid & 31;
+    for (int row = tid >> 5; row < rows; row += NT / 32) {
+      float top = -INFINITY, total = 0.f;
+      for (int c = lane; c < n; c += 32) top = fmaxf(top, __ldcg(stats(c, row)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      const float base = top == -INFINITY ? 0.f : top;
+      for (int c = lane; c < n; c += 32) total = fmaf(exp2f(__ldcg(stats(c, row)) - base), __ldcg(stats(c, row) + RT), total);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      for (int c = lane; c < n; c += 32) __stcg(stats(c, row), exp2f(__ldcg(stats(c, row)) - base) * inv);
+      if (lane == 0) write_lse(row, top, total);
+    }
+  }
+  ptx::named_barrier(bar, NT);
+  if (n <= 4)
+    join_sums<T, NT, RT, 4, 2>(a, first, n, rows, tid, place);
+  else
+    join_sums<T, NT, RT, 1, 8>(a, first, n, rows, tid, place);
 }
 
 }  // namespace at

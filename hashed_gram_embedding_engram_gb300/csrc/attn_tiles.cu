@@ -26,6 +26,7 @@
 #include "attn_internal.h"
 #include "attn_sched.cuh"
 #include "attn_tma.cuh"
+#include "f32x2.cuh"
 #include "ptx.cuh"
 
 namespace engram {
@@ -35,7 +36,7 @@ using namespace at;
 
 constexpr int kRT = 256;
 constexpr int kKT = 128;
-constexpr int kNT = 320;
+constexpr int kNT = 384;           // three warpgroups; warps 10 and 11 only round the third one up
 constexpr float kSlack = 8.f;      // powers of two a row's maximum may grow before O is rescaled
 
 template <int D>
@@ -134,121 +135,10 @@ __global__ void __launch_bounds__(kNT, 1)
   if (range.u0 < range.u1) {
     Walk w = walk_begin<kRT, kKT>(a, range);
     int64_t u = range.u0, tile_u0 = range.tile_u0;
-    if (warp == 8) {
-      // -------------------------------------------------------------- TMA
-      int stage = 0, filled = 0;
-      uint32_t phase = 0;
-      while (true) {
-        const int ua = static_cast<int>(u - tile_u0);
-        const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
-        for (int un = ua; un < ub && w.k.hi > 0; ++un) {
-          const int j0 = (w.k.lo / kKT + un) * kKT;
-          const int32_t row = page_row<kKT>(a, w, j0, lane);
-          wait_bounded(&sh.empty_k[stage], phase ^ 1, &sh.abort, a.err);
-          if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full_k[stage], kTile);
-          __syncwarp();
-          load_boxes<kKT, D>(a, &map_k, sk + stage * kTile, &sh.full_k[stage], row, j0, lane);
-          wait_bounded(&sh.empty_v[stage], phase ^ 1, &sh.abort, a.err);
-          if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full_v[stage], kTile);
-          __syncwarp();
-          load_boxes<kKT, D>(a, &map_v, sv + stage * kTile, &sh.full_v[stage], row, j0, lane);
-          if (filled < kStages) ++filled;
-          if (++stage == kStages) stage = 0, phase ^= 1;
-        }
-        u = tile_u0 + ub;
-        if (u >= range.u1) break;
-        tile_u0 = u;
-        walk_next<kRT, kKT>(a, w);
-      }
-      if (*reinterpret_cast<volatile int*>(&sh.abort)) {     // copies in flight land before the block ends
-        for (int i = 0; i < filled; ++i) {
-          stage = stage == 0 ? kStages - 1 : stage - 1;
-          if (stage == kStages - 1) phase ^= 1;
-          drain_bounded(&sh.full_k[stage], phase);
-          drain_bounded(&sh.full_v[stage], phase);
-        }
-      }
-    } else if (warp == 9) {
-      // -------------------------------------------------------------- MMA
-      int ks = 0, vs = 0;                       // ring stages
-      uint32_t kp = 0, vp = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
-      auto scores = [&](int t) {                // S(t) = Q(t) K^T of stage ks
-        if (lane == 0) {
-          const uint32_t qa = ptx::smem_u32(sq + t * kTile), ka = ptx::smem_u32(sk + ks * kTile);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
-            ptx::mma_bf16(tmem + t * 128, ptx::sdesc_kmajor_sw128(qa + off), ptx::sdesc_kmajor_sw128(ka + off), kIdescS,
-                          k > 0);
-          }
-          ptx::mma_commit(&sh.s_full[t]);
-        }
-        __syncwarp();
-      };
-      auto next_k = [&] {
-        if (lane == 0) ptx::mma_commit(&sh.empty_k[ks]);
-        __syncwarp();
-        if (++ks == kStages) ks = 0, kp ^= 1;
-      };
-      while (true) {
-        const int ua = static_cast<int>(u - tile_u0);
-        const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
-        if (w.k.hi > 0) {
-          const int nt = w.q.n * a.group - w.r * kRT > 128 ? 2 : 1;
-          for (int t = 0; t < nt; ++t) {
-            wait_bounded(&sh.q_full[t], qp[t], &sh.abort, a.err);
-            qp[t] ^= 1;
-            if (t == 0) wait_bounded(&sh.full_k[ks], kp, &sh.abort, a.err);
-            ptx::tc_fence_after();
-            scores(t);
-          }
-          next_k();
-          for (int un = ua; un < ub; ++un) {
-            for (int t = 0; t < nt; ++t) {
-              if (t == 0) {
-                wait_bounded(&sh.full_v[vs], vp, &sh.abort, a.err);
-                const int j0 = (w.k.lo / kKT + un) * kKT;
-                if (j0 < w.k.lo || j0 + kKT > w.k.hi) {
-                  zero_rows<kKT, D>(sv + vs * kTile, w.k.lo - j0, w.k.hi - j0, lane, 32);
-                  ptx::fence_proxy_async_smem();
-                  __syncwarp();
-                }
-              }
-              wait_bounded(&sh.p_full[t], pp[t], &sh.abort, a.err);
-              pp[t] ^= 1;
-              ptx::tc_fence_after();
-              if (lane == 0) {
-                const uint32_t va = ptx::smem_u32(sv + vs * kTile);
-#pragma unroll
-                for (int k = 0; k < kKT / 16; ++k)
-                  ptx::mma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
-                                   ptx::sdesc_mnmajor_sw128(va + k * 2048, 128 * 128), kIdescO, un > ua || k > 0);
-                ptx::mma_commit(&sh.o_full[t]);
-              }
-              __syncwarp();
-              if (un + 1 < ub) {
-                if (t == 0) {
-                  wait_bounded(&sh.full_k[ks], kp, &sh.abort, a.err);
-                  ptx::tc_fence_after();
-                }
-                scores(t);
-              }
-            }
-            if (lane == 0) ptx::mma_commit(&sh.empty_v[vs]);
-            __syncwarp();
-            if (++vs == kStages) vs = 0, vp ^= 1;
-            if (un + 1 < ub) next_k();
-          }
-        }
-        u = tile_u0 + ub;
-        if (u >= range.u1) break;
-        tile_u0 = u;
-        walk_next<kRT, kKT>(a, w);
-      }
-      if (lane == 0) ptx::mma_commit(&sh.drain);
-      __syncwarp();
-      drain_bounded(&sh.drain, 0);
-    } else {
+    // the block starts with 168 registers a thread (384 x 168 = 64512): the third warpgroup gives
+    // 96 of its own to the softmax warps, which hold a row of 128 scores (256 x 216 + 128 x 72 = 64512)
+    if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
       // -------------------------------------------------------------- softmax
       const int t = warp >> 2, warp4 = warp & 3;
       const uint32_t ts = tmem + t * 128 + (static_cast<uint32_t>(warp4 * 32) << 16);
@@ -316,23 +206,24 @@ __global__ void __launch_bounds__(kNT, 1)
             }
             op ^= 1;
             const float base = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const F2 scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
+            F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t pk[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float x0 = __uint_as_float(s[h * 2 + i / 16][(i % 16) * 2]);
-                const float x1 = __uint_as_float(s[h * 2 + i / 16][(i % 16) * 2 + 1]);
-                const float p0 = ex2(fmaf(x0, a.scale_log2, -base)), p1 = ex2(fmaf(x1, a.scale_log2, -base));
-                sum[(i & 1) * 2] += p0;
-                sum[(i & 1) * 2 + 1] += p1;
-                const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+                const uint32_t* x = &s[h * 2 + i / 16][(i % 16) * 2];
+                const float2 e = unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, base2));
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                sum[i & 1] = add2(sum[i & 1], pack2(p.x, p.y));
+                const __nv_bfloat162 b = __float22bfloat162_rn(p);
                 pk[i] = *reinterpret_cast<const uint32_t*>(&b);
               }
               ptx::tmem_st_32x32b_x32(ts + h * 32, pk);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 total = unpack2(add2(sum[0], sum[1]));
+            l += total.x + total.y;
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
@@ -387,12 +278,135 @@ __global__ void __launch_bounds__(kNT, 1)
         }
         if (!whole) {
           const int cf = block_of(range, tile_u0), cl = block_of(range, tile_u0 + w.units - 1);
-          if (arrive_last<256>(a, cf, cl, &sh.flag, tid, 1)) join_tile<__nv_bfloat16, 256, kRT>(a, w, cf, cl, tid);
+          if (arrive_last<256>(a, cf, cl, &sh.flag, tid, 1)) join_tile<__nv_bfloat16, 256, kRT>(a, w, cf, cl, tid, 1);
         }
         u = tile_u0 + ub;
         if (u >= range.u1) break;
         tile_u0 = u;
         walk_next<kRT, kKT>(a, w);
+      }
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      if (warp == 8) {
+        // -------------------------------------------------------------- TMA
+        int stage = 0, filled = 0;
+        uint32_t phase = 0;
+        while (true) {
+          const int ua = static_cast<int>(u - tile_u0);
+          const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+          for (int un = ua; un < ub && w.k.hi > 0; ++un) {
+            const int j0 = (w.k.lo / kKT + un) * kKT;
+            const int32_t row = page_row<kKT>(a, w, j0, lane);
+            wait_bounded(&sh.empty_k[stage], phase ^ 1, &sh.abort, a.err);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full_k[stage], kTile);
+            __syncwarp();
+            load_boxes<kKT, D>(a, &map_k, sk + stage * kTile, &sh.full_k[stage], row, j0, lane);
+            wait_bounded(&sh.empty_v[stage], phase ^ 1, &sh.abort, a.err);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full_v[stage], kTile);
+            __syncwarp();
+            load_boxes<kKT, D>(a, &map_v, sv + stage * kTile, &sh.full_v[stage], row, j0, lane);
+            if (filled < kStages) ++filled;
+            if (++stage == kStages) stage = 0, phase ^= 1;
+          }
+          u = tile_u0 + ub;
+          if (u >= range.u1) break;
+          tile_u0 = u;
+          walk_next<kRT, kKT>(a, w);
+        }
+        if (*reinterpret_cast<volatile int*>(&sh.abort)) {     // copies in flight land before the block ends
+          for (int i = 0; i < filled; ++i) {
+            stage = stage == 0 ? kStages - 1 : stage - 1;
+            if (stage == kStages - 1) phase ^= 1;
+            drain_bounded(&sh.full_k[stage], phase);
+            drain_bounded(&sh.full_v[stage], phase);
+          }
+        }
+      } else if (warp == 9) {
+        // -------------------------------------------------------------- MMA
+        int ks = 0, vs = 0;                       // ring stages
+        uint32_t kp = 0, vp = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
+        // descriptors are built from their low words at the instruction: as 64-bit values the compiler
+        // keeps all of them, spills them, and the issue becomes the bound
+        const uint64_t base_k = ptx::sdesc_kmajor_sw128(0), base_v = ptx::sdesc_mnmajor_sw128(0, 128 * 128);
+        const uint32_t hi_k = static_cast<uint32_t>(base_k >> 32), hi_v = static_cast<uint32_t>(base_v >> 32);
+        const uint32_t q_lo = static_cast<uint32_t>(base_k) | (ptx::smem_u32(sq) >> 4);
+        const uint32_t k_lo = static_cast<uint32_t>(base_k) | (ptx::smem_u32(sk) >> 4);
+        const uint32_t v_lo = static_cast<uint32_t>(base_v) | (ptx::smem_u32(sv) >> 4);
+        auto scores = [&](int t) {                // S(t) = Q(t) K^T of stage ks
+          if (ptx::elect_one()) {
+            const uint32_t qa = q_lo + t * (kTile >> 4), ka = k_lo + ks * (kTile >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+              ptx::mma_bf16_words(tmem + t * 128, qa + off, hi_k, ka + off, hi_k, kIdescS, k > 0);
+            }
+            ptx::mma_commit(&sh.s_full[t]);
+          }
+          __syncwarp();
+        };
+        auto next_k = [&] {
+          if (ptx::elect_one()) ptx::mma_commit(&sh.empty_k[ks]);
+          __syncwarp();
+          if (++ks == kStages) ks = 0, kp ^= 1;
+        };
+        while (true) {
+          const int ua = static_cast<int>(u - tile_u0);
+          const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+          if (w.k.hi > 0) {
+            const int nt = w.q.n * a.group - w.r * kRT > 128 ? 2 : 1;
+            for (int t = 0; t < nt; ++t) {
+              wait_bounded(&sh.q_full[t], qp[t], &sh.abort, a.err);
+              qp[t] ^= 1;
+              if (t == 0) wait_bounded(&sh.full_k[ks], kp, &sh.abort, a.err);
+              ptx::tc_fence_after();
+              scores(t);
+            }
+            next_k();
+            for (int un = ua; un < ub; ++un) {
+              for (int t = 0; t < nt; ++t) {
+                if (t == 0) {
+                  wait_bounded(&sh.full_v[vs], vp, &sh.abort, a.err);
+                  const int j0 = (w.k.lo / kKT + un) * kKT;
+                  if (j0 < w.k.lo || j0 + kKT > w.k.hi) {
+                    zero_rows<kKT, D>(sv + vs * kTile, w.k.lo - j0, w.k.hi - j0, lane, 32);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                  }
+                }
+                wait_bounded(&sh.p_full[t], pp[t], &sh.abort, a.err);
+                pp[t] ^= 1;
+                ptx::tc_fence_after();
+                if (ptx::elect_one()) {
+                  const uint32_t va = v_lo + vs * (kTile >> 4);
+#pragma unroll
+                  for (int k = 0; k < kKT / 16; ++k)
+                    ptx::mma_bf16_ta_words(tmem + 256 + t * 128, tmem + t * 128 + k * 8, va + k * (2048 >> 4), hi_v, kIdescO,
+                                           un > ua || k > 0);
+                  ptx::mma_commit(&sh.o_full[t]);
+                }
+                __syncwarp();
+                if (un + 1 < ub) {
+                  if (t == 0) {
+                    wait_bounded(&sh.full_k[ks], kp, &sh.abort, a.err);
+                    ptx::tc_fence_after();
+                  }
+                  scores(t);
+                }
+              }
+              if (ptx::elect_one()) ptx::mma_commit(&sh.empty_v[vs]);
+              __syncwarp();
+              if (++vs == kStages) vs = 0, vp ^= 1;
+              if (un + 1 < ub) next_k();
+            }
+          }
+          u = tile_u0 + ub;
+          if (u >= range.u1) break;
+          tile_u0 = u;
+          walk_next<kRT, kKT>(a, w);
+        }
+        if (ptx::elect_one()) ptx::mma_commit(&sh.drain);
+        __syncwarp();
+        drain_bounded(&sh.drain, 0);
       }
     }
   }

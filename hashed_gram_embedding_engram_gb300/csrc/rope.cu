@@ -18,15 +18,17 @@
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
+#include "f32x2.cuh"
 #include "ptx.cuh"
 
 namespace engram {
 namespace {
 
-constexpr int kNT = 256;
+constexpr int kNT = 128;
+constexpr int kMaxRounds = 16;
 constexpr int kBlocksPerSm = 6;
 
-// Two runs of four elements as they lie in memory, and as floats.
+// Two runs of four elements as they lie in memory, and as pairs of floats.
 template <typename T>
 struct Raw;
 template <>
@@ -38,28 +40,25 @@ struct Raw<__nv_bfloat16> {
   uint2 lo, hi;
 };
 
-__device__ __forceinline__ void to_float(const Raw<float>& r, float (&x)[8]) {
-  x[0] = __uint_as_float(r.lo.x), x[1] = __uint_as_float(r.lo.y), x[2] = __uint_as_float(r.lo.z);
-  x[3] = __uint_as_float(r.lo.w), x[4] = __uint_as_float(r.hi.x), x[5] = __uint_as_float(r.hi.y);
-  x[6] = __uint_as_float(r.hi.z), x[7] = __uint_as_float(r.hi.w);
+__device__ __forceinline__ F2 pack2u(uint32_t a, uint32_t b) { return pack2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ void to_float(const Raw<float>& r, F2 (&x)[4]) {
+  x[0] = pack2u(r.lo.x, r.lo.y), x[1] = pack2u(r.lo.z, r.lo.w), x[2] = pack2u(r.hi.x, r.hi.y), x[3] = pack2u(r.hi.z, r.hi.w);
 }
-__device__ __forceinline__ void to_float(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
+__device__ __forceinline__ void to_float(const Raw<__nv_bfloat16>& r, F2 (&x)[4]) {
   const uint32_t u[4] = {r.lo.x, r.lo.y, r.hi.x, r.hi.y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = pack2u(u[i] << 16, u[i] & 0xFFFF0000u);
 }
-__device__ __forceinline__ Raw<float> from_float(const float (&x)[8], float) {
-  return {make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])),
-          make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]))};
+__device__ __forceinline__ Raw<float> from_float(const F2 (&x)[4], float) {
+  const float2 a = unpack2(x[0]), b = unpack2(x[1]), c = unpack2(x[2]), d = unpack2(x[3]);
+  return {make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)),
+          make_uint4(__float_as_uint(c.x), __float_as_uint(c.y), __float_as_uint(d.x), __float_as_uint(d.y))};
 }
-__device__ __forceinline__ Raw<__nv_bfloat16> from_float(const float (&x)[8], __nv_bfloat16) {
+__device__ __forceinline__ Raw<__nv_bfloat16> from_float(const F2 (&x)[4], __nv_bfloat16) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 h = __float22bfloat162_rn(unpack2(x[i]));
     u[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return {make_uint2(u[0], u[1]), make_uint2(u[2], u[3])};
@@ -118,12 +117,12 @@ enum Kind { kQueries, kKeys, kValues };
 // one, the places of the block's tokens are found once, by a thread each.
 // kAppend: places from the sequences, k and v to pages; else from positions.
 template <typename T, int LG, bool kAppend>
-__global__ void __launch_bounds__(kNT)
+__global__ void __launch_bounds__(kNT, 8)
     rope_kernel(const __grid_constant__ RopeArgs a, int blocks_q, int blocks_k, int rounds, bool adjacent) {
   constexpr int kGroups = kNT / LG;
   using R = Raw<T>;
   using V = decltype(R::lo);
-  __shared__ Place places[kNT];
+  __shared__ Place places[kMaxRounds * kGroups];
   const int lane = threadIdx.x % LG, group = threadIdx.x / LG;
   int block = static_cast<int>(blockIdx.x);
   Kind kind = kQueries;
@@ -134,20 +133,23 @@ __global__ void __launch_bounds__(kNT)
   const HeadsView view = kind == kQueries ? a.q : (kind == kKeys ? a.k : a.v);
   const int heads = kind == kQueries ? a.heads : a.heads_kv;
   const float* g = kind == kQueries ? a.g_q : (kind == kKeys ? a.g_k : nullptr);
-  const int64_t items = static_cast<int64_t>(a.tokens) * heads;
-  const int64_t first = static_cast<int64_t>(block) * rounds * kGroups;
-  const int n = static_cast<int>(min(items - first, static_cast<int64_t>(rounds * kGroups)));
-  const int t0 = static_cast<int>(first / heads);
+  const unsigned first = static_cast<unsigned>(block) * (rounds * kGroups);   // below tokens * heads < 2^31
+  const int n = min(a.tokens * heads - static_cast<int>(first), rounds * kGroups);
+  const int t0 = static_cast<int>(first / static_cast<unsigned>(heads));
 
-  // this lane's two runs of a head, and the angles of its pairs
-  const bool mine = lane * 8 < a.D;
-  const bool in_rotary = kind != kValues && lane * 8 < a.rotary;
-  const bool split = in_rotary && !adjacent;
+  // this lane's two runs of a head
+  const bool mine = lane * 8 < a.D, turns = kind != kValues && lane * 8 < a.rotary;
+  const bool split = turns && !adjacent;
   const int at_lo = split ? lane * 4 : lane * 8, at_hi = split ? a.rotary / 2 + lane * 4 : lane * 8 + 4;
 
   // the group's head, and the steps to its next one
-  int t = static_cast<int>((first + group) / heads), h = static_cast<int>((first + group) - static_cast<int64_t>(t) * heads);
+  const int h0 = static_cast<int>(first) - t0 * heads + group;
+  int t = t0 + static_cast<int>(static_cast<unsigned>(h0) / static_cast<unsigned>(heads)), h = h0 - (t - t0) * heads;
   const int step_t = kGroups / heads, step_h = kGroups - step_t * heads;
+  auto step = [&](int& t, int& h) {
+    t += step_t, h += step_h;
+    if (h >= heads) h -= heads, ++t;
+  };
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   auto load = [&](int t, int h, bool live) {
@@ -160,12 +162,13 @@ __global__ void __launch_bounds__(kNT)
     return r;
   };
   R now = load(t, h, group < n);
-  float gw[8];
+  F2 gw[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) gw[i] = 1.f;
+  for (int i = 0; i < 4; ++i) gw[i] = pack2(1.f, 1.f);
   if (g && mine) {
-    const float4 lo = __ldg(reinterpret_cast<const float4*>(g + at_lo)), hi = __ldg(reinterpret_cast<const float4*>(g + at_hi));
-    gw[0] = lo.x, gw[1] = lo.y, gw[2] = lo.z, gw[3] = lo.w, gw[4] = hi.x, gw[5] = hi.y, gw[6] = hi.z, gw[7] = hi.w;
+    const float4 lo = __ldg(reinterpret_cast<const float4*>(g + at_lo));
+    const float4 hi = __ldg(reinterpret_cast<const float4*>(g + at_hi));
+    gw[0] = pack2(lo.x, lo.y), gw[1] = pack2(lo.z, lo.w), gw[2] = pack2(hi.x, hi.y), gw[3] = pack2(hi.z, hi.w);
   }
 
   int b = 0;
@@ -177,52 +180,56 @@ __global__ void __launch_bounds__(kNT)
   }
   const bool once = rounds == 1;
   if (!once) {
-    const int t1 = static_cast<int>((first + n - 1) / heads);     // at most kNT tokens: a block has at most kNT heads
-    if (t0 + static_cast<int>(threadIdx.x) <= t1) places[threadIdx.x] = find_place<kAppend>(a, t0 + threadIdx.x, b);
+    const int t1 = static_cast<int>((first + n - 1) / static_cast<unsigned>(heads));     // at most one token a head
+    for (int i = threadIdx.x; t0 + i <= t1; i += kNT) places[i] = find_place<kAppend>(a, t0 + i, b);
     __syncthreads();
   }
 
   // every group makes the same number of turns: all lanes of a warp take part in the shuffles
+#pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += kGroups) {
     const bool live = i0 + group < n;
-    int next_t = t + step_t, next_h = h + step_h;
-    if (next_h >= heads) next_h -= heads, ++next_t;
+    int next_t = t, next_h = h;
+    step(next_t, next_h);
     const R next = load(next_t, next_h, i0 + kGroups + group < n);
     Place place{-1, -1};
     if (live) place = once ? find_place<kAppend>(a, t, b) : places[t - t0];
-    float x[8];
+    F2 x[4];
     to_float(now, x);
     if (kind != kValues) {       // the same in the whole block
-      float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (in_rotary && place.pos >= 0) {
-        const float* row = a.rope + static_cast<int64_t>(place.pos) * a.rotary + lane * 4;
-        c4 = __ldg(reinterpret_cast<const float4*>(row));
-        s4 = __ldg(reinterpret_cast<const float4*>(row + a.rotary / 2));
-      }
       if (g) {
-        float ss = 0.f;
+        F2 ss = pack2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        for (int i = 0; i < 4; ++i) ss = fma2(x[i], x[i], ss);
+        const float2 s2 = unpack2(ss);
+        float sum = s2.x + s2.y;
 #pragma unroll
-        for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-        const float inv = rsqrtf(ss / a.D + a.eps);
+        for (int o = LG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        const float inv = rsqrtf(fmaf(sum, a.inv_D, a.eps));
+        const F2 inv2 = pack2(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= inv * gw[i];
+        for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], mul2(gw[i], inv2));
       }
-      const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
-      if (adjacent) {
+      if (turns && place.pos >= 0) {
+        const float* row = a.rope + static_cast<int64_t>(place.pos) * a.rotary + lane * 4;
+        const float4 c4 = __ldg(reinterpret_cast<const float4*>(row));
+        const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + a.rotary / 2));
+        if (adjacent) {
+          const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float lo = x[2 * i], hi = x[2 * i + 1];
-          x[2 * i] = lo * cs[i] - hi * sn[i];
-          x[2 * i + 1] = lo * sn[i] + hi * cs[i];
-        }
-      } else {
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = unpack2(x[i]);
+            x[i] = pack2(v.x * cs[i] - v.y * sn[i], v.x * sn[i] + v.y * cs[i]);
+          }
+        } else {
+          const F2 cs[2] = {pack2(c4.x, c4.y), pack2(c4.z, c4.w)}, sn[2] = {pack2(s4.x, s4.y), pack2(s4.z, s4.w)};
+          const F2 neg[2] = {pack2(-s4.x, -s4.y), pack2(-s4.z, -s4.w)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float lo = x[i], hi = x[4 + i];
-          x[i] = lo * cs[i] - hi * sn[i];
-          x[4 + i] = lo * sn[i] + hi * cs[i];
+          for (int i = 0; i < 2; ++i) {
+            const F2 lo = x[i], hi = x[2 + i];
+            x[i] = fma2(lo, cs[i], mul2(hi, neg[i]));
+            x[2 + i] = fma2(hi, cs[i], mul2(lo, sn[i]));
+          }
         }
       }
     }
@@ -254,7 +261,7 @@ cudaError_t run(const RopeArgs& a, bool adjacent, int num_sms, cudaStream_t s) {
   // heads of a group: one while that leaves the SMs less than kBlocksPerSm blocks each, then more,
   // so that the chain of loads that finds the places is paid for several at once
   int64_t rounds = (q + k + v) / (static_cast<int64_t>(kGroups) * num_sms * kBlocksPerSm);
-  rounds = rounds < 1 ? 1 : (rounds > LG ? LG : rounds);          // at most LG * kGroups = kNT heads a block
+  rounds = rounds < 1 ? 1 : (rounds > kMaxRounds ? kMaxRounds : rounds);
   const auto blocks = [&](int64_t n) { return (n + rounds * kGroups - 1) / (rounds * kGroups); };
   if (blocks(q) + blocks(k) + blocks(v) > INT32_MAX) return cudaErrorInvalidValue;
   const int bq = static_cast<int>(blocks(q)), bk = static_cast<int>(blocks(k));
