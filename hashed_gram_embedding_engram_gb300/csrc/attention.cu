@@ -273,8 +273,12 @@ engram_status_t engram_verify_drafts(const void* target, const void* draft_probs
   if (B == 0) return ENGRAM_OK;
   if (!target || !aligned16(target) || !aligned16(draft_probs) || !drafts || !u || !tokens || !accepted)
     return ENGRAM_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return ENGRAM_ERR_CUDA;
   return cuda_status(engram::launch_verify(target, draft_probs, dtype == ENGRAM_F32, drafts, n_drafts, u, B, S, V,
-                                           tokens, accepted, (cudaStream_t)stream));
+                                           tokens, accepted, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -102,6 +102,6 @@ cudaError_t launch_attention_rows(const engram_kv_cache* c, const AttnArgs& a, i
 cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const void* target, const void* draft, bool is_f32, const int32_t* drafts,
                           const int32_t* n_drafts, const float* u, int B, int S, int V, int32_t* tokens,
-                          int32_t* accepted, cudaStream_t s);
+                          int32_t* accepted, int num_sms, cudaStream_t s);
 
 }  // namespace engram

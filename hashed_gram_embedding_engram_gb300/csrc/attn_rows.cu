@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kNT, 2)
     if (!whole) {
       const int cf = block_of(range, tile_u0), cl = block_of(range, tile_u0 + w.units - 1);
       if (arrive_last<kWarps * 32>(a, cf, cl, &sh.flag, tid, 1))
-        join_tile<__nv_bfloat16, kWarps * 32, RT>(a, w, cf, cl, tid, 1);
+        join_tile<__nv_bfloat16, kWarps * 32, RT, true>(a, w, cf, cl, tid, 1);
     } else {
       ptx::named_barrier(1, kWarps * 32);          // s_sum is free for the next tile
     }

@@ -227,7 +227,9 @@ __device__ __forceinline__ int block_of(const Range& g, int64_t u) {
 
 // Partial tiles: slot 2c holds block c's piece of a tile that an earlier block
 // began, slot 2c + 1 its piece of one that it begins and does not end.  A slot
-// is [RT][D] sums, then RT maxima, then RT weight totals.
+// is the sums, then RT maxima, then RT weight totals.  The sums are [RT][D], or
+// [D / 4][RT][4] where a thread holds a row (lanes of a warp then write and
+// read 512 bytes in a row instead of 16 each of 32 rows).
 template <int RT>
 __device__ __forceinline__ float* part_slot(const AttnArgs& a, int slot) {
   return a.parts + static_cast<int64_t>(slot) * (RT * (a.D + 2));
@@ -264,19 +266,29 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Weighted sums of the parts for kEach 4-element vectors a thread, kParts parts' loads in flight.
-template <typename T, int NT, int RT, int kEach, int kParts, typename Place>
+// kByRow: slots of [RT][D] sums, the threads' vectors NT apart; else [D / 4][RT][4] (D a multiple
+// of 4 kEach), kEach neighbours of a row.
+template <typename T, int NT, int RT, int kEach, int kParts, bool kByRow, typename Place>
 __device__ __forceinline__ void join_sums(const AttnArgs& a, const float* first, int n, int rows, int tid,
                                           const Place& place) {
   const int64_t slot = RT * (a.D + 2);
-  const int vecs = a.D / 4;
-  for (int x0 = tid; x0 < rows * vecs; x0 += NT * kEach) {
-    int row[kEach], d[kEach];
+  const int vecs = a.D / 4, items = kByRow ? rows * vecs : rows * vecs / kEach;
+  for (int x0 = tid; x0 < items; x0 += kByRow ? NT * kEach : NT) {
+    int row[kEach], d[kEach], at[kEach];
     float4 o[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int x = min(x0 + i * NT, rows * vecs - 1);
-      row[i] = x / vecs;
-      d[i] = (x - row[i] * vecs) * 4;
+      if (kByRow) {
+        const int x = min(x0 + i * NT, rows * vecs - 1);
+        row[i] = x / vecs;
+        d[i] = (x - row[i] * vecs) * 4;
+        at[i] = row[i] * a.D + d[i];
+      } else {
+        const int g = x0 / rows;
+        row[i] = x0 - g * rows;
+        d[i] = (g * kEach + i) * 4;
+        at[i] = ((g * kEach + i) * RT + row[i]) * 4;
+      }
       o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int c0 = 0; c0 < n; c0 += kParts) {
@@ -289,7 +301,7 @@ __device__ __forceinline__ void join_sums(const AttnArgs& a, const float* first,
           const float* s = first + (c0 + c == 0 ? 0 : (2 * (c0 + c) - 1) * slot);
           const bool in = c0 + c < n;
           f[c][i] = in ? __ldcg(s + RT * a.D + row[i]) : 0.f;
-          v[c][i] = in ? __ldcg(reinterpret_cast<const float4*>(s + row[i] * a.D + d[i])) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[c][i] = in ? __ldcg(reinterpret_cast<const float4*>(s + at[i])) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
       for (int c = 0; c < kParts; ++c)
@@ -303,7 +315,7 @@ __device__ __forceinline__ void join_sums(const AttnArgs& a, const float* first,
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-      if (x0 + i * NT < rows * vecs) store4(static_cast<T*>(a.out) + place(row[i]) * a.D + d[i], o[i]);
+      if (!kByRow || x0 + i * NT < rows * vecs) store4(static_cast<T*>(a.out) + place(row[i]) * a.D + d[i], o[i]);
   }
 }
 
@@ -313,7 +325,7 @@ __device__ __forceinline__ void join_sums(const AttnArgs& a, const float* first,
 // thread a row where the parts are few, else a warp a row and a lane a part;
 // then the weighted sums.  Loads go out together in both: one after another,
 // two parts of 256 rows took 66 us.
-template <typename T, int NT, int RT>
+template <typename T, int NT, int RT, bool kByRow>
 __device__ void join_tile(const AttnArgs& a, const Walk& w, int cf, int cl, int tid, uint32_t bar) {
   const int rows = min(RT, w.q.n * a.group - w.r * RT), n = cl - cf + 1;
   const int64_t slot = RT * (a.D + 2);
@@ -362,9 +374,9 @@ __device__ void join_tile(const AttnArgs& a, const Walk& w, int cf, int cl, int 
   }
   ptx::named_barrier(bar, NT);
   if (n <= 4)
-    join_sums<T, NT, RT, 4, 2>(a, first, n, rows, tid, place);
+    join_sums<T, NT, RT, 4, 4, kByRow>(a, first, n, rows, tid, place);
   else
-    join_sums<T, NT, RT, 1, 8>(a, first, n, rows, tid, place);
+    join_sums<T, NT, RT, kByRow ? 1 : 4, kByRow ? 8 : 4, kByRow>(a, first, n, rows, tid, place);
 }
 
 }  // namespace at

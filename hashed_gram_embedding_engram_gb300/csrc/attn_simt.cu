@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
         }
       }
       const int cf = block_of(range, tile_u0), cl = block_of(range, tile_u0 + w.units - 1);
-      if (arrive_last<kNT>(a, cf, cl, &flag, tid, 1)) join_tile<T, kNT, RT>(a, w, cf, cl, tid, 1);
+      if (arrive_last<kNT>(a, cf, cl, &flag, tid, 1)) join_tile<T, kNT, RT, true>(a, w, cf, cl, tid, 1);
     }
     u = tile_u0 + ub;
     if (u >= range.u1) break;

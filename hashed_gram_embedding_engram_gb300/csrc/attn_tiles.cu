@@ -4,13 +4,17 @@
 //   S = Q K^T,  P = 2^(scale log2(e) S - m),  l = sum P,  O = P V
 //
 // A block has 256 rows (two tiles of 128) and takes 128 keys a step:
-//   warp 8      TMA: keys and values of a step into rings of their own, one
+//   warp 16     TMA: keys and values of a step into rings of their own, one
 //               box a page and 64 columns, 128-byte swizzle.
-//   warp 9      one elected lane issues tcgen05.mma: S = Q K^T (both operands
+//   warp 17     one elected lane issues tcgen05.mma: S = Q K^T (both operands
 //               from shared memory) and O += P V (P from TMEM, V as it lies in
 //               the cache, the head dimension contiguous: an MN-major operand).
-//   warps 0-3   softmax of tile 0, 4-7 of tile 1: one thread a row reads its
-//               128 scores from TMEM, writes its weights (bf16) over them.
+//   warps 0-7   softmax of tile 0, 8-15 of tile 1: two threads a row, 64 keys
+//               each, read the scores from TMEM and write the weights (bf16)
+//               over them.  One thread a row held 128 scores and took 1350 of a
+//               step's 2048 tensor clocks, more than the other tile's products
+//               hide; the two need one barrier a step, which also carries the
+//               vote on a new maximum.
 // While one tile's scores are in the softmax, the tensor core works on the
 // other's, so the two alternate: PV(0), S(0), PV(1), S(1), ...  TMEM is full:
 // two S/P tiles of 128 columns and two accumulators of D.
@@ -36,7 +40,8 @@ using namespace at;
 
 constexpr int kRT = 256;
 constexpr int kKT = 128;
-constexpr int kNT = 384;           // three warpgroups; warps 10 and 11 only round the third one up
+constexpr int kSoft = 512;         // softmax threads
+constexpr int kNT = kSoft + 128;   // warps 18 and 19 only round the last warpgroup up
 constexpr float kSlack = 8.f;      // powers of two a row's maximum may grow before O is rescaled
 
 template <int D>
@@ -57,6 +62,8 @@ struct Shared {
   int abort;
   int flag;
   Range range;
+  float top[2][2][128];      // [tile][half][row]: maxima of a step
+  float sum[2][2][2][128];   // [turn][tile][half][row]: weight totals of a tile
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -65,16 +72,32 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The 32 rows of a warp of tile t, from global memory to the swizzled tile.
+// Barrier `id` of a row's two warps with the OR of a predicate.
+__device__ __forceinline__ bool pair_any(uint32_t id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "setp.ne.b32 p, %2, 0;\n"
+      "barrier.cta.red.or.pred q, %1, 64, p;\n"
+      "selp.u32 %0, 1, 0, q;\n"
+      "}\n"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+
+// The 16 rows of a warp of tile t, from global memory to the swizzled tile.
 template <int D>
-__device__ __forceinline__ void load_queries(const AttnArgs& a, const Walk& w, uint8_t* tile, int t, int warp4,
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Walk& w, uint8_t* tile, int t, int warp8,
                                              int lane) {
   constexpr int kLanes = D / 8;             // 16-byte pieces of a row
   const int n_rows = w.q.n * a.group;
   const int piece = lane % kLanes;
-#pragma unroll 8
-  for (int i = 0; i < kLanes; ++i) {
-    const int row = warp4 * 32 + i * (32 / kLanes) + lane / kLanes;
+#pragma unroll
+  for (int i = 0; i < kLanes / 2; ++i) {
+    const int row = warp8 * 16 + i * (32 / kLanes) + lane / kLanes;
     const int rr = w.r * kRT + t * 128 + row;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (rr < n_rows)
@@ -109,9 +132,9 @@ __global__ void __launch_bounds__(kNT, 1)
       ptx::mbar_init(&sh.empty_v[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(&sh.q_full[t], 4);
+      ptx::mbar_init(&sh.q_full[t], 8);
       ptx::mbar_init(&sh.s_full[t], 1);
-      ptx::mbar_init(&sh.p_full[t], 4);
+      ptx::mbar_init(&sh.p_full[t], 8);
       ptx::mbar_init(&sh.o_full[t], 1);
     }
     ptx::mbar_init(&sh.drain, 1);
@@ -120,7 +143,7 @@ __global__ void __launch_bounds__(kNT, 1)
     ptx::tma_prefetch_desc(&map_k);
     ptx::tma_prefetch_desc(&map_v);
   }
-  if (warp == 9) {
+  if (warp == 17) {
     ptx::tmem_alloc(&sh.tmem, 512);
     ptx::tmem_relinquish();
   }
@@ -129,26 +152,29 @@ __global__ void __launch_bounds__(kNT, 1)
   ptx::tc_fence_before();
   find_range<kNT, kRT, kKT>(a, &sh.range);   // ends with a block barrier
   ptx::tc_fence_after();
-  const Range range = sh.range;
+  const Range& range = sh.range;
   const uint32_t tmem = sh.tmem;
 
   if (range.u0 < range.u1) {
     Walk w = walk_begin<kRT, kKT>(a, range);
     int64_t u = range.u0, tile_u0 = range.tile_u0;
-    // the block starts with 168 registers a thread (384 x 168 = 64512): the third warpgroup gives
-    // 96 of its own to the softmax warps, which hold a row of 128 scores (256 x 216 + 128 x 72 = 64512)
-    if (warp < 8) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // the block starts with 96 registers a thread (640 x 96 = 61440): the last warpgroup gives some of
+    // its own to the softmax warps, which hold 64 scores a thread (512 x 112 + 128 x 32 = 61440)
+    if (warp < 16) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
       // -------------------------------------------------------------- softmax
-      const int t = warp >> 2, warp4 = warp & 3;
-      const uint32_t ts = tmem + t * 128 + (static_cast<uint32_t>(warp4 * 32) << 16);
-      const uint32_t to = tmem + 256 + t * 128 + (static_cast<uint32_t>(warp4 * 32) << 16);
+      const int t = warp >> 3, half = (warp >> 2) & 1, warp4 = warp & 3;
+      const uint32_t quadrant = static_cast<uint32_t>(warp4 * 32) << 16;
+      const uint32_t ts = tmem + t * 128 + quadrant;
+      const uint32_t to = tmem + 256 + t * 128 + half * (D / 2) + quadrant;
+      const uint32_t pair = 2 + t * 4 + warp4;        // barrier of the two warps of these rows
+      int turn = 0;
       uint32_t sp = 0, op = 0;
       while (true) {
         const int ua = static_cast<int>(u - tile_u0);
         const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
         const int n_rows = w.q.n * a.group;
-        const int row = t * 128 + warp4 * 32 + lane, rr = w.r * kRT + row;
+        const int row = warp4 * 32 + lane, rr = w.r * kRT + t * 128 + row;
         const bool live = rr < n_rows;
         const bool work = w.k.hi > 0 && n_rows - w.r * kRT > t * 128;   // of the tile: same in all its warps
         const int p = w.q.len - w.q.n + rr / a.group;
@@ -156,7 +182,7 @@ __global__ void __launch_bounds__(kNT, 1)
         const int lo = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
         float m = -INFINITY, l = 0.f;
         if (work) {
-          load_queries<D>(a, w, sq + t * kTile, t, warp4, lane);
+          load_queries<D>(a, w, sq + t * kTile, t, warp & 7, lane);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.q_full[t]);
@@ -165,43 +191,50 @@ __global__ void __launch_bounds__(kNT, 1)
             wait_bounded(&sh.s_full[t], sp, &sh.abort, a.err);
             sp ^= 1;
             ptx::tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(ts + c * 32, s[c]);
+            uint32_t s[2][32];
+            ptx::tmem_ld_32x32b_x32(ts + half * 64, s[0]);
+            ptx::tmem_ld_32x32b_x32(ts + half * 64 + 32, s[1]);
             ptx::tmem_ld_wait();
-            if (__any_sync(~0u, j0 < lo || j0 + kKT > hi)) {
+            const int j1 = j0 + half * 64;
+            if (__any_sync(~0u, j1 < lo || j1 + 64 > hi)) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                  const int j = j0 + c * 32 + i;
+                  const int j = j1 + c * 32 + i;
                   if (j < lo || j >= hi) s[c][i] = 0xFF800000u;      // -inf
                 }
             }
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int i = 0; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(s[c][i]));
-            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
-            // m stays unless it is more than kSlack behind (or unset)
-            float f = 1.f;
-            if (top > m + kSlack || (m == -INFINITY && top > m)) {
-              f = ex2(m - top);
-              m = top;
-            }
-            if (un > ua && __any_sync(~0u, f != 1.f)) {
-              l *= f;
-              wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);   // the step before has been added
-              ptx::tc_fence_after();
+            float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
+            // both halves have read their scores here: the weights may go over them.  m stays unless a
+            // row of the two warps is more than kSlack ahead of it (or it is unset)
+            if (pair_any(pair, top > m + kSlack)) {
+              sh.top[t][half][row] = top;
+              ptx::named_barrier(pair, 64);
+              top = fmaxf(top, sh.top[t][half ^ 1][row]);
+              float f = 1.f;
+              if (top > m + kSlack) {
+                f = ex2(m - top);
+                m = top;
+              }
+              if (un > ua && __any_sync(~0u, f != 1.f)) {
+                l *= f;
+                wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);   // the step before has been added
+                ptx::tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                ptx::tmem_ld_32x32b_x32(to + c, o);
-                ptx::tmem_ld_wait();
+                for (int c = 0; c < D / 2; c += 32) {
+                  uint32_t o[32];
+                  ptx::tmem_ld_32x32b_x32(to + c, o);
+                  ptx::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                ptx::tmem_st_32x32b_x32(to + c, o);
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  ptx::tmem_st_32x32b_x32(to + c, o);
+                }
               }
             }
             op ^= 1;
@@ -209,18 +242,18 @@ __global__ void __launch_bounds__(kNT, 1)
             const F2 scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
             F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t pk[32];
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const uint32_t* x = &s[h * 2 + i / 16][(i % 16) * 2];
-                const float2 e = unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, base2));
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = unpack2(fma2(pack2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])),
+                                              scale2, base2));
                 const float2 p = make_float2(ex2(e.x), ex2(e.y));
                 sum[i & 1] = add2(sum[i & 1], pack2(p.x, p.y));
                 const __nv_bfloat162 b = __float22bfloat162_rn(p);
                 pk[i] = *reinterpret_cast<const uint32_t*>(&b);
               }
-              ptx::tmem_st_32x32b_x32(ts + h * 32, pk);
+              ptx::tmem_st_32x32b_x16(ts + half * 32 + c * 16, pk);
             }
             const float2 total = unpack2(add2(sum[0], sum[1]));
             l += total.x + total.y;
@@ -232,12 +265,16 @@ __global__ void __launch_bounds__(kNT, 1)
           wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);
           ptx::tc_fence_after();
         }
+        sh.sum[turn][t][half][row] = l;
+        ptx::named_barrier(pair, 64);
+        l = sh.sum[turn][t][0][row] + sh.sum[turn][t][1][row];
+        turn ^= 1;
         const bool whole = ua == 0 && ub == w.units;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t at = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
         float* part = part_slot<kRT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
           __syncwarp();
           if (work) {
@@ -248,7 +285,7 @@ __global__ void __launch_bounds__(kNT, 1)
             for (int i = 0; i < 32; ++i) o[i] = 0;
           }
           if (live && whole) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * D + c;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * D + half * (D / 2) + c;
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint32_t x[4];
@@ -263,22 +300,22 @@ __global__ void __launch_bounds__(kNT, 1)
           } else if (live) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part + row * D + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              *reinterpret_cast<uint4*>(part + ((half * (D / 2) + c + i) * (kRT / 4) + t * 128 + row) * 4) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
         __syncwarp();
         ptx::tc_fence_before();       // O is read: the next tile's first weights let it be overwritten
-        if (live) {
+        if (live && half == 0) {
           if (whole) {
             if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           } else {
-            part[kRT * D + row] = m;
-            part[kRT * D + kRT + row] = l;
+            part[kRT * D + t * 128 + row] = m;
+            part[kRT * D + kRT + t * 128 + row] = l;
           }
         }
         if (!whole) {
           const int cf = block_of(range, tile_u0), cl = block_of(range, tile_u0 + w.units - 1);
-          if (arrive_last<256>(a, cf, cl, &sh.flag, tid, 1)) join_tile<__nv_bfloat16, 256, kRT>(a, w, cf, cl, tid, 1);
+          if (arrive_last<kSoft>(a, cf, cl, &sh.flag, tid, 1)) join_tile<__nv_bfloat16, kSoft, kRT, false>(a, w, cf, cl, tid, 1);
         }
         u = tile_u0 + ub;
         if (u >= range.u1) break;
@@ -286,8 +323,8 @@ __global__ void __launch_bounds__(kNT, 1)
         walk_next<kRT, kKT>(a, w);
       }
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      if (warp == 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+      if (warp == 16) {
         // -------------------------------------------------------------- TMA
         int stage = 0, filled = 0;
         uint32_t phase = 0;
@@ -321,7 +358,7 @@ __global__ void __launch_bounds__(kNT, 1)
             drain_bounded(&sh.full_v[stage], phase);
           }
         }
-      } else if (warp == 9) {
+      } else if (warp == 17) {
         // -------------------------------------------------------------- MMA
         int ks = 0, vs = 0;                       // ring stages
         uint32_t kp = 0, vp = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
@@ -364,8 +401,16 @@ __global__ void __launch_bounds__(kNT, 1)
             next_k();
             for (int un = ua; un < ub; ++un) {
               for (int t = 0; t < nt; ++t) {
+                // one look at all that the two products need: the weights, the step's values and the next keys
+                const bool more = un + 1 < ub;
+                uint64_t* bar = &sh.p_full[t];
+                uint32_t parity = pp[t];
+                if (t == 0 && lane == 1) bar = &sh.full_v[vs], parity = vp;
+                if (t == 0 && lane == 2 && more) bar = &sh.full_k[ks], parity = kp;
+                wait_bounded(bar, parity, &sh.abort, a.err);
+                __syncwarp();
+                pp[t] ^= 1;
                 if (t == 0) {
-                  wait_bounded(&sh.full_v[vs], vp, &sh.abort, a.err);
                   const int j0 = (w.k.lo / kKT + un) * kKT;
                   if (j0 < w.k.lo || j0 + kKT > w.k.hi) {
                     zero_rows<kKT, D>(sv + vs * kTile, w.k.lo - j0, w.k.hi - j0, lane, 32);
@@ -373,8 +418,6 @@ __global__ void __launch_bounds__(kNT, 1)
                     __syncwarp();
                   }
                 }
-                wait_bounded(&sh.p_full[t], pp[t], &sh.abort, a.err);
-                pp[t] ^= 1;
                 ptx::tc_fence_after();
                 if (ptx::elect_one()) {
                   const uint32_t va = v_lo + vs * (kTile >> 4);
@@ -385,13 +428,7 @@ __global__ void __launch_bounds__(kNT, 1)
                   ptx::mma_commit(&sh.o_full[t]);
                 }
                 __syncwarp();
-                if (un + 1 < ub) {
-                  if (t == 0) {
-                    wait_bounded(&sh.full_k[ks], kp, &sh.abort, a.err);
-                    ptx::tc_fence_after();
-                  }
-                  scores(t);
-                }
+                if (more) scores(t);
               }
               if (ptx::elect_one()) ptx::mma_commit(&sh.empty_v[vs]);
               __syncwarp();
@@ -412,7 +449,7 @@ __global__ void __launch_bounds__(kNT, 1)
   }
 
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
