@@ -34,6 +34,7 @@ namespace {
 using namespace at;
 
 constexpr int kKT = 64;            // keys of a step
+constexpr int kCost = 2;           // steps that a tile's queries, output and joins are worth
 constexpr int kWarps = 4;          // compute warps
 constexpr int kNT = (kWarps + 1) * 32;
 constexpr int kPS = kKT + 8;       // bf16 a row of the weights: rows 144 bytes apart miss one another's banks
@@ -103,11 +104,11 @@ __global__ void __launch_bounds__(kNT, 2)
   }
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  find_range<kNT, RT, kKT>(a, &sh.range);   // ends with a block barrier
-  const Range range = sh.range;
-  if (range.u0 >= range.u1) return;
+  find_range<kNT, RT, kKT, kCost>(a, &sh.range);   // ends with a block barrier
+  const Range& range = sh.range;
+  if (range.places == 0) return;
   Walk w = walk_begin<RT, kKT>(a, range);
-  int64_t u = range.u0, tile_u0 = range.tile_u0;
+  int u = 0, at = range.at;
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- TMA
@@ -115,8 +116,8 @@ __global__ void __launch_bounds__(kNT, 2)
     uint32_t phase = 0;
     int filled = 0;
     while (true) {
-      const int ua = static_cast<int>(u - tile_u0);
-      const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+      const Piece piece = piece_of<kCost>(w, range, u, at);
+      const int ua = piece.a, ub = piece.b;
       if (w.k.hi > 0) {
         for (int un = ua; un < ub; ++un) {
           const int j0 = (w.k.lo / kKT + un) * kKT;
@@ -134,9 +135,9 @@ __global__ void __launch_bounds__(kNT, 2)
           if (++stage == kStages) stage = 0, phase ^= 1;
         }
       }
-      u = tile_u0 + ub;
-      if (u >= range.u1) break;
-      tile_u0 = u;
+      u = piece.next;
+      if (u >= range.places) break;
+      at = u;
       walk_next<RT, kKT>(a, w);
     }
     if (*reinterpret_cast<volatile int*>(&sh.abort)) {     // copies in flight land before the block ends
@@ -156,8 +157,9 @@ __global__ void __launch_bounds__(kNT, 2)
   int turn = 0;                                // of the double-buffered maxima and weights
   const int qr = lane >> 2, qc = (lane & 3) * 2;
   while (true) {
-    const int ua = static_cast<int>(u - tile_u0);
-    const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+    const Piece piece = piece_of<kCost>(w, range, u, at);
+    const int ua = piece.a, ub = piece.b;
+    if (ub > ua) {
     const int n_rows = w.q.n * a.group;
     const int r0 = w.r * RT;
     uint32_t qf[MT][NK][4];
@@ -310,16 +312,15 @@ __global__ void __launch_bounds__(kNT, 2)
         for (int x = 0; x < kWarps; ++x) total += s_sum[x][row];
         if (rr >= n_rows) continue;
         if (whole) {
-          const int64_t at =
-              (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
+          const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
           const float inv = total == 0.f ? 0.f : 1.f / total;
-          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at * D + warp * NC + qc;
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + to_row * D + warp * NC + qc;
 #pragma unroll
           for (int c = 0; c < NC / 8; ++c)
             *reinterpret_cast<__nv_bfloat162*>(to + c * 8) =
                 __floats2bfloat162_rn(o[t][c][e * 2] * inv, o[t][c][e * 2 + 1] * inv);
           if (warp == 0 && (lane & 3) == 0 && a.lse)
-            a.lse[at] = total == 0.f ? -INFINITY : (m[t][e] + log2f(total)) * kLn2;
+            a.lse[to_row] = total == 0.f ? -INFINITY : (m[t][e] + log2f(total)) * kLn2;
         } else {
           float* to = part + row * D + warp * NC + qc;
 #pragma unroll
@@ -332,15 +333,16 @@ __global__ void __launch_bounds__(kNT, 2)
         }
       }
     if (!whole) {
-      const int cf = block_of(range, tile_u0), cl = block_of(range, tile_u0 + w.units - 1);
+      const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
       if (arrive_last<kWarps * 32>(a, cf, cl, &sh.flag, tid, 1))
         join_tile<__nv_bfloat16, kWarps * 32, RT, true>(a, w, cf, cl, tid, 1);
     } else {
       ptx::named_barrier(1, kWarps * 32);          // s_sum is free for the next tile
     }
-    u = tile_u0 + ub;
-    if (u >= range.u1) break;
-    tile_u0 = u;
+    }
+    u = piece.next;
+    if (u >= range.places) break;
+    at = u;
     walk_next<RT, kKT>(a, w);
   }
 }

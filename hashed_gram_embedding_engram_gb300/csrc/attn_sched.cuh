@@ -9,7 +9,10 @@
 // form one line that is cut into equal ranges, one a block: ragged lengths,
 // few long sequences and many short ones balance by the same rule, and a
 // block works on at most one tile that it did not begin and one that it does
-// not end.  Such pieces are written as partials (rows relative to their own
+// not end.  Each tile is preceded in the line by `cost` places without work,
+// what its queries, its output and its joins take in steps: without them the
+// blocks that got many short tiles ended last (a chunk's by 10 %, ragged
+// drafts' by 20 %).  Such pieces are written as partials (rows relative to their own
 // maximum); the block that arrives last at the tile's counter joins them in
 // block order, so the result does not depend on the order of arrival.
 #pragma once
@@ -66,10 +69,11 @@ __device__ __forceinline__ int row_tiles(const Seq& q, int G) {
   return static_cast<int>((static_cast<int64_t>(q.n) * G + RT - 1) / RT);
 }
 
-// What a block works on: units [u0, u1) of U, beginning inside tile (b, h, r).
+// What a block works on: places [u0, u1) of U, beginning inside tile (b, h, r).
 struct Range {
-  int64_t u0, u1, U;
-  int64_t tile_u0;   // unit index of the tile's first step
+  int64_t u0, U;
+  int places;        // u1 - u0
+  int at;            // the tile's first place, from u0 (not positive)
   int C;             // blocks that have work
   int b, h, r;
 };
@@ -116,17 +120,33 @@ __device__ __forceinline__ void walk_next(const AttnArgs& a, Walk& w) {
   walk_tile<RT, KT>(a, w);
 }
 
+// The steps [a, b) of a tile that lie in a block's range (none: b <= a), the
+// places up to `next` being all of the tile or of the range.  Places are
+// counted from the range's begin here (u, at: of the tile) and have 31 bits.
+struct Piece {
+  int a, b, next;
+};
+
+template <int kCost>
+__device__ __forceinline__ Piece piece_of(const Walk& w, const Range& g, int u, int at) {
+  Piece p;
+  p.next = min(at + kCost + w.units, g.places);
+  p.a = max(u - at - kCost, 0);
+  p.b = p.next - at - kCost;
+  return p;
+}
+
 // All threads of the block (NT of them): the block's range.  Every block reads
 // all lengths; the sums are whole numbers, so all blocks agree.  A thread has a
 // sequence; one with several row tiles is summed by the lanes of its warp (as a
 // loop of the one thread, 64 tiles took 80 us).
-template <int NT, int RT, int KT>
+template <int NT, int RT, int KT, int kCost>
 __device__ void find_range(const AttnArgs& a, Range* out) {
   __shared__ int64_t warp_sum[NT / 32];
-  __shared__ int64_t rest;     // units before u0 in its sequence
+  __shared__ int64_t rest;     // places before u0 in its sequence and head
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto tile_units = [&](const Seq& q, int r) {
-    return units_of<KT>(key_range<RT>(q, a.group, r, a.causal, a.window));
+    return kCost + units_of<KT>(key_range<RT>(q, a.group, r, a.causal, a.window));
   };
   auto units_per_head = [&](int b, uint32_t* err) -> int64_t {
     Seq q{0, 0, 0};
@@ -177,7 +197,7 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
     out->U = U;
     out->C = C;
     out->u0 = u0;
-    out->u1 = u1;
+    out->places = static_cast<int>(u1 - u0);
   }
   if (u0 < u1) {
     int64_t before = 0;
@@ -211,7 +231,7 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
         const int64_t left = rest - at - (inc - n);
         if (left >= 0 && left < n) {       // one lane
           out->r = r0 + lane;
-          out->tile_u0 = u0 - left;
+          out->at = -static_cast<int>(left);
         }
         at += __shfl_sync(~0u, inc, 31);
       }
@@ -220,9 +240,19 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
   __syncthreads();
 }
 
-// Block that works on unit u.
+// Block that has place u.
 __device__ __forceinline__ int block_of(const Range& g, int64_t u) {
   return static_cast<int>(((u + 1) * g.C - 1) / g.U);
+}
+
+// First and last block with steps of the tile at place `at` of the range.
+template <int kCost>
+__device__ __forceinline__ int first_block(const Range& g, int at) {
+  return block_of(g, g.u0 + at + kCost);
+}
+template <int kCost>
+__device__ __forceinline__ int last_block(const Range& g, int at, const Walk& w) {
+  return block_of(g, g.u0 + at + kCost + w.units - 1);
 }
 
 // Partial tiles: slot 2c holds block c's piece of a tile that an earlier block

@@ -5,12 +5,16 @@
 //
 //   s = scale log2(e) q.k,  m = running max, l = sum 2^(s - m), o = sum 2^(s - m) v
 //
-// 256 threads hold an RT x 32 tile of scores: thread (ty, tx) has RT/16 rows
-// and the keys tx, tx + 16; the 16 threads of a row reduce its maximum and
-// total with shuffles and share its weights through shared memory.  Keys and
-// values are staged once a tile and read by all rows.  Work is divided and
-// joined as attn_sched.cuh says.  What bounds it: the FMA pipe on chunks
-// (RT = 64), device memory and the load latency on single tokens (RT = 16).
+// 256 threads hold an RT x 64 tile of scores (RT x 32 for heads of more than
+// 128): thread (ty, tx) has RT/16 rows and the keys tx, tx + 16, ..; the 16
+// threads of a row reduce its maximum and total with shuffles and share its
+// weights through shared memory.  Keys and values are staged once a tile and
+// read by all rows; a step's are on their way while the step before is worked
+// on.  Four rows by four keys a thread: with two keys the shared-memory reads
+// (8 cycles of them for 32 products a warp, four warps at a time) were the
+// bound.  Work is divided and joined as attn_sched.cuh says.  What bounds it:
+// the FMA pipe and the shared-memory reads on chunks (RT = 64), device memory
+// and the load latency on single tokens (RT = 16).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,7 +27,7 @@ namespace {
 using namespace at;
 
 constexpr int kNT = 256;
-constexpr int kKT = 32;
+constexpr int kCost = 2;           // steps that a tile's queries, output and joins are worth
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -34,12 +38,17 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 
 // DP: D padded to 64, 128 or 256 (the padding is zeros in shared memory).
 template <int DP, int RT>
-constexpr int simt_smem() {
-  return (RT * DP + kKT * (DP + 4) + kKT * DP + RT * kKT) * 4;
-}
+struct Cfg {
+  static constexpr int kKT = DP == 256 ? 32 : 64;      // keys of a step
+  static constexpr int kVecs = kKT * (DP / 4) / kNT;   // 4-element vectors of keys (and of values) a thread stages
+  static constexpr int kSmem = (RT * DP + kKT * (DP + 4) + kKT * DP + RT * kKT) * 4;
+};
 
 template <typename T, int DP, int RT>
 __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int kKT = Cfg<DP, RT>::kKT;
+  constexpr int kVecs = Cfg<DP, RT>::kVecs;
+  constexpr int K = kKT / 16;       // keys of a thread
   constexpr int R = RT / 16;        // rows of a thread
   constexpr int CV = DP / 64;       // 4-column groups of a thread
   constexpr int KS = DP + 4;        // key row stride: 8 rows in a quarter-warp's 16-byte loads miss one another's banks
@@ -53,14 +62,15 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  find_range<kNT, RT, kKT>(a, &range);
-  if (range.u0 >= range.u1) return;
+  find_range<kNT, RT, kKT, kCost>(a, &range);
+  if (range.places == 0) return;
   Walk w = walk_begin<RT, kKT>(a, range);
-  int64_t u = range.u0, tile_u0 = range.tile_u0;
+  int u = 0, at = range.at;
 
   while (true) {
-    const int ua = static_cast<int>(u - tile_u0);
-    const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+    const Piece piece = piece_of<kCost>(w, range, u, at);
+    const int ua = piece.a, ub = piece.b;
+    if (ub > ua) {
     const int n_rows = w.q.n * a.group;
     const int r0 = w.r * RT;
     __syncthreads();
@@ -89,38 +99,52 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
         for (int e = 0; e < 4; ++e) o[k][c][e] = 0.f;
     }
 
-    for (int un = ua; un < ub; ++un) {
+    // a step's keys and values, on their way to the registers
+    float4 kr[kVecs], vr[kVecs];
+    auto fetch = [&](int un) {
       const int j0 = (w.k.lo / kKT + un) * kKT;
-      __syncthreads();
-      for (int x = tid; x < kKT * (DP / 4); x += kNT) {
-        const int key = x / (DP / 4), d = (x % (DP / 4)) * 4, j = j0 + key;
-        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int x = tid + i * kNT, key = x / (DP / 4), d = (x % (DP / 4)) * 4, j = j0 + key;
+        kr[i] = vr[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (j >= w.k.lo && j < w.k.hi && d < a.D) {
           const int pid = __ldg(a.seq.table + static_cast<int64_t>(w.b) * a.seq.table_pages + (j >> a.seq.page_shift));
           if (pid >= 0 && pid < a.pages) {
             const int64_t row = ((static_cast<int64_t>(pid) * a.heads_kv + w.h) << a.seq.page_shift) +
                                 (j & ((1 << a.seq.page_shift) - 1));
-            kv = load4(static_cast<const T*>(a.k) + row * a.D + d);
-            vv = load4(static_cast<const T*>(a.v) + row * a.D + d);
+            kr[i] = load4(static_cast<const T*>(a.k) + row * a.D + d);
+            vr[i] = load4(static_cast<const T*>(a.v) + row * a.D + d);
           } else {
             atomicOr(a.err, kErrIndexRange);
           }
         }
-        *reinterpret_cast<float4*>(Ks + key * KS + d) = kv;
-        *reinterpret_cast<float4*>(Vs + key * DP + d) = vv;
+      }
+    };
+    fetch(ua);
+    const bool any_row = r0 + (ty & ~1) * R < n_rows;     // of the warp: its 2 R rows follow one another
+    for (int un = ua; un < ub; ++un) {
+      const int j0 = (w.k.lo / kKT + un) * kKT;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int x = tid + i * kNT, key = x / (DP / 4), d = (x % (DP / 4)) * 4;
+        *reinterpret_cast<float4*>(Ks + key * KS + d) = kr[i];
+        *reinterpret_cast<float4*>(Vs + key * DP + d) = vr[i];
       }
       __syncthreads();
-      float s[R][2] = {};
-#pragma unroll 4
+      if (un + 1 < ub) fetch(un + 1);
+      if (!any_row) continue;
+      float s[R][K] = {};
+#pragma unroll 2
       for (int d = 0; d < DP; d += 4) {
-        float4 kk[2];
+        float4 kk[K];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) kk[i] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * i) * KS + d);
+        for (int i = 0; i < K; ++i) kk[i] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * i) * KS + d);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
           const float4 q = *reinterpret_cast<const float4*>(Qs + (ty * R + k) * DP + d);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < K; ++i) {
             s[k][i] = fmaf(q.x, kk[i].x, s[k][i]);
             s[k][i] = fmaf(q.y, kk[i].y, s[k][i]);
             s[k][i] = fmaf(q.z, kk[i].z, s[k][i]);
@@ -132,7 +156,7 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
       for (int k = 0; k < R; ++k) {
         float top = m[k];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < K; ++i) {
           const int j = j0 + tx + 16 * i;
           s[k][i] = j >= lo[k] && j < hi[k] ? s[k][i] * a.scale_log2 : -INFINITY;
           top = fmaxf(top, s[k][i]);
@@ -144,7 +168,7 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
         m[k] = top;
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < K; ++i) {
           const float p = exp2f(s[k][i] - base);
           sum += p;
           Ps[(ty * R + k) * kKT + tx + 16 * i] = p;
@@ -188,16 +212,16 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
       for (int k = 0; k < R; ++k) {
         const int rr = r0 + ty * R + k;
         if (rr >= n_rows) continue;
-        const int64_t at = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
+        const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
         const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
 #pragma unroll
         for (int c = 0; c < CV; ++c) {
           const int d = c * 64 + tx * 4;
           if (d < a.D)
-            store4(static_cast<T*>(a.out) + at * a.D + d,
+            store4(static_cast<T*>(a.out) + to_row * a.D + d,
                    make_float4(o[k][c][0] * inv, o[k][c][1] * inv, o[k][c][2] * inv, o[k][c][3] * inv));
         }
-        if (tx == 0 && a.lse) a.lse[at] = l[k] == 0.f ? -INFINITY : (m[k] + log2f(l[k])) * kLn2;
+        if (tx == 0 && a.lse) a.lse[to_row] = l[k] == 0.f ? -INFINITY : (m[k] + log2f(l[k])) * kLn2;
       }
     } else {
       float* part = part_slot<RT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
@@ -214,19 +238,20 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
           part[RT * a.D + RT + row] = l[k];
         }
       }
-      const int cf = block_of(range, tile_u0), cl = block_of(range, tile_u0 + w.units - 1);
+      const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
       if (arrive_last<kNT>(a, cf, cl, &flag, tid, 1)) join_tile<T, kNT, RT, true>(a, w, cf, cl, tid, 1);
     }
-    u = tile_u0 + ub;
-    if (u >= range.u1) break;
-    tile_u0 = u;
+    }
+    u = piece.next;
+    if (u >= range.places) break;
+    at = u;
     walk_next<RT, kKT>(a, w);
   }
 }
 
 template <typename T, int DP, int RT>
 cudaError_t run(const engram_attn_plan* p, const AttnArgs& a, cudaStream_t s) {
-  constexpr int smem = simt_smem<DP, RT>();
+  constexpr int smem = Cfg<DP, RT>::kSmem;
   static int per_sm = 0;      // per template instance; idempotent if raced
   if (per_sm == 0) {
     cudaError_t e =

@@ -40,6 +40,7 @@ using namespace at;
 
 constexpr int kRT = 256;
 constexpr int kKT = 128;
+constexpr int kCost = 5;           // steps that a tile's queries, output and joins are worth
 constexpr int kSoft = 512;         // softmax threads
 constexpr int kNT = kSoft + 128;   // warps 18 and 19 only round the last warpgroup up
 constexpr float kSlack = 8.f;      // powers of two a row's maximum may grow before O is rescaled
@@ -150,14 +151,14 @@ __global__ void __launch_bounds__(kNT, 1)
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   ptx::tc_fence_before();
-  find_range<kNT, kRT, kKT>(a, &sh.range);   // ends with a block barrier
+  find_range<kNT, kRT, kKT, kCost>(a, &sh.range);   // ends with a block barrier
   ptx::tc_fence_after();
   const Range& range = sh.range;
   const uint32_t tmem = sh.tmem;
 
-  if (range.u0 < range.u1) {
+  if (range.places > 0) {
     Walk w = walk_begin<kRT, kKT>(a, range);
-    int64_t u = range.u0, tile_u0 = range.tile_u0;
+    int u = 0, at = range.at;
     // the block starts with 96 registers a thread (640 x 96 = 61440): the last warpgroup gives some of
     // its own to the softmax warps, which hold 64 scores a thread (512 x 112 + 128 x 32 = 61440)
     if (warp < 16) {
@@ -171,8 +172,9 @@ __global__ void __launch_bounds__(kNT, 1)
       int turn = 0;
       uint32_t sp = 0, op = 0;
       while (true) {
-        const int ua = static_cast<int>(u - tile_u0);
-        const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+        const Piece piece = piece_of<kCost>(w, range, u, at);
+        const int ua = piece.a, ub = piece.b;
+        if (ub > ua) {
         const int n_rows = w.q.n * a.group;
         const int row = warp4 * 32 + lane, rr = w.r * kRT + t * 128 + row;
         const bool live = rr < n_rows;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kNT, 1)
         turn ^= 1;
         const bool whole = ua == 0 && ub == w.units;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t at = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
+        const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
         float* part = part_slot<kRT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kNT, 1)
             for (int i = 0; i < 32; ++i) o[i] = 0;
           }
           if (live && whole) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * D + half * (D / 2) + c;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + to_row * D + half * (D / 2) + c;
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint32_t x[4];
@@ -307,19 +309,20 @@ __global__ void __launch_bounds__(kNT, 1)
         ptx::tc_fence_before();       // O is read: the next tile's first weights let it be overwritten
         if (live && half == 0) {
           if (whole) {
-            if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (a.lse) a.lse[to_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           } else {
             part[kRT * D + t * 128 + row] = m;
             part[kRT * D + kRT + t * 128 + row] = l;
           }
         }
         if (!whole) {
-          const int cf = block_of(range, tile_u0), cl = block_of(range, tile_u0 + w.units - 1);
+          const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
           if (arrive_last<kSoft>(a, cf, cl, &sh.flag, tid, 1)) join_tile<__nv_bfloat16, kSoft, kRT, false>(a, w, cf, cl, tid, 1);
         }
-        u = tile_u0 + ub;
-        if (u >= range.u1) break;
-        tile_u0 = u;
+        }
+        u = piece.next;
+        if (u >= range.places) break;
+        at = u;
         walk_next<kRT, kKT>(a, w);
       }
     } else {
@@ -329,8 +332,8 @@ __global__ void __launch_bounds__(kNT, 1)
         int stage = 0, filled = 0;
         uint32_t phase = 0;
         while (true) {
-          const int ua = static_cast<int>(u - tile_u0);
-          const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
+          const Piece piece = piece_of<kCost>(w, range, u, at);
+          const int ua = piece.a, ub = piece.b;
           for (int un = ua; un < ub && w.k.hi > 0; ++un) {
             const int j0 = (w.k.lo / kKT + un) * kKT;
             const int32_t row = page_row<kKT>(a, w, j0, lane);
@@ -345,9 +348,9 @@ __global__ void __launch_bounds__(kNT, 1)
             if (filled < kStages) ++filled;
             if (++stage == kStages) stage = 0, phase ^= 1;
           }
-          u = tile_u0 + ub;
-          if (u >= range.u1) break;
-          tile_u0 = u;
+          u = piece.next;
+          if (u >= range.places) break;
+          at = u;
           walk_next<kRT, kKT>(a, w);
         }
         if (*reinterpret_cast<volatile int*>(&sh.abort)) {     // copies in flight land before the block ends
@@ -387,9 +390,9 @@ __global__ void __launch_bounds__(kNT, 1)
           if (++ks == kStages) ks = 0, kp ^= 1;
         };
         while (true) {
-          const int ua = static_cast<int>(u - tile_u0);
-          const int ub = static_cast<int>(min(static_cast<int64_t>(w.units), range.u1 - tile_u0));
-          if (w.k.hi > 0) {
+          const Piece piece = piece_of<kCost>(w, range, u, at);
+          const int ua = piece.a, ub = piece.b;
+          if (w.k.hi > 0 && ub > ua) {
             const int nt = w.q.n * a.group - w.r * kRT > 128 ? 2 : 1;
             for (int t = 0; t < nt; ++t) {
               wait_bounded(&sh.q_full[t], qp[t], &sh.abort, a.err);
@@ -436,9 +439,9 @@ __global__ void __launch_bounds__(kNT, 1)
               if (un + 1 < ub) next_k();
             }
           }
-          u = tile_u0 + ub;
-          if (u >= range.u1) break;
-          tile_u0 = u;
+          u = piece.next;
+          if (u >= range.places) break;
+          at = u;
           walk_next<kRT, kKT>(a, w);
         }
         if (ptx::elect_one()) ptx::mma_commit(&sh.drain);
