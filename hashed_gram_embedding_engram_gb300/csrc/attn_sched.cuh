@@ -72,6 +72,7 @@ __device__ __forceinline__ int row_tiles(const Seq& q, int G) {
 // What a block works on: places [u0, u1) of U, beginning inside tile (b, h, r).
 struct Range {
   int64_t u0, U;
+  unsigned each, extra;   // U / C, U % C (where U has 31 bits)
   int places;        // u1 - u0
   int at;            // the tile's first place, from u0 (not positive)
   int C;             // blocks that have work
@@ -166,6 +167,12 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
     return n;
   };
   auto scan = [&](int64_t v, int64_t& total) -> int64_t {   // inclusive, over the block
+    if (a.seq.B == 1) {                      // the one sequence is thread 0's
+      if (tid == 0) warp_sum[0] = v;
+      __syncthreads();
+      total = warp_sum[0];
+      return total;
+    }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t t = __shfl_up_sync(~0u, v, o);
@@ -192,8 +199,23 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
   }
   const int C = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));
   const int c = blockIdx.x;
-  const int64_t u0 = c < C ? c * U / C : 0, u1 = c < C ? (c + 1) * U / C : 0;
+  const bool small = U < 0x7FFFFFFF;       // quotients in 32 bits (see block_of)
+  int64_t u0 = 0, u1 = 0;
+  unsigned each = 0, extra = 0;
+  if (c < C) {
+    if (small) {
+      each = static_cast<unsigned>(U) / static_cast<unsigned>(C);
+      extra = static_cast<unsigned>(U) - each * static_cast<unsigned>(C);
+      u0 = c * each + c * extra / static_cast<unsigned>(C);
+      u1 = (c + 1) * each + (c + 1) * extra / static_cast<unsigned>(C);
+    } else {
+      u0 = c * U / C;
+      u1 = (c + 1) * U / C;
+    }
+  }
   if (tid == 0) {
+    out->each = each;
+    out->extra = extra;
     out->U = U;
     out->C = C;
     out->u0 = u0;
@@ -208,10 +230,18 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
         upto = scan(mine, total);
       }
       if (before + upto - mine <= u0 && u0 < before + upto) {   // one thread: sequence base + tid
-        const int64_t in = u0 - (before + upto - mine), per = mine / a.heads_kv;
+        const int64_t in = u0 - (before + upto - mine);
         out->b = base + tid;
-        out->h = static_cast<int>(in / per);
-        rest = in % per;
+        if (small) {
+          const unsigned per = static_cast<unsigned>(mine) / static_cast<unsigned>(a.heads_kv);
+          const unsigned h = static_cast<unsigned>(in) / per;
+          out->h = static_cast<int>(h);
+          rest = static_cast<unsigned>(in) - h * per;
+        } else {
+          const int64_t per = mine / a.heads_kv;
+          out->h = static_cast<int>(in / per);
+          rest = in % per;
+        }
       }
       before += total;
     }
@@ -220,7 +250,11 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
       const Seq q = load_seq(a.seq, out->b, nullptr);
       const int tiles = row_tiles<RT>(q, a.group);
       int64_t at = 0;
-      for (int r0 = 0; r0 < tiles; r0 += 32) {
+      if (tiles == 1 && lane == 0) {
+        out->r = 0;
+        out->at = -static_cast<int>(rest);
+      }
+      for (int r0 = 0; r0 < tiles && tiles > 1; r0 += 32) {
         const int64_t n = r0 + lane < tiles ? tile_units(q, r0 + lane) : 0;
         int64_t inc = n;
 #pragma unroll
@@ -240,9 +274,18 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
   __syncthreads();
 }
 
-// Block that has place u.
+// Block that has place u: the c with floor(cU / C) <= u < floor((c + 1)U / C).
+// A 64-bit quotient is a chain of some 700 clocks, so where U has 31 bits (all
+// but absurd calls) an estimate in float is put right by whole-number compares.
 __device__ __forceinline__ int block_of(const Range& g, int64_t u) {
-  return static_cast<int>(((u + 1) * g.C - 1) / g.U);
+  if (g.U >= 0x7FFFFFFF) return static_cast<int>(((u + 1) * g.C - 1) / g.U);
+  auto begin = [&](unsigned c) { return c * g.each + c * g.extra / static_cast<unsigned>(g.C); };
+  const unsigned x = static_cast<unsigned>(u);
+  unsigned c = min(static_cast<unsigned>(__fdividef(static_cast<float>(x) * g.C, static_cast<float>(g.U))),
+                   static_cast<unsigned>(g.C - 1));
+  while (c + 1 < g.C && begin(c + 1) <= x) ++c;
+  while (c > 0 && begin(c) > x) --c;
+  return static_cast<int>(c);
 }
 
 // First and last block with steps of the tile at place `at` of the range.

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kNT = 128;
 constexpr int kMaxRounds = 16;
-constexpr int kBlocksPerSm = 6;
+constexpr int kBlocksPerSm = 32;
 
 // Two runs of four elements as they lie in memory, and as pairs of floats.
 template <typename T>
@@ -258,8 +258,9 @@ cudaError_t run(const RopeArgs& a, bool adjacent, int num_sms, cudaStream_t s) {
   constexpr int kGroups = kNT / LG;
   const int64_t q = a.q.ptr ? static_cast<int64_t>(a.tokens) * a.heads : 0;
   const int64_t k = a.k.ptr ? static_cast<int64_t>(a.tokens) * a.heads_kv : 0, v = a.k_pages ? k : 0;
-  // heads of a group: one while that leaves the SMs less than kBlocksPerSm blocks each, then more,
-  // so that the chain of loads that finds the places is paid for several at once
+  // heads of a group: one while that gives the SMs up to kBlocksPerSm blocks each (four waves of 8:
+  // with 6 blocks an SM the last, short wave took 16k fp32 tokens from 31 to 37 us), then more, so
+  // that the chain of loads that finds the places is paid for several at once
   int64_t rounds = (q + k + v) / (static_cast<int64_t>(kGroups) * num_sms * kBlocksPerSm);
   rounds = rounds < 1 ? 1 : (rounds > kMaxRounds ? kMaxRounds : rounds);
   const auto blocks = [&](int64_t n) { return (n + rounds * kGroups - 1) / (rounds * kGroups); };
