@@ -447,9 +447,9 @@ __device__ void join_tile(const AttnArgs& a, const Walk& w, int cf, int cl, int 
   }
   ptx::named_barrier(bar, NT);
   if (n <= 4)
-    join_sums<T, NT, RT, 4, 4, kByRow>(a, first, n, rows, tid, place);
+    join_sums<T, NT, RT, 4, kByRow ? 4 : 2, kByRow>(a, first, n, rows, tid, place);
   else
-    join_sums<T, NT, RT, kByRow ? 1 : 4, kByRow ? 8 : 4, kByRow>(a, first, n, rows, tid, place);
+    join_sums<T, NT, RT, kByRow ? 1 : 4, kByRow ? 8 : 2, kByRow>(a, first, n, rows, tid, place);
 }
 
 }  // namespace at

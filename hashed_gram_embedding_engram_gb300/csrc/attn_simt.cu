@@ -45,7 +45,7 @@ struct Cfg {
 };
 
 template <typename T, int DP, int RT>
-__global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 : 1) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kKT = Cfg<DP, RT>::kKT;
   constexpr int kVecs = Cfg<DP, RT>::kVecs;
   constexpr int K = kKT / 16;       // keys of a thread
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
       if (un + 1 < ub) fetch(un + 1);
       if (!any_row) continue;
       float s[R][K] = {};
-#pragma unroll 2
+#pragma unroll 8
       for (int d = 0; d < DP; d += 4) {
         float4 kk[K];
 #pragma unroll
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kNT) attn_simt_kernel(const __grid_constant__ 
           for (int e = 0; e < 4; ++e) o[k][c][e] *= f;
       }
       __syncwarp();                  // a row's weights are written and read by one half-warp
-#pragma unroll 2
+#pragma unroll 4
       for (int j = 0; j < kKT; j += 4) {
         float4 p[R];
 #pragma unroll

@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kNT, 1)
         const int lo = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
         float m = -INFINITY, l = 0.f;
         if (work) {
+          ptx::named_barrier(10 + t, 256);       // the tile's warps have read their output from here
           load_queries<D>(a, w, sq + t * kTile, t, warp & 7, lane);
           ptx::fence_proxy_async_smem();
           __syncwarp();
@@ -275,6 +276,9 @@ __global__ void __launch_bounds__(kNT, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
         float* part = part_slot<kRT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
+        // the warp's output passes through its share of the tile's queries, which are done with
+        constexpr int kChunks = D / 16;
+        uint8_t* stage = sq + t * kTile + (warp & 7) * (32 * D);
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
@@ -286,8 +290,7 @@ __global__ void __launch_bounds__(kNT, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0;
           }
-          if (live && whole) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + to_row * D + half * (D / 2) + c;
+          if (whole) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint32_t x[4];
@@ -297,7 +300,8 @@ __global__ void __launch_bounds__(kNT, 1)
                                                                __uint_as_float(o[i + 2 * k + 1]) * inv);
                 x[k] = *reinterpret_cast<const uint32_t*>(&b);
               }
-              *reinterpret_cast<uint4*>(out + i) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(stage + lane * D + ((((c + i) >> 3) ^ (lane & (kChunks - 1))) << 4)) =
+                  make_uint4(x[0], x[1], x[2], x[3]);
             }
           } else if (live) {
 #pragma unroll
@@ -306,6 +310,17 @@ __global__ void __launch_bounds__(kNT, 1)
           }
         }
         __syncwarp();
+        if (whole) {                  // whole rows of 128 (or 64) bytes, not 16 of each lane's row
+#pragma unroll 4
+          for (int i = 0; i < kChunks; ++i) {
+            const int x = i * 32 + lane, r = x / kChunks, q = x % kChunks;
+            const int to_r = __shfl_sync(~0u, static_cast<int>(to_row), r);
+            if (w.r * kRT + t * 128 + warp4 * 32 + r < n_rows)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<int64_t>(to_r) * D +
+                                        half * (D / 2) + q * 8) =
+                  *reinterpret_cast<const uint4*>(stage + r * D + ((q ^ (r & (kChunks - 1))) << 4));
+          }
+        }
         ptx::tc_fence_before();       // O is read: the next tile's first weights let it be overwritten
         if (live && half == 0) {
           if (whole) {
