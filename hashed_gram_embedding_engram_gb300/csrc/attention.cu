@@ -248,6 +248,7 @@ engram_status_t engram_paged_attention(const engram_kv_cache_t* cache, const eng
   a.heads = plan->cfg.heads;
   a.heads_kv = plan->cfg.heads_kv;
   a.group = plan->group;
+  a.group_recip = (65536 + plan->group - 1) / plan->group;
   a.D = plan->cfg.head_dim;
   a.causal = causal != 0;
   a.window = window;

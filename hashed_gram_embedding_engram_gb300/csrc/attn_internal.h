@@ -76,6 +76,7 @@ struct AttnArgs {
   float* lse;                 // [tokens, heads] or null
   SeqArgs seq;
   int heads, heads_kv, group, D;
+  int group_recip;            // ceil(2^16 / group)
   int causal, window;
   float scale_log2;           // scale * log2(e): scores in powers of two
   uint32_t* counters;         // kAttnCounters words, zero between calls

@@ -69,6 +69,23 @@ __device__ __forceinline__ int row_tiles(const Seq& q, int G) {
   return static_cast<int>((static_cast<int64_t>(q.n) * G + RT - 1) / RT);
 }
 
+// New token and head of the group of rows base, base + 1, .. base + 127: one
+// division for all of them.  x floor(2^16 / G + 1) >> 16 is x / G for x < 256
+// and G <= 128 (the excess, below x / 2^16, is less than 1 / G).
+struct RowMap {
+  int token, g;
+};
+
+__device__ __forceinline__ RowMap row_map(const AttnArgs& a, int base) {
+  const int token = base / a.group;
+  return {token, base - token * a.group};
+}
+
+__device__ __forceinline__ RowMap row_at(const AttnArgs& a, const RowMap& m, int offset) {
+  const int x = m.g + offset, n = x * a.group_recip >> 16;
+  return {m.token + n, x - n * a.group};
+}
+
 // What a block works on: places [u0, u1) of U, beginning inside tile (b, h, r).
 struct Range {
   int64_t u0, U;

@@ -96,16 +96,22 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Walk& w, u
   constexpr int kLanes = D / 8;             // 16-byte pieces of a row
   const int n_rows = w.q.n * a.group;
   const int piece = lane % kLanes;
+  const int base = w.r * kRT + t * 128 + warp8 * 16;
+  const RowMap map = row_map(a, base);
+  const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q.ptr) + w.q.row0 * a.q.ts +
+                              static_cast<int64_t>(w.h * a.group) * a.q.hs + piece * 8;
+  uint4 x[kLanes / 2];                      // all on their way before the first is stored
+#pragma unroll
+  for (int i = 0; i < kLanes / 2; ++i) {
+    const int offset = i * (32 / kLanes) + lane / kLanes;
+    const RowMap at = row_at(a, map, offset);
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (base + offset < n_rows) x[i] = __ldg(reinterpret_cast<const uint4*>(from + at.token * a.q.ts + at.g * a.q.hs));
+  }
 #pragma unroll
   for (int i = 0; i < kLanes / 2; ++i) {
     const int row = warp8 * 16 + i * (32 / kLanes) + lane / kLanes;
-    const int rr = w.r * kRT + t * 128 + row;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (rr < n_rows)
-      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.ptr) +
-                                               (w.q.row0 + rr / a.group) * a.q.ts +
-                                               (w.h * a.group + rr % a.group) * a.q.hs + piece * 8));
-    *reinterpret_cast<uint4*>(tile + (piece >> 3) * (128 * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = x;
+    *reinterpret_cast<uint4*>(tile + (piece >> 3) * (128 * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = x[i];
   }
 }
 
@@ -179,7 +185,8 @@ __global__ void __launch_bounds__(kNT, 1)
         const int row = warp4 * 32 + lane, rr = w.r * kRT + t * 128 + row;
         const bool live = rr < n_rows;
         const bool work = w.k.hi > 0 && n_rows - w.r * kRT > t * 128;   // of the tile: same in all its warps
-        const int p = w.q.len - w.q.n + rr / a.group;
+        const RowMap at_row = row_at(a, row_map(a, w.r * kRT + t * 128 + warp4 * 32), lane);
+        const int p = w.q.len - w.q.n + at_row.token;
         const int hi = !live || p < 0 ? 0 : (a.causal ? p + 1 : w.q.len);
         const int lo = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
         float m = -INFINITY, l = 0.f;
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(kNT, 1)
         turn ^= 1;
         const bool whole = ua == 0 && ub == w.units;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
+        const int64_t to_row = (static_cast<int64_t>(w.q.row0) + at_row.token) * a.heads + w.h * a.group + at_row.g;
         float* part = part_slot<kRT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
         // the warp's output passes through its share of the tile's queries, which are done with
         constexpr int kChunks = D / 16;

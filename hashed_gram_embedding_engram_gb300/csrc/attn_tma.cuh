@@ -63,12 +63,17 @@ __device__ __forceinline__ void load_boxes(const AttnArgs& a, const CUtensorMap*
     if (lane < boxes) ptx::tma_load_2d_nohint(to + c * KT * 128 + lane * box * 128, map, bar, c * 64, row);
 }
 
-// Zero the rows of a loaded tile outside [lo, hi) (threads tid of n).
+// Zero the rows of a loaded tile outside [lo, hi) (threads tid of n): the first
+// lo and the last KT - hi of each block of 64 columns, which lie in a row.
 template <int KT, int D>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int lo, int hi, int tid, int n) {
-  for (int x = tid; x < KT * (D / 8); x += n) {
-    const int row = (x / 8) % KT;
-    if (row < lo || row >= hi) *reinterpret_cast<uint4*>(tile + x * 16) = make_uint4(0, 0, 0, 0);
+  const int after = min(max(hi, 0), KT);
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    uint4* block = reinterpret_cast<uint4*>(tile + c * KT * 128);
+    for (int x = tid; x < lo * 8; x += n) block[x] = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int x = after * 8 + tid; x < KT * 8; x += n) block[x] = make_uint4(0, 0, 0, 0);
   }
 }
 
