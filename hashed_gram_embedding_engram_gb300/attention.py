@@ -16,6 +16,7 @@ from . import _lib
 from .engram import _ACT_DTYPES, _dev, _stream
 
 _ROPE_STYLES = {"halves": 0, "adjacent": 1}
+_COUNTER_BYTES = 16384      # of a workspace, zero when it is new (engram_attn_workspace_bytes)
 
 # engram_heads_view_t and engram_sequences_t as bytes of the call's own: a step's calls take a few
 # microseconds on the device, so the front end must not take longer (a ctypes structure costs three times this)
@@ -95,10 +96,16 @@ class AttentionPlan:
 
     def new_workspace(self, device="cuda") -> torch.Tensor:
         """A workspace for attention calls; calls that may run at the same time need one each."""
-        return torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
+        ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+        ws[:_COUNTER_BYTES].zero_()
+        return ws
 
     def _workspace(self, stream: int) -> torch.Tensor:
-        """The plan's own workspace of a stream (calls on one stream run one after another)."""
+        """The plan's own workspace of a stream (calls on one stream run one after another).  A call
+        under capture gets one of its own, in the graph's memory and zeroed by every replay: replays
+        may run beside the stream's calls, and nothing of the capture has run yet when they do."""
+        if torch.cuda.is_current_stream_capturing():
+            return self.new_workspace()
         ws = self._workspaces.get(stream)
         if ws is None:
             ws = self._workspaces[stream] = self.new_workspace()
@@ -244,7 +251,8 @@ class PagedCache:
             lse = torch.empty(T, p.heads, dtype=torch.float32, device=q.device)
         s = _current_stream(p.device)
         if workspace is None:
-            ws_ptr, ws_bytes = p._workspace(s).data_ptr(), p.workspace_bytes
+            ws = p._workspace(s)
+            ws_ptr, ws_bytes = ws.data_ptr(), p.workspace_bytes
         else:
             ws_ptr, ws_bytes = _dev(workspace, "workspace", torch.uint8), workspace.numel()
         _lib.check(self._lib.engram_paged_attention(

@@ -84,7 +84,7 @@ struct AttnArgs {
   uint32_t* err;
 };
 
-constexpr int kAttnCounters = 4096;      // at least the blocks of any attention grid
+constexpr int kAttnCounters = 4096;      // at least the blocks of any attention grid (16384 bytes, as the header says)
 constexpr int kAttnPartRows = 256;       // rows of partial tiles per SM, twice (workspace bound)
 
 inline size_t attn_workspace_bytes(const engram_attn_plan* p) {

@@ -29,11 +29,18 @@ using namespace at;
 constexpr int kNT = 256;
 constexpr int kCost = 2;           // steps that a tile's queries, output and joins are worth
 
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+// Volatile: the loads of a step stay where they are issued, before the work on
+// the step before (as plain read-only loads the compiler may sink them past it).
+__device__ __forceinline__ float4 load4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.nc.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
+  uint32_t x, y;
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "l"(p));
+  return make_float4(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u), __uint_as_float(y << 16),
+                     __uint_as_float(y & 0xFFFF0000u));
 }
 
 // DP: D padded to 64, 128 or 256 (the padding is zeros in shared memory).
@@ -103,20 +110,30 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
     float4 kr[kVecs], vr[kVecs];
     auto fetch = [&](int un) {
       const int j0 = (w.k.lo / kKT + un) * kKT;
+      const int32_t* table = a.seq.table + static_cast<int64_t>(w.b) * a.seq.table_pages;
+      // all page ids first, then all rows: one after the other, each waited for its own page id
+      int pid[kVecs];
+      bool bad = false;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
-        const int x = tid + i * kNT, key = x / (DP / 4), d = (x % (DP / 4)) * 4, j = j0 + key;
+        const int j = j0 + (tid + i * kNT) / (DP / 4);
+        const bool in = j >= w.k.lo && j < w.k.hi;
+        pid[i] = in ? __ldg(table + (j >> a.seq.page_shift)) : -1;
+        if (in && (pid[i] < 0 || pid[i] >= a.pages)) {
+          bad = true;
+          pid[i] = -1;
+        }
+      }
+      if (bad) atomicOr(a.err, kErrIndexRange);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int x = tid + i * kNT, d = (x % (DP / 4)) * 4, j = j0 + x / (DP / 4);
+        const int64_t row = ((static_cast<int64_t>(pid[i]) * a.heads_kv + w.h) << a.seq.page_shift) +
+                            (j & ((1 << a.seq.page_shift) - 1));
         kr[i] = vr[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j >= w.k.lo && j < w.k.hi && d < a.D) {
-          const int pid = __ldg(a.seq.table + static_cast<int64_t>(w.b) * a.seq.table_pages + (j >> a.seq.page_shift));
-          if (pid >= 0 && pid < a.pages) {
-            const int64_t row = ((static_cast<int64_t>(pid) * a.heads_kv + w.h) << a.seq.page_shift) +
-                                (j & ((1 << a.seq.page_shift) - 1));
-            kr[i] = load4(static_cast<const T*>(a.k) + row * a.D + d);
-            vr[i] = load4(static_cast<const T*>(a.v) + row * a.D + d);
-          } else {
-            atomicOr(a.err, kErrIndexRange);
-          }
+        if (pid[i] >= 0 && d < a.D) {
+          kr[i] = load4(static_cast<const T*>(a.k) + row * a.D + d);
+          vr[i] = load4(static_cast<const T*>(a.v) + row * a.D + d);
         }
       }
     };

@@ -85,8 +85,8 @@ engram_status_t engram_attn_plan_destroy(engram_attn_plan_t* plan);
 engram_status_t engram_attn_get_error(const engram_attn_plan_t* plan, engram_stream_t stream, uint32_t* flags_out);
 
 /* Bytes of device workspace engram_paged_attention needs.  The caller zero-fills
- * it once when new; the calls leave it ready for the next one.  Calls that may
- * run at the same time need a workspace each. */
+ * its first 16384 bytes (counters) once when new; the calls leave them ready for
+ * the next one.  Calls that may run at the same time need a workspace each. */
 engram_status_t engram_attn_workspace_bytes(const engram_attn_plan_t* plan, size_t* bytes);
 
 /* A layer's cache over caller-owned device memory: keys and values, each dense

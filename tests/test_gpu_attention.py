@@ -587,3 +587,27 @@ def test_pages_outside_a_window_are_not_looked_at(hint):
     table[0, :(600 - 2 - 100) // 16] = 2 ** 30
     table[1, :(131 - 1 - 99) // 16] = -3
     c.check(*c.run())
+
+
+def test_capture_on_a_new_stream_leaves_its_later_calls_alone():
+    """The first call on a stream is captured; calls on that stream, before and between replays,
+    share nothing with the graph."""
+    c = Case(seed=16, new=(1, 1), length=(4000, 900), heads=8, heads_kv=2, D=128, page=32)
+    want = c.run()
+    torch.cuda.synchronize()
+    junk = torch.full((1 << 28,), 255, dtype=torch.uint8, device="cuda")     # what a new allocation may hold
+    del junk
+    out, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:2], device="cuda")
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        c.cache.attend(c.batch, c.q, out=out, lse=lse)
+    for _ in range(2):
+        with torch.cuda.stream(s):
+            got = c.cache.attend(c.batch, c.q)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
