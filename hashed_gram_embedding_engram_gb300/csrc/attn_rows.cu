@@ -160,185 +160,186 @@ __global__ void __launch_bounds__(kNT, 2)
     const Piece piece = piece_of<kCost>(w, range, u, at);
     const int ua = piece.a, ub = piece.b;
     if (ub > ua) {
-    const int n_rows = w.q.n * a.group;
-    const int r0 = w.r * RT;
-    uint32_t qf[MT][NK][4];
-    int lo[MT][2], hi[MT][2];
-    float m[MT][2], l[MT][2], o[MT][NC / 8][4];
+      const int n_rows = w.q.n * a.group;
+      const int r0 = w.r * RT;
+      uint32_t qf[MT][NK][4];
+      int lo[MT][2], hi[MT][2];
+      float m[MT][2], l[MT][2], o[MT][NC / 8][4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
+      for (int t = 0; t < MT; ++t) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = r0 + t * 16 + e * 8 + qr;
-        const bool live = rr < n_rows;
-        const int p = w.q.len - w.q.n + rr / a.group;
-        hi[t][e] = !live || p < 0 ? 0 : (a.causal ? p + 1 : w.q.len);
-        lo[t][e] = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
-        m[t][e] = -INFINITY;
-        l[t][e] = 0.f;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.ptr) + (w.q.row0 + rr / a.group) * a.q.ts +
-                                   (w.h * a.group + rr % a.group) * a.q.hs + qc;
+        for (int e = 0; e < 2; ++e) {
+          const int rr = r0 + t * 16 + e * 8 + qr;
+          const bool live = rr < n_rows;
+          const int p = w.q.len - w.q.n + rr / a.group;
+          hi[t][e] = !live || p < 0 ? 0 : (a.causal ? p + 1 : w.q.len);
+          lo[t][e] = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
+          m[t][e] = -INFINITY;
+          l[t][e] = 0.f;
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.ptr) + (w.q.row0 + rr / a.group) * a.q.ts +
+                                     (w.h * a.group + rr % a.group) * a.q.hs + qc;
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          qf[t][k][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16)) : 0u;
-          qf[t][k][2 + e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16 + 8)) : 0u;
+          for (int k = 0; k < NK; ++k) {
+            qf[t][k][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16)) : 0u;
+            qf[t][k][2 + e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16 + 8)) : 0u;
+          }
         }
+#pragma unroll
+        for (int c = 0; c < NC / 8; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][c][e] = 0.f;
       }
-#pragma unroll
-      for (int c = 0; c < NC / 8; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][c][e] = 0.f;
-    }
 
-    for (int un = ua; un < ub && w.k.hi > 0; ++un) {
-      const int j0 = (w.k.lo / kKT + un) * kKT;
-      const uint32_t kt = ptx::smem_u32(ring + stage * 2 * kTile), vt = kt + kTile;
-      // scores of keys 16 warp .. + 15
-      float s[MT][2][4] = {};
-      wait_bounded(&sh.full_k[stage], phase, &sh.abort, a.err);
-      {
-        const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t base = kt + key * 128;
-        const int sw = key & 7, c0 = (lane >> 3) & 1;
+      for (int un = ua; un < ub && w.k.hi > 0; ++un) {
+        const int j0 = (w.k.lo / kKT + un) * kKT;
+        const uint32_t kt = ptx::smem_u32(ring + stage * 2 * kTile), vt = kt + kTile;
+        // scores of keys 16 warp .. + 15
+        float s[MT][2][4] = {};
+        wait_bounded(&sh.full_k[stage], phase, &sh.abort, a.err);
+        {
+          const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+          const uint32_t base = kt + key * 128;
+          const int sw = key & 7, c0 = (lane >> 3) & 1;
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          uint32_t b[4];
-          const int chunk = (k * 2 + c0) & 7;
-          ldsm4(base + (k / 4) * kHalf + ((chunk ^ sw) << 4), b);
+          for (int k = 0; k < NK; ++k) {
+            uint32_t b[4];
+            const int chunk = (k * 2 + c0) & 7;
+            ldsm4(base + (k / 4) * kHalf + ((chunk ^ sw) << 4), b);
 #pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            mma16816(s[t][0], qf[t][k], b[0], b[1]);
-            mma16816(s[t][1], qf[t][k], b[2], b[3]);
-          }
-        }
-      }
-      // each row's maximum over the step
-      float top[MT][2];
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int j = j0 + warp * 16 + n * 8 + qc + i;
-              float& v = s[t][n][e * 2 + i];
-              v = j >= lo[t][e] && j < hi[t][e] ? v * a.scale_log2 : -INFINITY;
-              x = fmaxf(x, v);
+            for (int t = 0; t < MT; ++t) {
+              mma16816(s[t][0], qf[t][k], b[0], b[1]);
+              mma16816(s[t][1], qf[t][k], b[2], b[3]);
             }
-          x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-          if ((lane & 3) == 0) s_max[turn][warp][t * 16 + e * 8 + qr] = x;
-        }
-      ptx::named_barrier(1, kWarps * 32);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = t * 16 + e * 8 + qr;
-          top[t][e] = m[t][e];
-#pragma unroll
-          for (int x = 0; x < kWarps; ++x) top[t][e] = fmaxf(top[t][e], s_max[turn][x][row]);
-          const float base = top[t][e] == -INFINITY ? 0.f : top[t][e];
-          const float f = exp2f(m[t][e] - base);
-          m[t][e] = top[t][e];
-          float sum = 0.f;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = exp2f(s[t][n][e * 2] - base), p1 = exp2f(s[t][n][e * 2 + 1] - base);
-            sum += p0 + p1;
-            *reinterpret_cast<__nv_bfloat162*>(&s_p[turn][row * kPS + warp * 16 + n * 8 + qc]) =
-                __floats2bfloat162_rn(p0, p1);
-          }
-          l[t][e] = fmaf(l[t][e], f, sum);
-#pragma unroll
-          for (int c = 0; c < NC / 8; ++c) {
-            o[t][c][e * 2] *= f;
-            o[t][c][e * 2 + 1] *= f;
           }
         }
-      wait_bounded(&sh.full_v[stage], phase, &sh.abort, a.err);
-      const bool edge = j0 < w.k.lo || j0 + kKT > w.k.hi;
-      if (edge) zero_rows<kKT, D>(ring + stage * 2 * kTile + kTile, w.k.lo - j0, w.k.hi - j0, tid, kWarps * 32);
-      ptx::named_barrier(1, kWarps * 32);
-      // output columns NC warp .. + NC - 1
-#pragma unroll
-      for (int k = 0; k < kKT / 16; ++k) {
-        uint32_t pf[MT][4];
+        // each row's maximum over the step
+        float top[MT][2];
 #pragma unroll
         for (int t = 0; t < MT; ++t)
-          ldsm4(ptx::smem_u32(&s_p[turn][(t * 16 + (lane & 15)) * kPS + k * 16 + ((lane >> 4) << 3)]), pf[t]);
-        const int key = k * 16 + (lane & 15);
 #pragma unroll
-        for (int c = 0; c < NC / 16; ++c) {
-          uint32_t b[4];
-          const int col = warp * NC + c * 16 + ((lane >> 4) << 3);
-          ldsm4_t(vt + (col >> 6) * kHalf + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4), b);
+          for (int e = 0; e < 2; ++e) {
+            float x = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            mma16816(o[t][2 * c], pf[t], b[0], b[1]);
-            mma16816(o[t][2 * c + 1], pf[t], b[2], b[3]);
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int j = j0 + warp * 16 + n * 8 + qc + i;
+                float& v = s[t][n][e * 2 + i];
+                v = j >= lo[t][e] && j < hi[t][e] ? v * a.scale_log2 : -INFINITY;
+                x = fmaxf(x, v);
+              }
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+            if ((lane & 3) == 0) s_max[turn][warp][t * 16 + e * 8 + qr] = x;
+          }
+        ptx::named_barrier(1, kWarps * 32);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = t * 16 + e * 8 + qr;
+            top[t][e] = m[t][e];
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) top[t][e] = fmaxf(top[t][e], s_max[turn][x][row]);
+            const float base = top[t][e] == -INFINITY ? 0.f : top[t][e];
+            const float f = exp2f(m[t][e] - base);
+            m[t][e] = top[t][e];
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float p0 = exp2f(s[t][n][e * 2] - base), p1 = exp2f(s[t][n][e * 2 + 1] - base);
+              sum += p0 + p1;
+              *reinterpret_cast<__nv_bfloat162*>(&s_p[turn][row * kPS + warp * 16 + n * 8 + qc]) =
+                  __floats2bfloat162_rn(p0, p1);
+            }
+            l[t][e] = fmaf(l[t][e], f, sum);
+#pragma unroll
+            for (int c = 0; c < NC / 8; ++c) {
+              o[t][c][e * 2] *= f;
+              o[t][c][e * 2 + 1] *= f;
+            }
+          }
+        wait_bounded(&sh.full_v[stage], phase, &sh.abort, a.err);
+        const bool edge = j0 < w.k.lo || j0 + kKT > w.k.hi;
+        if (edge) zero_rows<kKT, D>(ring + stage * 2 * kTile + kTile, w.k.lo - j0, w.k.hi - j0, tid, kWarps * 32);
+        ptx::named_barrier(1, kWarps * 32);
+        // output columns NC warp .. + NC - 1
+#pragma unroll
+        for (int k = 0; k < kKT / 16; ++k) {
+          uint32_t pf[MT][4];
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+            ldsm4(ptx::smem_u32(&s_p[turn][(t * 16 + (lane & 15)) * kPS + k * 16 + ((lane >> 4) << 3)]), pf[t]);
+          const int key = k * 16 + (lane & 15);
+#pragma unroll
+          for (int c = 0; c < NC / 16; ++c) {
+            uint32_t b[4];
+            const int col = warp * NC + c * 16 + ((lane >> 4) << 3);
+            ldsm4_t(vt + (col >> 6) * kHalf + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4), b);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              mma16816(o[t][2 * c], pf[t], b[0], b[1]);
+              mma16816(o[t][2 * c + 1], pf[t], b[2], b[3]);
+            }
           }
         }
+        if (edge) ptx::fence_proxy_async_smem();     // the zeros, before the next copy into the stage
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.empty[stage]);
+        if (++stage == kStages) stage = 0, phase ^= 1;
+        turn ^= 1;
       }
-      if (edge) ptx::fence_proxy_async_smem();     // the zeros, before the next copy into the stage
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.empty[stage]);
-      if (++stage == kStages) stage = 0, phase ^= 1;
-      turn ^= 1;
-    }
 
-    // the rows' totals over the warps
+      // the rows' totals over the warps
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[t][e] += __shfl_xor_sync(~0u, l[t][e], 1);
-        l[t][e] += __shfl_xor_sync(~0u, l[t][e], 2);
-        if ((lane & 3) == 0) s_sum[warp][t * 16 + e * 8 + qr] = l[t][e];
-      }
-    ptx::named_barrier(1, kWarps * 32);
-    const bool whole = ua == 0 && ub == w.units;
-    float* part = part_slot<RT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
+        for (int e = 0; e < 2; ++e) {
+          l[t][e] += __shfl_xor_sync(~0u, l[t][e], 1);
+          l[t][e] += __shfl_xor_sync(~0u, l[t][e], 2);
+          if ((lane & 3) == 0) s_sum[warp][t * 16 + e * 8 + qr] = l[t][e];
+        }
+      ptx::named_barrier(1, kWarps * 32);
+      const bool whole = ua == 0 && ub == w.units;
+      float* part = part_slot<RT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = t * 16 + e * 8 + qr, rr = r0 + row;
-        float total = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          const int row = t * 16 + e * 8 + qr, rr = r0 + row;
+          float total = 0.f;
 #pragma unroll
-        for (int x = 0; x < kWarps; ++x) total += s_sum[x][row];
-        if (rr >= n_rows) continue;
-        if (whole) {
-          const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
-          const float inv = total == 0.f ? 0.f : 1.f / total;
-          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + to_row * D + warp * NC + qc;
+          for (int x = 0; x < kWarps; ++x) total += s_sum[x][row];
+          if (rr >= n_rows) continue;
+          if (whole) {
+            const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group +
+                                   rr % a.group;
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + to_row * D + warp * NC + qc;
 #pragma unroll
-          for (int c = 0; c < NC / 8; ++c)
-            *reinterpret_cast<__nv_bfloat162*>(to + c * 8) =
-                __floats2bfloat162_rn(o[t][c][e * 2] * inv, o[t][c][e * 2 + 1] * inv);
-          if (warp == 0 && (lane & 3) == 0 && a.lse)
-            a.lse[to_row] = total == 0.f ? -INFINITY : (m[t][e] + log2f(total)) * kLn2;
-        } else {
-          float* to = part + row * D + warp * NC + qc;
+            for (int c = 0; c < NC / 8; ++c)
+              *reinterpret_cast<__nv_bfloat162*>(to + c * 8) =
+                  __floats2bfloat162_rn(o[t][c][e * 2] * inv, o[t][c][e * 2 + 1] * inv);
+            if (warp == 0 && (lane & 3) == 0 && a.lse)
+              a.lse[to_row] = total == 0.f ? -INFINITY : (m[t][e] + log2f(total)) * kLn2;
+          } else {
+            float* to = part + row * D + warp * NC + qc;
 #pragma unroll
-          for (int c = 0; c < NC / 8; ++c)
-            *reinterpret_cast<float2*>(to + c * 8) = make_float2(o[t][c][e * 2], o[t][c][e * 2 + 1]);
-          if (warp == 0 && (lane & 3) == 0) {
-            part[RT * D + row] = m[t][e];
-            part[RT * D + RT + row] = total;
+            for (int c = 0; c < NC / 8; ++c)
+              *reinterpret_cast<float2*>(to + c * 8) = make_float2(o[t][c][e * 2], o[t][c][e * 2 + 1]);
+            if (warp == 0 && (lane & 3) == 0) {
+              part[RT * D + row] = m[t][e];
+              part[RT * D + RT + row] = total;
+            }
           }
         }
+      if (!whole) {
+        const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
+        if (arrive_last<kWarps * 32>(a, cf, cl, &sh.flag, tid, 1))
+          join_tile<__nv_bfloat16, kWarps * 32, RT, true>(a, w, cf, cl, tid, 1);
+      } else {
+        ptx::named_barrier(1, kWarps * 32);          // s_sum is free for the next tile
       }
-    if (!whole) {
-      const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
-      if (arrive_last<kWarps * 32>(a, cf, cl, &sh.flag, tid, 1))
-        join_tile<__nv_bfloat16, kWarps * 32, RT, true>(a, w, cf, cl, tid, 1);
-    } else {
-      ptx::named_barrier(1, kWarps * 32);          // s_sum is free for the next tile
-    }
     }
     u = piece.next;
     if (u >= range.places) break;

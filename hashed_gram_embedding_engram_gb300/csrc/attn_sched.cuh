@@ -33,7 +33,8 @@ struct Seq {
 };
 
 __device__ __forceinline__ Seq load_seq(const SeqArgs& s, int b, uint32_t* err) {
-  const int a0 = __ldg(s.start + b), a1 = __ldg(s.start + b + 1), len = __ldg(s.length + b);
+  const int a0 = ptx::ld_after_wait(s.start + b), a1 = ptx::ld_after_wait(s.start + b + 1);
+  const int len = ptx::ld_after_wait(s.length + b);
   Seq q;
   q.row0 = min(max(a0, 0), s.tokens);
   q.n = min(max(a1, q.row0), s.tokens) - q.row0;
@@ -454,7 +455,8 @@ __device__ void join_tile(const AttnArgs& a, const Walk& w, int cf, int cl, int 
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
       const float base = top == -INFINITY ? 0.f : top;
-      for (int c = lane; c < n; c += 32) total = fmaf(exp2f(__ldcg(stats(c, row)) - base), __ldcg(stats(c, row) + RT), total);
+      for (int c = lane; c < n; c += 32)
+        total = fmaf(exp2f(__ldcg(stats(c, row)) - base), __ldcg(stats(c, row) + RT), total);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
       const float inv = total == 0.f ? 0.f : 1.f / total;

@@ -52,7 +52,8 @@ struct Cfg {
 };
 
 template <typename T, int DP, int RT>
-__global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 : 1) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 : 1)
+    attn_simt_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kKT = Cfg<DP, RT>::kKT;
   constexpr int kVecs = Cfg<DP, RT>::kVecs;
   constexpr int K = kKT / 16;       // keys of a thread
@@ -78,186 +79,187 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
     const Piece piece = piece_of<kCost>(w, range, u, at);
     const int ua = piece.a, ub = piece.b;
     if (ub > ua) {
-    const int n_rows = w.q.n * a.group;
-    const int r0 = w.r * RT;
-    __syncthreads();
-    for (int x = tid; x < RT * (DP / 4); x += kNT) {
-      const int row = x / (DP / 4), d = (x % (DP / 4)) * 4, rr = r0 + row;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (rr < n_rows && d < a.D)
-        v = load4(static_cast<const T*>(a.q.ptr) + (w.q.row0 + rr / a.group) * a.q.ts +
-                  (w.h * a.group + rr % a.group) * a.q.hs + d);
-      *reinterpret_cast<float4*>(Qs + row * DP + d) = v;
-    }
-    int lo[R], hi[R];
-    float m[R], l[R], o[R][CV][4];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int rr = r0 + ty * R + k;
-      const int p = w.q.len - w.q.n + rr / a.group;
-      const bool sees = rr < n_rows && p >= 0;
-      hi[k] = !sees ? 0 : (a.causal ? p + 1 : w.q.len);
-      lo[k] = sees && a.window > 0 ? max(0, p - a.window + 1) : 0;
-      m[k] = -INFINITY;
-      l[k] = 0.f;
-#pragma unroll
-      for (int c = 0; c < CV; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[k][c][e] = 0.f;
-    }
-
-    // a step's keys and values, on their way to the registers
-    float4 kr[kVecs], vr[kVecs];
-    auto fetch = [&](int un) {
-      const int j0 = (w.k.lo / kKT + un) * kKT;
-      const int32_t* table = a.seq.table + static_cast<int64_t>(w.b) * a.seq.table_pages;
-      // all page ids first, then all rows: one after the other, each waited for its own page id
-      int pid[kVecs];
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int j = j0 + (tid + i * kNT) / (DP / 4);
-        const bool in = j >= w.k.lo && j < w.k.hi;
-        pid[i] = in ? __ldg(table + (j >> a.seq.page_shift)) : -1;
-        if (in && (pid[i] < 0 || pid[i] >= a.pages)) {
-          bad = true;
-          pid[i] = -1;
-        }
-      }
-      if (bad) atomicOr(a.err, kErrIndexRange);
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int x = tid + i * kNT, d = (x % (DP / 4)) * 4, j = j0 + x / (DP / 4);
-        const int64_t row = ((static_cast<int64_t>(pid[i]) * a.heads_kv + w.h) << a.seq.page_shift) +
-                            (j & ((1 << a.seq.page_shift) - 1));
-        kr[i] = vr[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (pid[i] >= 0 && d < a.D) {
-          kr[i] = load4(static_cast<const T*>(a.k) + row * a.D + d);
-          vr[i] = load4(static_cast<const T*>(a.v) + row * a.D + d);
-        }
-      }
-    };
-    fetch(ua);
-    const bool any_row = r0 + (ty & ~1) * R < n_rows;     // of the warp: its 2 R rows follow one another
-    for (int un = ua; un < ub; ++un) {
-      const int j0 = (w.k.lo / kKT + un) * kKT;
+      const int n_rows = w.q.n * a.group;
+      const int r0 = w.r * RT;
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int x = tid + i * kNT, key = x / (DP / 4), d = (x % (DP / 4)) * 4;
-        *reinterpret_cast<float4*>(Ks + key * KS + d) = kr[i];
-        *reinterpret_cast<float4*>(Vs + key * DP + d) = vr[i];
+      for (int x = tid; x < RT * (DP / 4); x += kNT) {
+        const int row = x / (DP / 4), d = (x % (DP / 4)) * 4, rr = r0 + row;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (rr < n_rows && d < a.D)
+          v = load4(static_cast<const T*>(a.q.ptr) + (w.q.row0 + rr / a.group) * a.q.ts +
+                    (w.h * a.group + rr % a.group) * a.q.hs + d);
+        *reinterpret_cast<float4*>(Qs + row * DP + d) = v;
       }
-      __syncthreads();
-      if (un + 1 < ub) fetch(un + 1);
-      if (!any_row) continue;
-      float s[R][K] = {};
-#pragma unroll 8
-      for (int d = 0; d < DP; d += 4) {
-        float4 kk[K];
-#pragma unroll
-        for (int i = 0; i < K; ++i) kk[i] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * i) * KS + d);
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-          const float4 q = *reinterpret_cast<const float4*>(Qs + (ty * R + k) * DP + d);
-#pragma unroll
-          for (int i = 0; i < K; ++i) {
-            s[k][i] = fmaf(q.x, kk[i].x, s[k][i]);
-            s[k][i] = fmaf(q.y, kk[i].y, s[k][i]);
-            s[k][i] = fmaf(q.z, kk[i].z, s[k][i]);
-            s[k][i] = fmaf(q.w, kk[i].w, s[k][i]);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        float top = m[k];
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-          const int j = j0 + tx + 16 * i;
-          s[k][i] = j >= lo[k] && j < hi[k] ? s[k][i] * a.scale_log2 : -INFINITY;
-          top = fmaxf(top, s[k][i]);
-        }
-#pragma unroll
-        for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-        const float base = top == -INFINITY ? 0.f : top;
-        const float f = exp2f(m[k] - base);
-        m[k] = top;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-          const float p = exp2f(s[k][i] - base);
-          sum += p;
-          Ps[(ty * R + k) * kKT + tx + 16 * i] = p;
-        }
-        l[k] = fmaf(l[k], f, sum);   // this thread's keys only: the row's total is summed at the end
-#pragma unroll
-        for (int c = 0; c < CV; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[k][c][e] *= f;
-      }
-      __syncwarp();                  // a row's weights are written and read by one half-warp
-#pragma unroll 4
-      for (int j = 0; j < kKT; j += 4) {
-        float4 p[R];
-#pragma unroll
-        for (int k = 0; k < R; ++k) p[k] = *reinterpret_cast<const float4*>(Ps + (ty * R + k) * kKT + j);
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-          for (int c = 0; c < CV; ++c) {
-            const float4 v = *reinterpret_cast<const float4*>(Vs + (j + jj) * DP + c * 64 + tx * 4);
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-              const float pk = jj == 0 ? p[k].x : (jj == 1 ? p[k].y : (jj == 2 ? p[k].z : p[k].w));
-              o[k][c][0] = fmaf(pk, v.x, o[k][c][0]);
-              o[k][c][1] = fmaf(pk, v.y, o[k][c][1]);
-              o[k][c][2] = fmaf(pk, v.z, o[k][c][2]);
-              o[k][c][3] = fmaf(pk, v.w, o[k][c][3]);
-            }
-          }
-      }
-    }
-
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) l[k] += __shfl_xor_sync(~0u, l[k], x);
-    const bool whole = ua == 0 && ub == w.units;
-    if (whole) {
+      int lo[R], hi[R];
+      float m[R], l[R], o[R][CV][4];
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         const int rr = r0 + ty * R + k;
-        if (rr >= n_rows) continue;
-        const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
-        const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
+        const int p = w.q.len - w.q.n + rr / a.group;
+        const bool sees = rr < n_rows && p >= 0;
+        hi[k] = !sees ? 0 : (a.causal ? p + 1 : w.q.len);
+        lo[k] = sees && a.window > 0 ? max(0, p - a.window + 1) : 0;
+        m[k] = -INFINITY;
+        l[k] = 0.f;
 #pragma unroll
-        for (int c = 0; c < CV; ++c) {
-          const int d = c * 64 + tx * 4;
-          if (d < a.D)
-            store4(static_cast<T*>(a.out) + to_row * a.D + d,
-                   make_float4(o[k][c][0] * inv, o[k][c][1] * inv, o[k][c][2] * inv, o[k][c][3] * inv));
-        }
-        if (tx == 0 && a.lse) a.lse[to_row] = l[k] == 0.f ? -INFINITY : (m[k] + log2f(l[k])) * kLn2;
+        for (int c = 0; c < CV; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[k][c][e] = 0.f;
       }
-    } else {
-      float* part = part_slot<RT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
+
+      // a step's keys and values, on their way to the registers
+      float4 kr[kVecs], vr[kVecs];
+      auto fetch = [&](int un) {
+        const int j0 = (w.k.lo / kKT + un) * kKT;
+        const int32_t* table = a.seq.table + static_cast<int64_t>(w.b) * a.seq.table_pages;
+        // all page ids first, then all rows: one after the other, each waited for its own page id
+        int pid[kVecs];
+        bool bad = false;
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const int row = ty * R + k;
-#pragma unroll
-        for (int c = 0; c < CV; ++c) {
-          const int d = c * 64 + tx * 4;
-          if (d < a.D) store4(part + row * a.D + d, make_float4(o[k][c][0], o[k][c][1], o[k][c][2], o[k][c][3]));
+        for (int i = 0; i < kVecs; ++i) {
+          const int j = j0 + (tid + i * kNT) / (DP / 4);
+          const bool in = j >= w.k.lo && j < w.k.hi;
+          pid[i] = in ? ptx::ld_after_wait(table + (j >> a.seq.page_shift)) : -1;
+          if (in && (pid[i] < 0 || pid[i] >= a.pages)) {
+            bad = true;
+            pid[i] = -1;
+          }
         }
-        if (tx == 0) {
-          part[RT * a.D + row] = m[k];
-          part[RT * a.D + RT + row] = l[k];
+        if (bad) atomicOr(a.err, kErrIndexRange);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          const int x = tid + i * kNT, d = (x % (DP / 4)) * 4, j = j0 + x / (DP / 4);
+          const int64_t row = ((static_cast<int64_t>(pid[i]) * a.heads_kv + w.h) << a.seq.page_shift) +
+                              (j & ((1 << a.seq.page_shift) - 1));
+          kr[i] = vr[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (pid[i] >= 0 && d < a.D) {
+            kr[i] = load4(static_cast<const T*>(a.k) + row * a.D + d);
+            vr[i] = load4(static_cast<const T*>(a.v) + row * a.D + d);
+          }
+        }
+      };
+      fetch(ua);
+      const bool any_row = r0 + (ty & ~1) * R < n_rows;     // of the warp: its 2 R rows follow one another
+      for (int un = ua; un < ub; ++un) {
+        const int j0 = (w.k.lo / kKT + un) * kKT;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          const int x = tid + i * kNT, key = x / (DP / 4), d = (x % (DP / 4)) * 4;
+          *reinterpret_cast<float4*>(Ks + key * KS + d) = kr[i];
+          *reinterpret_cast<float4*>(Vs + key * DP + d) = vr[i];
+        }
+        __syncthreads();
+        if (un + 1 < ub) fetch(un + 1);
+        if (!any_row) continue;
+        float s[R][K] = {};
+#pragma unroll 8
+        for (int d = 0; d < DP; d += 4) {
+          float4 kk[K];
+#pragma unroll
+          for (int i = 0; i < K; ++i) kk[i] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * i) * KS + d);
+#pragma unroll
+          for (int k = 0; k < R; ++k) {
+            const float4 q = *reinterpret_cast<const float4*>(Qs + (ty * R + k) * DP + d);
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+              s[k][i] = fmaf(q.x, kk[i].x, s[k][i]);
+              s[k][i] = fmaf(q.y, kk[i].y, s[k][i]);
+              s[k][i] = fmaf(q.z, kk[i].z, s[k][i]);
+              s[k][i] = fmaf(q.w, kk[i].w, s[k][i]);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          float top = m[k];
+#pragma unroll
+          for (int i = 0; i < K; ++i) {
+            const int j = j0 + tx + 16 * i;
+            s[k][i] = j >= lo[k] && j < hi[k] ? s[k][i] * a.scale_log2 : -INFINITY;
+            top = fmaxf(top, s[k][i]);
+          }
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+          const float base = top == -INFINITY ? 0.f : top;
+          const float f = exp2f(m[k] - base);
+          m[k] = top;
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < K; ++i) {
+            const float p = exp2f(s[k][i] - base);
+            sum += p;
+            Ps[(ty * R + k) * kKT + tx + 16 * i] = p;
+          }
+          l[k] = fmaf(l[k], f, sum);   // this thread's keys only: the row's total is summed at the end
+#pragma unroll
+          for (int c = 0; c < CV; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[k][c][e] *= f;
+        }
+        __syncwarp();                  // a row's weights are written and read by one half-warp
+#pragma unroll 4
+        for (int j = 0; j < kKT; j += 4) {
+          float4 p[R];
+#pragma unroll
+          for (int k = 0; k < R; ++k) p[k] = *reinterpret_cast<const float4*>(Ps + (ty * R + k) * kKT + j);
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+            for (int c = 0; c < CV; ++c) {
+              const float4 v = *reinterpret_cast<const float4*>(Vs + (j + jj) * DP + c * 64 + tx * 4);
+#pragma unroll
+              for (int k = 0; k < R; ++k) {
+                const float pk = jj == 0 ? p[k].x : (jj == 1 ? p[k].y : (jj == 2 ? p[k].z : p[k].w));
+                o[k][c][0] = fmaf(pk, v.x, o[k][c][0]);
+                o[k][c][1] = fmaf(pk, v.y, o[k][c][1]);
+                o[k][c][2] = fmaf(pk, v.z, o[k][c][2]);
+                o[k][c][3] = fmaf(pk, v.w, o[k][c][3]);
+              }
+            }
         }
       }
-      const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
-      if (arrive_last<kNT>(a, cf, cl, &flag, tid, 1)) join_tile<T, kNT, RT, true>(a, w, cf, cl, tid, 1);
-    }
+
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) l[k] += __shfl_xor_sync(~0u, l[k], x);
+      const bool whole = ua == 0 && ub == w.units;
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          const int rr = r0 + ty * R + k;
+          if (rr >= n_rows) continue;
+          const int64_t to_row = (static_cast<int64_t>(w.q.row0) + rr / a.group) * a.heads + w.h * a.group +
+                                 rr % a.group;
+          const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
+#pragma unroll
+          for (int c = 0; c < CV; ++c) {
+            const int d = c * 64 + tx * 4;
+            if (d < a.D)
+              store4(static_cast<T*>(a.out) + to_row * a.D + d,
+                     make_float4(o[k][c][0] * inv, o[k][c][1] * inv, o[k][c][2] * inv, o[k][c][3] * inv));
+          }
+          if (tx == 0 && a.lse) a.lse[to_row] = l[k] == 0.f ? -INFINITY : (m[k] + log2f(l[k])) * kLn2;
+        }
+      } else {
+        float* part = part_slot<RT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          const int row = ty * R + k;
+#pragma unroll
+          for (int c = 0; c < CV; ++c) {
+            const int d = c * 64 + tx * 4;
+            if (d < a.D) store4(part + row * a.D + d, make_float4(o[k][c][0], o[k][c][1], o[k][c][2], o[k][c][3]));
+          }
+          if (tx == 0) {
+            part[RT * a.D + row] = m[k];
+            part[RT * a.D + RT + row] = l[k];
+          }
+        }
+        const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
+        if (arrive_last<kNT>(a, cf, cl, &flag, tid, 1)) join_tile<T, kNT, RT, true>(a, w, cf, cl, tid, 1);
+      }
     }
     u = piece.next;
     if (u >= range.places) break;

@@ -181,166 +181,168 @@ __global__ void __launch_bounds__(kNT, 1)
         const Piece piece = piece_of<kCost>(w, range, u, at);
         const int ua = piece.a, ub = piece.b;
         if (ub > ua) {
-        const int n_rows = w.q.n * a.group;
-        const int row = warp4 * 32 + lane, rr = w.r * kRT + t * 128 + row;
-        const bool live = rr < n_rows;
-        const bool work = w.k.hi > 0 && n_rows - w.r * kRT > t * 128;   // of the tile: same in all its warps
-        const RowMap at_row = row_at(a, row_map(a, w.r * kRT + t * 128 + warp4 * 32), lane);
-        const int p = w.q.len - w.q.n + at_row.token;
-        const int hi = !live || p < 0 ? 0 : (a.causal ? p + 1 : w.q.len);
-        const int lo = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
-        float m = -INFINITY, l = 0.f;
-        if (work) {
-          ptx::named_barrier(10 + t, 256);       // the tile's warps have read their output from here
-          load_queries<D>(a, w, sq + t * kTile, t, warp & 7, lane);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sh.q_full[t]);
-          for (int un = ua; un < ub; ++un) {
-            const int j0 = (w.k.lo / kKT + un) * kKT;
-            wait_bounded(&sh.s_full[t], sp, &sh.abort, a.err);
-            sp ^= 1;
-            ptx::tc_fence_after();
-            uint32_t s[2][32];
-            ptx::tmem_ld_32x32b_x32(ts + half * 64, s[0]);
-            ptx::tmem_ld_32x32b_x32(ts + half * 64 + 32, s[1]);
-            ptx::tmem_ld_wait();
-            const int j1 = j0 + half * 64;
-            if (__any_sync(~0u, j1 < lo || j1 + 64 > hi)) {
+          const int n_rows = w.q.n * a.group;
+          const int row = warp4 * 32 + lane, rr = w.r * kRT + t * 128 + row;
+          const bool live = rr < n_rows;
+          const bool work = w.k.hi > 0 && n_rows - w.r * kRT > t * 128;   // of the tile: same in all its warps
+          const RowMap at_row = row_at(a, row_map(a, w.r * kRT + t * 128 + warp4 * 32), lane);
+          const int p = w.q.len - w.q.n + at_row.token;
+          const int hi = !live || p < 0 ? 0 : (a.causal ? p + 1 : w.q.len);
+          const int lo = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
+          float m = -INFINITY, l = 0.f;
+          if (work) {
+            ptx::named_barrier(10 + t, 256);       // the tile's warps have read their output from here
+            load_queries<D>(a, w, sq + t * kTile, t, warp & 7, lane);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.q_full[t]);
+            for (int un = ua; un < ub; ++un) {
+              const int j0 = (w.k.lo / kKT + un) * kKT;
+              wait_bounded(&sh.s_full[t], sp, &sh.abort, a.err);
+              sp ^= 1;
+              ptx::tc_fence_after();
+              uint32_t s[2][32];
+              ptx::tmem_ld_32x32b_x32(ts + half * 64, s[0]);
+              ptx::tmem_ld_32x32b_x32(ts + half * 64 + 32, s[1]);
+              ptx::tmem_ld_wait();
+              const int j1 = j0 + half * 64;
+              if (__any_sync(~0u, j1 < lo || j1 + 64 > hi)) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    const int j = j1 + c * 32 + i;
+                    if (j < lo || j >= hi) s[c][i] = 0xFF800000u;      // -inf
+                  }
+              }
+              float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const int j = j1 + c * 32 + i;
-                  if (j < lo || j >= hi) s[c][i] = 0xFF800000u;      // -inf
+                for (int i = 0; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(s[c][i]));
+              float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
+              // both halves have read their scores here: the weights may go over them.  m stays unless a
+              // row of the two warps is more than kSlack ahead of it (or it is unset)
+              if (pair_any(pair, top > m + kSlack)) {
+                sh.top[t][half][row] = top;
+                ptx::named_barrier(pair, 64);
+                top = fmaxf(top, sh.top[t][half ^ 1][row]);
+                float f = 1.f;
+                if (top > m + kSlack) {
+                  f = ex2(m - top);
+                  m = top;
                 }
-            }
-            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(s[c][i]));
-            float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
-            // both halves have read their scores here: the weights may go over them.  m stays unless a
-            // row of the two warps is more than kSlack ahead of it (or it is unset)
-            if (pair_any(pair, top > m + kSlack)) {
-              sh.top[t][half][row] = top;
-              ptx::named_barrier(pair, 64);
-              top = fmaxf(top, sh.top[t][half ^ 1][row]);
-              float f = 1.f;
-              if (top > m + kSlack) {
-                f = ex2(m - top);
-                m = top;
-              }
-              if (un > ua && __any_sync(~0u, f != 1.f)) {
-                l *= f;
-                wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);   // the step before has been added
-                ptx::tc_fence_after();
+                if (un > ua && __any_sync(~0u, f != 1.f)) {
+                  l *= f;
+                  wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);   // the step before has been added
+                  ptx::tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 32) {
-                  uint32_t o[32];
-                  ptx::tmem_ld_32x32b_x32(to + c, o);
-                  ptx::tmem_ld_wait();
+                  for (int c = 0; c < D / 2; c += 32) {
+                    uint32_t o[32];
+                    ptx::tmem_ld_32x32b_x32(to + c, o);
+                    ptx::tmem_ld_wait();
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                  ptx::tmem_st_32x32b_x32(to + c, o);
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    ptx::tmem_st_32x32b_x32(to + c, o);
+                  }
                 }
               }
-            }
-            op ^= 1;
-            const float base = m == -INFINITY ? 0.f : m;
-            const F2 scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
-            F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+              op ^= 1;
+              const float base = m == -INFINITY ? 0.f : m;
+              const F2 scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
+              F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pk[16];
+              for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 e = unpack2(fma2(pack2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])),
-                                              scale2, base2));
-                const float2 p = make_float2(ex2(e.x), ex2(e.y));
-                sum[i & 1] = add2(sum[i & 1], pack2(p.x, p.y));
-                const __nv_bfloat162 b = __float22bfloat162_rn(p);
-                pk[i] = *reinterpret_cast<const uint32_t*>(&b);
+                for (int i = 0; i < 16; ++i) {
+                  const float2 e = unpack2(fma2(pack2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])),
+                                                scale2, base2));
+                  const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                  sum[i & 1] = add2(sum[i & 1], pack2(p.x, p.y));
+                  const __nv_bfloat162 b = __float22bfloat162_rn(p);
+                  pk[i] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+                ptx::tmem_st_32x32b_x16(ts + half * 32 + c * 16, pk);
               }
-              ptx::tmem_st_32x32b_x16(ts + half * 32 + c * 16, pk);
+              const float2 total = unpack2(add2(sum[0], sum[1]));
+              l += total.x + total.y;
+              ptx::tmem_st_wait();
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
             }
-            const float2 total = unpack2(add2(sum[0], sum[1]));
-            l += total.x + total.y;
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
+            wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);
+            ptx::tc_fence_after();
+          }
+          sh.sum[turn][t][half][row] = l;
+          ptx::named_barrier(pair, 64);
+          l = sh.sum[turn][t][0][row] + sh.sum[turn][t][1][row];
+          turn ^= 1;
+          const bool whole = ua == 0 && ub == w.units;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int64_t to_row = (static_cast<int64_t>(w.q.row0) + at_row.token) * a.heads + w.h * a.group + at_row.g;
+          float* part = part_slot<kRT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
+          // the warp's output passes through its share of the tile's queries, which are done with
+          constexpr int kChunks = D / 16;
+          uint8_t* stage = sq + t * kTile + (warp & 7) * (32 * D);
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 32) {
+            uint32_t o[32];
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
-          }
-          wait_bounded(&sh.o_full[t], op ^ 1, &sh.abort, a.err);
-          ptx::tc_fence_after();
-        }
-        sh.sum[turn][t][half][row] = l;
-        ptx::named_barrier(pair, 64);
-        l = sh.sum[turn][t][0][row] + sh.sum[turn][t][1][row];
-        turn ^= 1;
-        const bool whole = ua == 0 && ub == w.units;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t to_row = (static_cast<int64_t>(w.q.row0) + at_row.token) * a.heads + w.h * a.group + at_row.g;
-        float* part = part_slot<kRT>(a, 2 * static_cast<int>(blockIdx.x) + (ua == 0));
-        // the warp's output passes through its share of the tile's queries, which are done with
-        constexpr int kChunks = D / 16;
-        uint8_t* stage = sq + t * kTile + (warp & 7) * (32 * D);
-#pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
-          uint32_t o[32];
-          __syncwarp();
-          if (work) {
-            ptx::tmem_ld_32x32b_x32(to + c, o);
-            ptx::tmem_ld_wait();
-          } else {
+            if (work) {
+              ptx::tmem_ld_32x32b_x32(to + c, o);
+              ptx::tmem_ld_wait();
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0;
-          }
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t x[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[i + 2 * k]) * inv,
-                                                               __uint_as_float(o[i + 2 * k + 1]) * inv);
-                x[k] = *reinterpret_cast<const uint32_t*>(&b);
-              }
-              *reinterpret_cast<uint4*>(stage + lane * D + ((((c + i) >> 3) ^ (lane & (kChunks - 1))) << 4)) =
-                  make_uint4(x[0], x[1], x[2], x[3]);
+              for (int i = 0; i < 32; ++i) o[i] = 0;
             }
-          } else if (live) {
+            if (whole) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part + ((half * (D / 2) + c + i) * (kRT / 4) + t * 128 + row) * 4) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[i + 2 * k]) * inv,
+                                                                 __uint_as_float(o[i + 2 * k + 1]) * inv);
+                  x[k] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+                *reinterpret_cast<uint4*>(stage + lane * D + ((((c + i) >> 3) ^ (lane & (kChunks - 1))) << 4)) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            } else if (live) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(part + ((half * (D / 2) + c + i) * (kRT / 4) + t * 128 + row) * 4) =
+                    make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
           }
-        }
-        __syncwarp();
-        if (whole) {                  // whole rows of 128 (or 64) bytes, not 16 of each lane's row
+          __syncwarp();
+          if (whole) {                  // whole rows of 128 (or 64) bytes, not 16 of each lane's row
 #pragma unroll 4
-          for (int i = 0; i < kChunks; ++i) {
-            const int x = i * 32 + lane, r = x / kChunks, q = x % kChunks;
-            const int to_r = __shfl_sync(~0u, static_cast<int>(to_row), r);
-            if (w.r * kRT + t * 128 + warp4 * 32 + r < n_rows)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<int64_t>(to_r) * D +
-                                        half * (D / 2) + q * 8) =
-                  *reinterpret_cast<const uint4*>(stage + r * D + ((q ^ (r & (kChunks - 1))) << 4));
+            for (int i = 0; i < kChunks; ++i) {
+              const int x = i * 32 + lane, r = x / kChunks, q = x % kChunks;
+              const int to_r = __shfl_sync(~0u, static_cast<int>(to_row), r);
+              if (w.r * kRT + t * 128 + warp4 * 32 + r < n_rows)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<int64_t>(to_r) * D +
+                                          half * (D / 2) + q * 8) =
+                    *reinterpret_cast<const uint4*>(stage + r * D + ((q ^ (r & (kChunks - 1))) << 4));
+            }
           }
-        }
-        ptx::tc_fence_before();       // O is read: the next tile's first weights let it be overwritten
-        if (live && half == 0) {
-          if (whole) {
-            if (a.lse) a.lse[to_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-          } else {
-            part[kRT * D + t * 128 + row] = m;
-            part[kRT * D + kRT + t * 128 + row] = l;
+          ptx::tc_fence_before();       // O is read: the next tile's first weights let it be overwritten
+          if (live && half == 0) {
+            if (whole) {
+              if (a.lse) a.lse[to_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            } else {
+              part[kRT * D + t * 128 + row] = m;
+              part[kRT * D + kRT + t * 128 + row] = l;
+            }
           }
-        }
-        if (!whole) {
-          const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
-          if (arrive_last<kSoft>(a, cf, cl, &sh.flag, tid, 1)) join_tile<__nv_bfloat16, kSoft, kRT, false>(a, w, cf, cl, tid, 1);
-        }
+          if (!whole) {
+            const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
+            if (arrive_last<kSoft>(a, cf, cl, &sh.flag, tid, 1))
+              join_tile<__nv_bfloat16, kSoft, kRT, false>(a, w, cf, cl, tid, 1);
+          }
         }
         u = piece.next;
         if (u >= range.places) break;
@@ -448,7 +450,8 @@ __global__ void __launch_bounds__(kNT, 1)
                   const uint32_t va = v_lo + vs * (kTile >> 4);
 #pragma unroll
                   for (int k = 0; k < kKT / 16; ++k)
-                    ptx::mma_bf16_ta_words(tmem + 256 + t * 128, tmem + t * 128 + k * 8, va + k * (2048 >> 4), hi_v, kIdescO,
+                    ptx::mma_bf16_ta_words(tmem + 256 + t * 128, tmem + t * 128 + k * 8, va + k * (2048 >> 4), hi_v,
+                                           kIdescO,
                                            un > ua || k > 0);
                   ptx::mma_commit(&sh.o_full[t]);
                 }

@@ -43,7 +43,7 @@ __device__ __forceinline__ int32_t page_row(const AttnArgs& a, const Walk& w, in
   const int j = j0 + lane * box;
   const int32_t end = static_cast<int32_t>((a.pages * a.heads_kv) << shift);
   if (lane * box >= KT || j >= w.k.hi || j + box <= w.k.lo) return end;
-  const int pid = __ldg(a.seq.table + static_cast<int64_t>(w.b) * a.seq.table_pages + (j >> shift));
+  const int pid = ptx::ld_after_wait(a.seq.table + static_cast<int64_t>(w.b) * a.seq.table_pages + (j >> shift));
   if (pid < 0 || pid >= a.pages) {
     atomicOr(a.err, kErrIndexRange);
     return end;

@@ -31,6 +31,22 @@ __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.w
 
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Plain 32-bit loads that keep their place after grid_dep_wait.  A read-only
+// load (__ldg) counts as one of memory that nothing writes while the kernel
+// runs, so the compiler may move it before the wait; under programmatic launch
+// the previous kernel still writes then.  Loads whose addresses come from one
+// of these follow them.
+__device__ __forceinline__ int32_t ld_after_wait(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_after_wait(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // 32-bit load with acquire semantics at GPU scope (pairs with a release or a
 // fence-then-atomic on the writing side).
 __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t* p) {

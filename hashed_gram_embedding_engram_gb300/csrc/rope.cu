@@ -42,7 +42,8 @@ struct Raw<__nv_bfloat16> {
 
 __device__ __forceinline__ F2 pack2u(uint32_t a, uint32_t b) { return pack2(__uint_as_float(a), __uint_as_float(b)); }
 __device__ __forceinline__ void to_float(const Raw<float>& r, F2 (&x)[4]) {
-  x[0] = pack2u(r.lo.x, r.lo.y), x[1] = pack2u(r.lo.z, r.lo.w), x[2] = pack2u(r.hi.x, r.hi.y), x[3] = pack2u(r.hi.z, r.hi.w);
+  x[0] = pack2u(r.lo.x, r.lo.y), x[1] = pack2u(r.lo.z, r.lo.w);
+  x[2] = pack2u(r.hi.x, r.hi.y), x[3] = pack2u(r.hi.z, r.hi.w);
 }
 __device__ __forceinline__ void to_float(const Raw<__nv_bfloat16>& r, F2 (&x)[4]) {
   const uint32_t u[4] = {r.lo.x, r.lo.y, r.hi.x, r.hi.y};
@@ -76,17 +77,19 @@ __device__ __forceinline__ Place find_place(const RopeArgs& a, int token, int b)
   Place x{-1, -1};
   bool bad = false;
   if constexpr (kAppend) {
-    while (b < a.seq.B && __ldg(a.seq.start + b + 1) <= token) ++b;
+    while (b < a.seq.B && ptx::ld_after_wait(a.seq.start + b + 1) <= token) ++b;
     if (b >= a.seq.B) {
       bad = true;          // a row that no sequence has
     } else {
-      const int begin = __ldg(a.seq.start + b), end = __ldg(a.seq.start + b + 1), len = __ldg(a.seq.length + b);
+      const int begin = ptx::ld_after_wait(a.seq.start + b), end = ptx::ld_after_wait(a.seq.start + b + 1);
+      const int len = ptx::ld_after_wait(a.seq.length + b);
       const int64_t room = static_cast<int64_t>(a.seq.table_pages) << a.seq.page_shift;
       bad = begin < 0 || begin > token || end > a.tokens || len < 0 || len > room;
       if (!bad) x.pos = max(len - end + token, -1);
     }
     if (x.pos >= 0) {
-      const int pid = __ldg(a.seq.table + static_cast<int64_t>(b) * a.seq.table_pages + (x.pos >> a.seq.page_shift));
+      const int pid = ptx::ld_after_wait(a.seq.table + static_cast<int64_t>(b) * a.seq.table_pages +
+                                         (x.pos >> a.seq.page_shift));
       if (pid < 0 || pid >= a.pages)
         bad = true;
       else
@@ -94,7 +97,7 @@ __device__ __forceinline__ Place find_place(const RopeArgs& a, int token, int b)
                  (x.pos & ((1 << a.seq.page_shift) - 1));
     }
   } else if (a.positions) {
-    x.pos = __ldg(a.positions + token);
+    x.pos = ptx::ld_after_wait(a.positions + token);
     bad = x.pos < 0;
   }
   if (a.rope && a.rotary > 0) {
@@ -166,8 +169,8 @@ __global__ void __launch_bounds__(kNT, 8)
 #pragma unroll
   for (int i = 0; i < 4; ++i) gw[i] = pack2(1.f, 1.f);
   if (g && mine) {
-    const float4 lo = __ldg(reinterpret_cast<const float4*>(g + at_lo));
-    const float4 hi = __ldg(reinterpret_cast<const float4*>(g + at_hi));
+    const float4 lo = *reinterpret_cast<const float4*>(g + at_lo);
+    const float4 hi = *reinterpret_cast<const float4*>(g + at_hi);
     gw[0] = pack2(lo.x, lo.y), gw[1] = pack2(lo.z, lo.w), gw[2] = pack2(hi.x, hi.y), gw[3] = pack2(hi.z, hi.w);
   }
 
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kNT, 8)
   if constexpr (kAppend) {       // the sequence of the first token, by a count over start[1..B]
     for (int base = 1; base <= a.seq.B; base += kNT) {
       const int i = base + threadIdx.x;
-      b += __syncthreads_count(i <= a.seq.B && __ldg(a.seq.start + i) <= t0);
+      b += __syncthreads_count(i <= a.seq.B && ptx::ld_after_wait(a.seq.start + i) <= t0);
     }
   }
   const bool once = rounds == 1;

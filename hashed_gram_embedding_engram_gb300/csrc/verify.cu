@@ -141,18 +141,18 @@ __global__ void __launch_bounds__(kNT, 2)
   ptx::grid_dep_launch();
 
   if (warp == 0) {
-    const int n = n_drafts ? min(max(__ldg(n_drafts + b), 0), S) : S;
+    const int n = n_drafts ? min(max(ptx::ld_after_wait(n_drafts + b), 0), S) : S;
     int a = n;
     for (int i0 = 0; i0 < n && a == n; i0 += 32) {
       const int i = i0 + lane;
       bool ok = true;
       if (i < n) {
-        const int x = __ldg(drafts + static_cast<int64_t>(b) * S + i);
+        const int x = ptx::ld_after_wait(drafts + static_cast<int64_t>(b) * S + i);
         ok = false;
         if (x >= 0 && x < V) {
           const uint64_t p = fix(as_float(target[(static_cast<int64_t>(b) * (S + 1) + i) * V + x]));
           const uint64_t q = draft ? fix(as_float(draft[(static_cast<int64_t>(b) * S + i) * V + x])) : 1ull << 38;
-          ok = fix_u(__ldg(u + static_cast<int64_t>(b) * (S + 1) + i)) * q < p << 24;
+          ok = fix_u(ptx::ld_after_wait(u + static_cast<int64_t>(b) * (S + 1) + i)) * q < p << 24;
         }
       }
       const uint32_t turned_down = __ballot_sync(~0u, !ok);
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kNT, 2)
   Row<T> row;
   row.p = target + (static_cast<int64_t>(b) * (S + 1) + a) * V;
   row.q = turned_down && draft ? draft + (static_cast<int64_t>(b) * S + a) * V : nullptr;
-  row.certain = turned_down && !draft ? __ldg(drafts + static_cast<int64_t>(b) * S + a) : -1;
+  row.certain = turned_down && !draft ? ptx::ld_after_wait(drafts + static_cast<int64_t>(b) * S + a) : -1;
 
   // pieces of whole 32-lane steps, so that only the last ones are short
   constexpr int kStep = 32 * VEC;
@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kNT, 2)
     row.certain = -1;
   }
   int32_t* out = tokens + static_cast<int64_t>(b) * (S + 1);
-  if (rank == 0 && tid <= S && tid != a) out[tid] = tid < a ? __ldg(drafts + static_cast<int64_t>(b) * S + tid) : -1;
+  if (rank == 0 && tid <= S && tid != a)
+    out[tid] = tid < a ? ptx::ld_after_wait(drafts + static_cast<int64_t>(b) * S + tid) : -1;
   if (rank == 0 && tid == 0) accepted[b] = a;
 
   // first warp of every block: the goal and the piece that holds it
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kNT, 2)
       mine[i] = lane * kEach + i < parts ? sums[lane * kEach + i] : 0;
       own_sum += mine[i];
     }
-    const uint64_t U = fix_u(__ldg(u + static_cast<int64_t>(b) * (S + 1) + S));
+    const uint64_t U = fix_u(ptx::ld_after_wait(u + static_cast<int64_t>(b) * (S + 1) + S));
     const uint64_t goal = (__umul64hi(U, all) << 40) | ((U * all) >> 24);
     uint64_t upto = own_sum;
 #pragma unroll
@@ -341,7 +342,8 @@ cudaError_t launch_verify(const void* target, const void* draft, bool is_f32, co
     if (V % 4 == 0) return run<float, 4>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
     return run<float, 1>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
   }
-  if (V % 8 == 0) return run<__nv_bfloat16, 8>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
+  if (V % 8 == 0)
+    return run<__nv_bfloat16, 8>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
   return run<__nv_bfloat16, 1>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
 }
 
