@@ -23,6 +23,7 @@ _COUNTER_BYTES = 16384      # of a workspace, zero when it is new (engram_attn_w
 _pack_view = struct.Struct("@Pqq").pack
 _pack_sequences = struct.Struct("@PPPiiqi4x").pack
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _current_stream(device: int) -> int:
@@ -104,7 +105,7 @@ class AttentionPlan:
         """The plan's own workspace of a stream (calls on one stream run one after another).  A call
         under capture gets one of its own, in the graph's memory and zeroed by every replay: replays
         may run beside the stream's calls, and nothing of the capture has run yet when they do."""
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing():
             return self.new_workspace()
         ws = self._workspaces.get(stream)
         if ws is None:

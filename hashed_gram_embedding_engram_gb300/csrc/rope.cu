@@ -4,11 +4,11 @@
 // over the pairs of the first `rotary` elements; cosines and sines come from
 // the row of the token's position in a float table.
 //
-// One group of 8, 16 or 32 lanes holds one head of one token, 8 elements a
-// lane: four from each half of the rotated part (pairs i, i + rotary/2) or
-// eight that follow one another (adjacent pairs, and what is not rotated).  So
-// both elements of a pair, and the four cosines and sines that they need, are
-// in one lane; only the sum of squares crosses lanes.  A block has heads of
+// One group of 4 to 32 lanes holds one head of one token, two 16-byte runs a
+// lane: one from each half of the rotated part (pairs i, i + rotary/2) or two
+// that follow one another (adjacent pairs, and what is not rotated).  So both
+// elements of a pair, and the cosines and sines that they need, are in one
+// lane; only the sum of squares crosses lanes.  A block has heads of
 // one kind (queries, keys or values): its pointers, strides and norm weights
 // are the same for all its lanes.  All arithmetic is float; the outputs are
 // rounded once.  What bounds it: device memory on long inputs, the launch and
@@ -28,41 +28,39 @@ constexpr int kNT = 128;
 constexpr int kMaxRounds = 16;
 constexpr int kBlocksPerSm = 32;
 
-// Two runs of four elements as they lie in memory, and as pairs of floats.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<float> {
+// Two 16-byte runs as they lie in memory, and as pairs of floats (the first
+// half of them from `lo`).
+struct Raw {
   uint4 lo, hi;
-};
-template <>
-struct Raw<__nv_bfloat16> {
-  uint2 lo, hi;
 };
 
 __device__ __forceinline__ F2 pack2u(uint32_t a, uint32_t b) { return pack2(__uint_as_float(a), __uint_as_float(b)); }
-__device__ __forceinline__ void to_float(const Raw<float>& r, F2 (&x)[4]) {
+__device__ __forceinline__ void to_float(const Raw& r, F2 (&x)[4]) {       // float
   x[0] = pack2u(r.lo.x, r.lo.y), x[1] = pack2u(r.lo.z, r.lo.w);
   x[2] = pack2u(r.hi.x, r.hi.y), x[3] = pack2u(r.hi.z, r.hi.w);
 }
-__device__ __forceinline__ void to_float(const Raw<__nv_bfloat16>& r, F2 (&x)[4]) {
-  const uint32_t u[4] = {r.lo.x, r.lo.y, r.hi.x, r.hi.y};
+__device__ __forceinline__ void to_float(const Raw& r, F2 (&x)[8]) {       // bf16
+  const uint32_t u[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = pack2u(u[i] << 16, u[i] & 0xFFFF0000u);
+  for (int i = 0; i < 8; ++i) x[i] = pack2u(u[i] << 16, u[i] & 0xFFFF0000u);
 }
-__device__ __forceinline__ Raw<float> from_float(const F2 (&x)[4], float) {
-  const float2 a = unpack2(x[0]), b = unpack2(x[1]), c = unpack2(x[2]), d = unpack2(x[3]);
-  return {make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)),
-          make_uint4(__float_as_uint(c.x), __float_as_uint(c.y), __float_as_uint(d.x), __float_as_uint(d.y))};
-}
-__device__ __forceinline__ Raw<__nv_bfloat16> from_float(const F2 (&x)[4], __nv_bfloat16) {
-  uint32_t u[4];
+__device__ __forceinline__ Raw from_float(const F2 (&x)[4]) {
+  uint32_t u[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2(x[i]);
+    u[2 * i] = __float_as_uint(f.x), u[2 * i + 1] = __float_as_uint(f.y);
+  }
+  return {make_uint4(u[0], u[1], u[2], u[3]), make_uint4(u[4], u[5], u[6], u[7])};
+}
+__device__ __forceinline__ Raw from_float(const F2 (&x)[8]) {
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
     const __nv_bfloat162 h = __float22bfloat162_rn(unpack2(x[i]));
     u[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  return {make_uint2(u[0], u[1]), make_uint2(u[2], u[3])};
+  return {make_uint4(u[0], u[1], u[2], u[3]), make_uint4(u[4], u[5], u[6], u[7])};
 }
 
 // Where a token's keys and values go.
@@ -123,8 +121,7 @@ template <typename T, int LG, bool kAppend>
 __global__ void __launch_bounds__(kNT, 8)
     rope_kernel(const __grid_constant__ RopeArgs a, int blocks_q, int blocks_k, int rounds, bool adjacent) {
   constexpr int kGroups = kNT / LG;
-  using R = Raw<T>;
-  using V = decltype(R::lo);
+  constexpr int E = 16 / sizeof(T);         // elements of a run, pairs of a lane
   __shared__ Place places[kMaxRounds * kGroups];
   const int lane = threadIdx.x % LG, group = threadIdx.x / LG;
   int block = static_cast<int>(blockIdx.x);
@@ -141,9 +138,9 @@ __global__ void __launch_bounds__(kNT, 8)
   const int t0 = static_cast<int>(first / static_cast<unsigned>(heads));
 
   // this lane's two runs of a head
-  const bool mine = lane * 8 < a.D, turns = kind != kValues && lane * 8 < a.rotary;
-  const bool split = turns && !adjacent;
-  const int at_lo = split ? lane * 4 : lane * 8, at_hi = split ? a.rotary / 2 + lane * 4 : lane * 8 + 4;
+  const bool turns = kind != kValues && lane * 2 * E < a.rotary, split = turns && !adjacent;
+  const int at_lo = split ? lane * E : lane * 2 * E, at_hi = split ? a.rotary / 2 + lane * E : lane * 2 * E + E;
+  const bool has_lo = at_lo < a.D, has_hi = at_hi < a.D;
 
   // the group's head, and the steps to its next one
   const int h0 = static_cast<int>(first) - t0 * heads + group;
@@ -156,22 +153,20 @@ __global__ void __launch_bounds__(kNT, 8)
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   auto load = [&](int t, int h, bool live) {
-    R r{};
-    if (live && mine) {
-      const T* p = static_cast<const T*>(view.ptr) + t * view.ts + h * view.hs;
-      r.lo = *reinterpret_cast<const V*>(p + at_lo);
-      r.hi = *reinterpret_cast<const V*>(p + at_hi);
-    }
+    Raw r{};
+    const T* p = static_cast<const T*>(view.ptr) + t * view.ts + h * view.hs;
+    if (live && has_lo) r.lo = *reinterpret_cast<const uint4*>(p + at_lo);
+    if (live && has_hi) r.hi = *reinterpret_cast<const uint4*>(p + at_hi);
     return r;
   };
-  R now = load(t, h, group < n);
-  F2 gw[4];
+  Raw now = load(t, h, group < n);
+  F2 gw[E];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) gw[i] = pack2(1.f, 1.f);
-  if (g && mine) {
-    const float4 lo = *reinterpret_cast<const float4*>(g + at_lo);
-    const float4 hi = *reinterpret_cast<const float4*>(g + at_hi);
-    gw[0] = pack2(lo.x, lo.y), gw[1] = pack2(lo.z, lo.w), gw[2] = pack2(hi.x, hi.y), gw[3] = pack2(hi.z, hi.w);
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 one = make_float2(1.f, 1.f);
+    const float2 lo = g && has_lo ? *reinterpret_cast<const float2*>(g + at_lo + 2 * i) : one;
+    const float2 hi = g && has_hi ? *reinterpret_cast<const float2*>(g + at_hi + 2 * i) : one;
+    gw[i] = pack2(lo.x, lo.y), gw[E / 2 + i] = pack2(hi.x, hi.y);
   }
 
   int b = 0;
@@ -194,16 +189,16 @@ __global__ void __launch_bounds__(kNT, 8)
     const bool live = i0 + group < n;
     int next_t = t, next_h = h;
     step(next_t, next_h);
-    const R next = load(next_t, next_h, i0 + kGroups + group < n);
+    const Raw next = load(next_t, next_h, i0 + kGroups + group < n);
     Place place{-1, -1};
     if (live) place = once ? find_place<kAppend>(a, t, b) : places[t - t0];
-    F2 x[4];
+    F2 x[E];
     to_float(now, x);
     if (kind != kValues) {       // the same in the whole block
       if (g) {
         F2 ss = pack2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ss = fma2(x[i], x[i], ss);
+        for (int i = 0; i < E; ++i) ss = fma2(x[i], x[i], ss);
         const float2 s2 = unpack2(ss);
         float sum = s2.x + s2.y;
 #pragma unroll
@@ -211,32 +206,35 @@ __global__ void __launch_bounds__(kNT, 8)
         const float inv = rsqrtf(fmaf(sum, a.inv_D, a.eps));
         const F2 inv2 = pack2(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], mul2(gw[i], inv2));
+        for (int i = 0; i < E; ++i) x[i] = mul2(x[i], mul2(gw[i], inv2));
       }
       if (turns && place.pos >= 0) {
-        const float* row = a.rope + static_cast<int64_t>(place.pos) * a.rotary + lane * 4;
-        const float4 c4 = __ldg(reinterpret_cast<const float4*>(row));
-        const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + a.rotary / 2));
-        if (adjacent) {
-          const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+        const float* row = a.rope + static_cast<int64_t>(place.pos) * a.rotary + lane * E;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 v = unpack2(x[i]);
-            x[i] = pack2(v.x * cs[i] - v.y * sn[i], v.x * sn[i] + v.y * cs[i]);
-          }
-        } else {
-          const F2 cs[2] = {pack2(c4.x, c4.y), pack2(c4.z, c4.w)}, sn[2] = {pack2(s4.x, s4.y), pack2(s4.z, s4.w)};
-          const F2 neg[2] = {pack2(-s4.x, -s4.y), pack2(-s4.z, -s4.w)};
+        for (int c = 0; c < E / 4; ++c) {              // four angles, eight elements
+          const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + c * 4));
+          const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + a.rotary / 2 + c * 4));
+          if (adjacent) {
+            const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const F2 lo = x[i], hi = x[2 + i];
-            x[i] = fma2(lo, cs[i], mul2(hi, neg[i]));
-            x[2 + i] = fma2(hi, cs[i], mul2(lo, sn[i]));
+            for (int i = 0; i < 4; ++i) {
+              const float2 v = unpack2(x[c * 4 + i]);
+              x[c * 4 + i] = pack2(v.x * cs[i] - v.y * sn[i], v.x * sn[i] + v.y * cs[i]);
+            }
+          } else {
+            const F2 cs[2] = {pack2(c4.x, c4.y), pack2(c4.z, c4.w)}, sn[2] = {pack2(s4.x, s4.y), pack2(s4.z, s4.w)};
+            const F2 neg[2] = {pack2(-s4.x, -s4.y), pack2(-s4.z, -s4.w)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const F2 lo = x[c * 2 + i], hi = x[E / 2 + c * 2 + i];
+              x[c * 2 + i] = fma2(lo, cs[i], mul2(hi, neg[i]));
+              x[E / 2 + c * 2 + i] = fma2(hi, cs[i], mul2(lo, sn[i]));
+            }
           }
         }
       }
     }
-    if (live && mine) {
+    if (live) {
       T* to = nullptr;
       if (kind == kQueries)
         to = static_cast<T*>(a.q_out) + (static_cast<int64_t>(t) * heads + h) * a.D;
@@ -246,9 +244,9 @@ __global__ void __launch_bounds__(kNT, 8)
         to = static_cast<T*>(kind == kKeys ? a.k_pages : a.v_pages) +
              (place.slot + (static_cast<int64_t>(h) << a.seq.page_shift)) * a.D;
       if (to) {
-        const R r = from_float(x, T());
-        *reinterpret_cast<V*>(to + at_lo) = r.lo;
-        *reinterpret_cast<V*>(to + at_hi) = r.hi;
+        const Raw r = from_float(x);
+        if (has_lo) *reinterpret_cast<uint4*>(to + at_lo) = r.lo;
+        if (has_hi) *reinterpret_cast<uint4*>(to + at_hi) = r.hi;
       }
     }
     __syncwarp();
@@ -279,9 +277,10 @@ cudaError_t run(const RopeArgs& a, bool adjacent, int num_sms, cudaStream_t s) {
 
 template <typename T>
 cudaError_t pick_lanes(const RopeArgs& a, bool adjacent, int num_sms, cudaStream_t s) {
-  if (a.D <= 64) return run<T, 8>(a, adjacent, num_sms, s);
-  if (a.D <= 128) return run<T, 16>(a, adjacent, num_sms, s);
-  return run<T, 32>(a, adjacent, num_sms, s);
+  constexpr int kFewest = 64 * sizeof(T) / 32;      // lanes of a head of up to 64
+  if (a.D <= 64) return run<T, kFewest>(a, adjacent, num_sms, s);
+  if (a.D <= 128) return run<T, 2 * kFewest>(a, adjacent, num_sms, s);
+  return run<T, 4 * kFewest>(a, adjacent, num_sms, s);
 }
 
 }  // namespace
