@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
             }
           }
         }
+        float scale[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
           float top = m[k];
@@ -192,12 +193,12 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
             Ps[(ty * R + k) * kKT + tx + 16 * i] = p;
           }
           l[k] = fmaf(l[k], f, sum);   // this thread's keys only: the row's total is summed at the end
-#pragma unroll
-          for (int c = 0; c < CV; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[k][c][e] *= f;
+          scale[k] = f;
         }
         __syncwarp();                  // a row's weights are written and read by one half-warp
+        // the step's own sums, added to the row's once: as one chain over all keys the rounding errors
+        // grow with the square root of their number (1.1e-6 of the output at 27k keys)
+        float t[R][CV][4] = {};
 #pragma unroll 4
         for (int j = 0; j < kKT; j += 4) {
           float4 p[R];
@@ -211,13 +212,19 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
 #pragma unroll
               for (int k = 0; k < R; ++k) {
                 const float pk = jj == 0 ? p[k].x : (jj == 1 ? p[k].y : (jj == 2 ? p[k].z : p[k].w));
-                o[k][c][0] = fmaf(pk, v.x, o[k][c][0]);
-                o[k][c][1] = fmaf(pk, v.y, o[k][c][1]);
-                o[k][c][2] = fmaf(pk, v.z, o[k][c][2]);
-                o[k][c][3] = fmaf(pk, v.w, o[k][c][3]);
+                t[k][c][0] = fmaf(pk, v.x, t[k][c][0]);
+                t[k][c][1] = fmaf(pk, v.y, t[k][c][1]);
+                t[k][c][2] = fmaf(pk, v.z, t[k][c][2]);
+                t[k][c][3] = fmaf(pk, v.w, t[k][c][3]);
               }
             }
         }
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+          for (int c = 0; c < CV; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[k][c][e] = fmaf(o[k][c][e], scale[k], t[k][c][e]);
       }
 
 #pragma unroll

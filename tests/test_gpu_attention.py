@@ -611,3 +611,18 @@ def test_capture_on_a_new_stream_leaves_its_later_calls_alone():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("D,page", [(64, 32), (128, 64)])
+def test_fp32_errors_do_not_grow_with_the_length(D, page):
+    """Norm-wise error of a single token over 30000 keys.  Scores of size up to 8 (in powers of two)
+    are rounded to 2^-24 of that, 4 2^-24 on average in a weight; a step's sum is a chain of 64
+    additions (about sqrt(64) / 2 = 4 roundings of the partial sums' size) and the steps' sums one of
+    a few hundred in a block, each again half a rounding: 16 2^-24 = 1e-6 is not reached, where one
+    chain over all keys (sqrt(30000) / 2 = 87 roundings) is several times it."""
+    c = Case(seed=17, dtype="f32", new=(1,), length=(30000,), heads=4, heads_kv=2, D=D, page=page)
+    out, lse = c.run()
+    ref, ref_lse, _ = O.attention(f64(c.q), c.k.double().numpy(), c.v.double().numpy(), c.start, c.length, c.table,
+                                  D ** -0.5)
+    assert np.linalg.norm(f64(out) - ref) <= 16 * U * np.linalg.norm(ref)
+    assert np.abs(f64(lse) - ref_lse).max() <= 16 * U * np.abs(ref_lse).max()
