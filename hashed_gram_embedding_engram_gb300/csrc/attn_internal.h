@@ -97,6 +97,9 @@ cudaError_t launch_rope(const engram_attn_plan* p, const RopeArgs& a, cudaStream
 cudaError_t launch_attention_simt(const engram_attn_plan* p, const AttnArgs& a, int max_new, cudaStream_t s);
 // Attention of at most 32 rows a sequence and cache head (new tokens x group) on
 // the tensor cores, where the cache has tensor maps; more rows make more tiles.
+// 16 sequences over 16384 tokens, 8 cache heads, D 128, against the tiles kernel:
+// 16 rows 182 us / 244, 32 rows 188 / 237, 36 rows (two tiles, the keys read
+// twice) 348 / 240, 64 rows 353 / 235; the same order at 64 x 2000 and 32 x 512.
 bool attention_rows_applies(const engram_kv_cache* c, int64_t rows);
 cudaError_t launch_attention_rows(const engram_kv_cache* c, const AttnArgs& a, int64_t rows, cudaStream_t s);
 // Attention of longer chunks on the tensor cores, 256 rows a tile.

@@ -468,7 +468,7 @@ __device__ void join_tile(const AttnArgs& a, const Walk& w, int cf, int cl, int 
   if (n <= 4)
     join_sums<T, NT, RT, 4, kByRow ? 4 : 2, kByRow>(a, first, n, rows, tid, place);
   else
-    join_sums<T, NT, RT, kByRow ? 1 : 4, kByRow ? 8 : 2, kByRow>(a, first, n, rows, tid, place);
+    join_sums<T, NT, RT, kByRow ? 2 : 4, kByRow ? 8 : 2, kByRow>(a, first, n, rows, tid, place);
 }
 
 }  // namespace at
