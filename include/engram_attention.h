@@ -119,8 +119,11 @@ engram_status_t engram_kv_append(engram_kv_cache_t* cache, const engram_sequence
 
 /* Attention of the new tokens' queries over the cache: query of position p sees
  * key j if j < length[b], j <= p (causal != 0) and j > p - window (window > 0).
- * A query that sees no key gets out 0 and lse -inf.  out: dense [tokens, heads,
- * D]; lse: float [tokens, heads] or NULL.  The scores, the running maximum and
+ * A query that sees no key gets out 0 and lse -inf.  What lies in the slots past
+ * a length, and in pages that no query sees, does not matter.  A key of the
+ * sequence that this query does not see has weight 0 for it; its value has to
+ * be finite (0 times infinity or NaN is NaN).  out: dense [tokens, heads, D],
+ * rows of no sequence are not written; lse: float [tokens, heads] or NULL.  The scores, the running maximum and
  * sum and the accumulated output are float; for BF16 the weights exp(s - max)
  * are rounded to bf16 for the product with v (their sum is of the unrounded). */
 engram_status_t engram_paged_attention(const engram_kv_cache_t* cache, const engram_sequences_t* seq,
