@@ -70,7 +70,7 @@ struct Place {
   int pos;         // row of the table, or -1: not rotated
 };
 
-// The place of token `token`; `first`: sequence of the block's first token.
+// The place of token `token`; b: the sequence of the block's first token.
 template <bool kAppend>
 __device__ __forceinline__ Place find_place(const RopeArgs& a, int token, int b) {
   Place x{-1, -1};
