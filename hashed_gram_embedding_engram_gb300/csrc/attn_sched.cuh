@@ -32,14 +32,19 @@ struct Seq {
   int len;     // tokens in the cache
 };
 
+// A sequence with a start or a length out of range keeps the rows that exist, without
+// keys: with a length or a row count cut to what fits, its rows would stand at other
+// positions and read entries of the table that it does not use, which may name another
+// sequence's pages.  The append leaves the same sequences out.
 __device__ __forceinline__ Seq load_seq(const SeqArgs& s, int b, uint32_t* err) {
   const int a0 = ptx::ld_after_wait(s.start + b), a1 = ptx::ld_after_wait(s.start + b + 1);
   const int len = ptx::ld_after_wait(s.length + b);
   Seq q;
   q.row0 = min(max(a0, 0), s.tokens);
   q.n = min(max(a1, q.row0), s.tokens) - q.row0;
-  q.len = min(max(len, 0), s.table_pages << s.page_shift);
-  if (err && (q.row0 != a0 || q.row0 + q.n != a1 || q.len != len)) atomicOr(err, kErrIndexRange);
+  const bool bad = q.row0 != a0 || q.row0 + q.n != a1 || len < 0 || len > s.table_pages << s.page_shift;
+  q.len = bad ? 0 : len;
+  if (err && bad) atomicOr(err, kErrIndexRange);
   return q;
 }
 

@@ -62,10 +62,10 @@ typedef struct {
  * is padding (an idle slot of a fixed-size batch has length 0): it is not
  * appended, its query sees no key.  Position p lives in slot p mod page of
  * cache page table[b * table_pages + p / page].  All three arrays are device
- * memory.  A start outside [0, tokens], a length above table_pages * page or a
- * used page id outside the cache sets the plan's INDEX_RANGE flag: such rows,
- * positions and pages are left out (not read, not written; keys of a page
- * left out count as zeros). */
+ * memory.  A start outside [0, tokens], a length outside [0, table_pages * page]
+ * or a used page id outside the cache sets the plan's INDEX_RANGE flag.  Of a
+ * sequence with such a start or length nothing is appended and its queries see
+ * no key; such a page is not read or written, and its keys count as zeros. */
 typedef struct {
   const int32_t* start;         /* [B + 1] */
   const int32_t* length;        /* [B] */
