@@ -84,7 +84,15 @@ engram_status_t engram_attn_plan_create(const engram_attn_config_t* cfg, engram_
   p->scale = c.scale > 0.f ? c.scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.head_dim)));
   p->device = dev;
   p->num_sms = sms;
-  if (cudaMalloc(&p->err, sizeof(uint32_t)) != cudaSuccess || cudaMemset(p->err, 0, sizeof(uint32_t)) != cudaSuccess) {
+  cudaError_t e = cudaMalloc(&p->err, sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(uint32_t));
+  if (e == cudaSuccess && engram::attn_tensor_cores(c)) {
+    e = engram::prepare_attention_rows(p);
+    if (e == cudaSuccess) e = engram::prepare_attention_tiles(p);
+  } else if (e == cudaSuccess) {
+    e = engram::prepare_attention_simt(p);
+  }
+  if (e != cudaSuccess) {
     cudaFree(p->err);
     delete p;
     return ENGRAM_ERR_CUDA;
@@ -134,7 +142,7 @@ engram_status_t engram_kv_cache_create(const engram_attn_plan_t* plan, void* k, 
   c->v = v;
   c->pages = pages;
   const int D = plan->cfg.head_dim;
-  c->maps = plan->cfg.dtype == ENGRAM_BF16 && (D == 64 || D == 128);
+  c->maps = engram::attn_tensor_cores(plan->cfg);
   if (c->maps) {
     const uint64_t rows = static_cast<uint64_t>(pages) * plan->cfg.heads_kv << plan->page_shift;
     auto map = [&](CUtensorMap* m, const void* base, int most) {

@@ -16,6 +16,7 @@ struct engram_attn_plan {
   float scale;
   int device;
   int num_sms;
+  int simt_grid[2];           // blocks of the CUDA-core kernel, with 16 and with 64 rows a tile
   uint32_t* err;              // device error word
 };
 
@@ -91,6 +92,17 @@ inline size_t attn_workspace_bytes(const engram_attn_plan* p) {
   return kAttnCounters * 4 +
          static_cast<size_t>(p->num_sms) * 2 * kAttnPartRows * (static_cast<size_t>(p->cfg.head_dim) + 2) * 4;
 }
+
+// bf16 with heads of 64 or 128: tensor maps, the rows and the tiles kernel; else the CUDA cores.
+inline bool attn_tensor_cores(const engram_attn_config_t& c) {
+  return c.dtype == ENGRAM_BF16 && (c.head_dim == 64 || c.head_dim == 128);
+}
+
+// Once a plan, with its device current: what the runtime keeps of a kernel for each
+// device (its shared memory above 48 KB, the blocks that fit an SM).
+cudaError_t prepare_attention_rows(const engram_attn_plan* p);
+cudaError_t prepare_attention_tiles(const engram_attn_plan* p);
+cudaError_t prepare_attention_simt(engram_attn_plan* p);
 
 cudaError_t launch_rope(const engram_attn_plan* p, const RopeArgs& a, cudaStream_t s);
 // Attention on the CUDA cores: every type and head size.

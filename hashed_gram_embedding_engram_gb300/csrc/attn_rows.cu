@@ -354,19 +354,24 @@ __global__ void __launch_bounds__(kNT, 2)
 
 template <int D, int MT>
 cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
-  constexpr int smem = Cfg<D>::kSmem;
-  static bool attr_set = false;   // per template instance; idempotent if raced
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
-  return launch_pdl(attn_rows_kernel<D, MT>, dim3(p->num_sms * 2), dim3(kNT), smem, s, a, c->k64, c->v64);
+  return launch_pdl(attn_rows_kernel<D, MT>, dim3(p->num_sms * 2), dim3(kNT), Cfg<D>::kSmem, s, a, c->k64, c->v64);
+}
+
+template <int D>
+cudaError_t prepare() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_rows_kernel<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attn_rows_kernel<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
 }
 
 }  // namespace
 
 bool attention_rows_applies(const engram_kv_cache* c, int64_t rows) { return c->maps && rows <= 32; }
+
+cudaError_t prepare_attention_rows(const engram_attn_plan* p) {
+  return p->cfg.head_dim == 64 ? prepare<64>() : prepare<128>();
+}
 
 cudaError_t launch_attention_rows(const engram_kv_cache* c, const AttnArgs& a, int64_t rows, cudaStream_t s) {
   const engram_attn_plan* p = c->plan;

@@ -278,21 +278,34 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
 
 template <typename T, int DP, int RT>
 cudaError_t run(const engram_attn_plan* p, const AttnArgs& a, cudaStream_t s) {
+  return launch_pdl(attn_simt_kernel<T, DP, RT>, dim3(p->simt_grid[RT == 64]), dim3(kNT), Cfg<DP, RT>::kSmem, s, a);
+}
+
+template <typename T, int DP, int RT>
+cudaError_t prepare(engram_attn_plan* p) {
   constexpr int smem = Cfg<DP, RT>::kSmem;
-  static int per_sm = 0;      // per template instance; idempotent if raced
-  if (per_sm == 0) {
-    cudaError_t e =
-        cudaFuncSetAttribute(attn_simt_kernel<T, DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_simt_kernel<T, DP, RT>, kNT, smem);
-    if (e != cudaSuccess) return e;
-    // the workspace holds kAttnPartRows rows of partials an SM, twice
-    const int fit = kAttnPartRows / RT;
-    per_sm = n < 1 ? 1 : (n > fit ? fit : n);
-  }
-  const int grid = p->num_sms * per_sm;
-  return launch_pdl(attn_simt_kernel<T, DP, RT>, dim3(grid), dim3(kNT), smem, s, a);
+  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  int n = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_simt_kernel<T, DP, RT>, kNT, smem);
+  if (e != cudaSuccess) return e;
+  // the workspace holds kAttnPartRows rows of partials an SM, twice
+  const int fit = kAttnPartRows / RT;
+  p->simt_grid[RT == 64] = p->num_sms * (n < 1 ? 1 : (n > fit ? fit : n));
+  return cudaSuccess;
+}
+
+template <typename T, int DP>
+cudaError_t prepare_rows(engram_attn_plan* p) {
+  const cudaError_t e = prepare<T, DP, 16>(p);
+  return e != cudaSuccess ? e : prepare<T, DP, 64>(p);
+}
+
+template <typename T>
+cudaError_t prepare_dim(engram_attn_plan* p) {
+  if (p->cfg.head_dim <= 64) return prepare_rows<T, 64>(p);
+  if (p->cfg.head_dim <= 128) return prepare_rows<T, 128>(p);
+  return prepare_rows<T, 256>(p);
 }
 
 template <typename T, int DP>
@@ -309,6 +322,10 @@ cudaError_t pick_dim(const engram_attn_plan* p, const AttnArgs& a, int max_new, 
 }
 
 }  // namespace
+
+cudaError_t prepare_attention_simt(engram_attn_plan* p) {
+  return p->cfg.dtype == ENGRAM_F32 ? prepare_dim<float>(p) : prepare_dim<__nv_bfloat16>(p);
+}
 
 cudaError_t launch_attention_simt(const engram_attn_plan* p, const AttnArgs& a, int max_new, cudaStream_t s) {
   return p->cfg.dtype == ENGRAM_F32 ? pick_dim<float>(p, a, max_new, s) : pick_dim<__nv_bfloat16>(p, a, max_new, s);

@@ -492,17 +492,16 @@ __global__ void __launch_bounds__(kNT, 1)
 
 template <int D>
 cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
-  constexpr int smem = Cfg<D>::kSmem;
-  static bool attr_set = false;   // per template instance; idempotent if raced
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
-  return launch_pdl(attn_tiles_kernel<D>, dim3(p->num_sms), dim3(kNT), smem, s, a, c->k128, c->v128);
+  return launch_pdl(attn_tiles_kernel<D>, dim3(p->num_sms), dim3(kNT), Cfg<D>::kSmem, s, a, c->k128, c->v128);
 }
 
 }  // namespace
+
+cudaError_t prepare_attention_tiles(const engram_attn_plan* p) {
+  if (p->cfg.head_dim == 64)
+    return cudaFuncSetAttribute(attn_tiles_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<64>::kSmem);
+  return cudaFuncSetAttribute(attn_tiles_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::kSmem);
+}
 
 cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
   return a.D == 64 ? run<64>(c->plan, c, a, s) : run<128>(c->plan, c, a, s);
