@@ -23,6 +23,14 @@ bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u
 int elem_bytes(engram_dtype_t t) { return t == ENGRAM_F32 ? 4 : 2; }
 engram_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? ENGRAM_OK : ENGRAM_ERR_CUDA; }
 
+// A plan's calls launch on the current device, which has to be the plan's: its error word,
+// and what its kernels may use, are that device's.
+engram_status_t device_ok(const engram_attn_plan* p) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ENGRAM_ERR_CUDA;
+  return dev == p->device ? ENGRAM_OK : ENGRAM_ERR_INVALID_ARG;
+}
+
 bool view_ok(const engram_heads_view_t* v, engram_dtype_t t) {
   if (!v || !v->ptr || !aligned16(v->ptr)) return false;
   const int64_t step = 16 / elem_bytes(t);
@@ -110,6 +118,7 @@ engram_status_t engram_attn_plan_destroy(engram_attn_plan_t* plan) {
 
 engram_status_t engram_attn_get_error(const engram_attn_plan_t* plan, engram_stream_t stream, uint32_t* flags_out) {
   if (!plan) return ENGRAM_ERR_INVALID_ARG;
+  if (engram_status_t e = device_ok(plan)) return e;
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return ENGRAM_ERR_CUDA;
   uint32_t bits = 0;
   const uint32_t zero = 0;
@@ -176,6 +185,7 @@ engram_status_t engram_qk_norm_rope(const engram_attn_plan_t* plan, const engram
   if (!rope_ok(plan, rope, rope_len) || (g_q && !aligned16(g_q)) || (g_k && !aligned16(g_k)))
     return ENGRAM_ERR_INVALID_ARG;
   if (plan->cfg.rotary_dim > 0 && (!rope || !positions)) return ENGRAM_ERR_INVALID_ARG;
+  if (engram_status_t e = device_ok(plan)) return e;
   engram::RopeArgs a{};
   a.q = view_of(q);
   a.k = view_of(with_k ? k : nullptr);
@@ -210,6 +220,7 @@ engram_status_t engram_kv_append(engram_kv_cache_t* cache, const engram_sequence
   if (with_q && (!view_ok(q, plan->cfg.dtype) || !q_out || !aligned16(q_out))) return ENGRAM_ERR_INVALID_ARG;
   if (!rope_ok(plan, rope, rope_len) || (g_q && !aligned16(g_q)) || (g_k && !aligned16(g_k)))
     return ENGRAM_ERR_INVALID_ARG;
+  if (engram_status_t e = device_ok(plan)) return e;
   engram::RopeArgs a{};
   a.q = view_of(with_q ? q : nullptr);
   a.k = view_of(k);
@@ -245,6 +256,7 @@ engram_status_t engram_paged_attention(const engram_kv_cache_t* cache, const eng
   if (!view_ok(q, plan->cfg.dtype) || !out || !aligned16(out)) return ENGRAM_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < engram::attn_workspace_bytes(plan)) return ENGRAM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ENGRAM_ERR_INVALID_ARG;
+  if (engram_status_t e = device_ok(plan)) return e;
   engram::AttnArgs a{};
   a.q = view_of(q);
   a.k = cache->k;

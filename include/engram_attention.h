@@ -18,6 +18,8 @@
  *
  * Conventions are those of engram.h: stream-ordered calls, host-checked
  * arguments, caller-owned buffers, status codes, an error word per plan.
+ * A plan belongs to the device that was current when it was made; its calls
+ * with another device current return ENGRAM_ERR_INVALID_ARG.
  * Every call is capturable in a CUDA graph; the lengths, starts and page
  * tables are read on the device when the call runs.
  */

@@ -84,11 +84,34 @@ struct Layer {
     engram_attn_workspace_bytes(plan, &bytes);
     expect(engram_kv_cache_create(plan, kMem, kMem, 16, &cache) == ENGRAM_OK, "cache", D, device);
   }
+  engram_status_t norm() { return engram_qk_norm_rope(plan, &kView, nullptr, 4, nullptr, nullptr, 0, nullptr, nullptr, kMem, nullptr, nullptr); }
+  engram_status_t append() {
+    const engram_sequences_t s = {kInts, kInts, kInts, 1, 4, 4, 4};
+    return engram_kv_append(cache, &s, &kView, &kView, nullptr, 0, nullptr, nullptr, nullptr, nullptr, nullptr);
+  }
   engram_status_t attend(int n) {
     const engram_sequences_t s = {kInts, kInts, kInts, 1, 4, n, n};
     return engram_paged_attention(cache, &s, &kView, 1, 0, kMem, nullptr, kMem, bytes, nullptr);
   }
 };
+
+// Every call of a plan belongs to the plan's device: elsewhere it is refused and nothing starts.
+static void other_device() {
+  Layer x(ENGRAM_BF16, 128, 0);
+  g_device = 1;
+  const int before = g_launches;
+  expect(x.norm() == ENGRAM_ERR_INVALID_ARG, "norm on another device", 0, 1);
+  expect(x.append() == ENGRAM_ERR_INVALID_ARG, "append on another device", 0, 1);
+  expect(x.attend(1) == ENGRAM_ERR_INVALID_ARG && x.attend(4) == ENGRAM_ERR_INVALID_ARG &&
+         x.attend(100) == ENGRAM_ERR_INVALID_ARG, "attention on another device", 0, 1);
+  expect(engram_attn_get_error(x.plan, nullptr, nullptr) == ENGRAM_ERR_INVALID_ARG && g_syncs == 0,
+         "get_error on another device", 0, 1);
+  expect(g_launches == before, "launches on another device", before, g_launches);
+  g_device = 0;
+  expect(x.norm() == ENGRAM_OK && x.append() == ENGRAM_OK && x.attend(1) == ENGRAM_OK &&
+         engram_attn_get_error(x.plan, nullptr, nullptr) == ENGRAM_OK, "calls on the plan's device", 0, 0);
+  expect(g_launches == before + 3, "launches on the plan's device", before, g_launches);
+}
 
 // Attention of every kernel and head size, on each device in turn.
 static void each_device(int first) {
@@ -105,6 +128,7 @@ static void each_device(int first) {
 }
 
 int main(int argc, char** argv) {
+  if (!strcmp(argv[1], "other")) other_device();
   if (!strcmp(argv[1], "each01")) each_device(0);
   if (!strcmp(argv[1], "each10")) each_device(1);
   std::printf("bad %d\n", g_bad);
@@ -132,6 +156,10 @@ def program(tmp_path_factory):
 def run(program, scenario):
     r = subprocess.run([program, scenario], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and "bad 0" in r.stdout, r.stdout + r.stderr
+
+
+def test_calls_with_another_device_current_are_refused(program):
+    run(program, "other")
 
 
 @pytest.mark.parametrize("order", ["each01", "each10"])
