@@ -24,6 +24,7 @@ _pack_view = struct.Struct("@Pqq").pack
 _pack_sequences = struct.Struct("@PPPiiqi4x").pack
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _current_stream(device: int) -> int:
@@ -32,20 +33,27 @@ def _current_stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
-    """_dev with its checks in one test where all hold."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+def _off_device(t: torch.Tensor, name: str, device: int) -> ValueError:
+    where = f"cuda:{t.get_device()}" if t.is_cuda else str(t.device)
+    return ValueError(f"{name}: must be a CUDA tensor on cuda:{device}, is on {where}")
+
+
+def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
+    """_dev with its checks in one test where all hold, on the device that the call runs on."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
         return t.data_ptr()
-    return _dev(t, name, dtype, shape)
+    _dev(t, name, dtype, shape)
+    raise _off_device(t, name, device)
 
 
-def _view(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, head_dim: int,
+def _view(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, head_dim: int, device: int,
           tokens: Optional[int] = None) -> bytes:
     """A [tokens, heads, head_dim] device tensor whose last dimension is dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.get_device() != device:
+        raise _off_device(t, name, device)
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     shape = t.shape
@@ -59,12 +67,13 @@ def _view(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, head_dim: 
     return _pack_view(t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if heads > 1 else 0)
 
 
-def _norm_weight(g: Optional[torch.Tensor], name: str, head_dim: int) -> int:
-    return 0 if g is None else _ptr(g, name, torch.float32, (head_dim,))
+def _norm_weight(g: Optional[torch.Tensor], name: str, head_dim: int, device: int) -> int:
+    return 0 if g is None else _ptr(g, name, torch.float32, (head_dim,), device)
 
 
 class AttentionPlan:
-    """A validated attention shape bound to the current CUDA device.
+    """A validated attention shape bound to the current CUDA device: its calls are made with that
+    device current, on its tensors.
 
     ``rotary_dim`` elements of each head are rotated (default: all); ``rope_style``
     pairs element i with i + rotary_dim/2 ("halves") or 2i with 2i+1 ("adjacent").
@@ -95,8 +104,9 @@ class AttentionPlan:
         _lib.check(self._lib.engram_attn_workspace_bytes(self._h, ctypes.byref(n)), "engram_attn_workspace_bytes")
         self.workspace_bytes = n.value
 
-    def new_workspace(self, device="cuda") -> torch.Tensor:
+    def new_workspace(self, device=None) -> torch.Tensor:
         """A workspace for attention calls; calls that may run at the same time need one each."""
+        device = torch.device("cuda", self.device) if device is None else device
         ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
         ws[:_COUNTER_BYTES].zero_()
         return ws
@@ -141,7 +151,7 @@ class AttentionPlan:
             return 0, 0
         if not isinstance(rope, torch.Tensor) or rope.dim() != 2 or rope.shape[1] != self.rotary_dim:
             raise ValueError(f"rope: expected a tensor of shape (length, {self.rotary_dim})")
-        return _ptr(rope, "rope", torch.float32, rope.shape), rope.shape[0]
+        return _ptr(rope, "rope", torch.float32, rope.shape, self.device), rope.shape[0]
 
     def qk_norm_rope(self, q: torch.Tensor, k: Optional[torch.Tensor] = None,
                      positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None, *,
@@ -150,22 +160,23 @@ class AttentionPlan:
                      ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
         """Per-head norm (where a weight is given) and rotation of q [T, heads, D] and k
         [T, heads_kv, D] in one launch (engram_qk_norm_rope): dense outputs (q, k)."""
-        D, dt = self.head_dim, self.torch_dtype
+        D, dt, dev = self.head_dim, self.torch_dtype, self.device
         T = q.shape[0]
-        vq = _view(q, "q", dt, self.heads, D)
+        vq = _view(q, "q", dt, self.heads, D, dev)
         if q_out is None:
             q_out = torch.empty(T, self.heads, D, dtype=dt, device=q.device)
         vk, k_ptr = None, 0
         if k is not None:
-            vk = _view(k, "k", dt, self.heads_kv, D, T)
+            vk = _view(k, "k", dt, self.heads_kv, D, dev, T)
             if k_out is None:
                 k_out = torch.empty(T, self.heads_kv, D, dtype=dt, device=q.device)
-            k_ptr = _ptr(k_out, "k_out", dt, (T, self.heads_kv, D))
+            k_ptr = _ptr(k_out, "k_out", dt, (T, self.heads_kv, D), dev)
         rope_ptr, rope_len = self._rope(rope)
-        pos = 0 if positions is None else _ptr(positions, "positions", torch.int32, (T,))
+        pos = 0 if positions is None else _ptr(positions, "positions", torch.int32, (T,), dev)
         _lib.check(self._lib.engram_qk_norm_rope(
-            self._h, vq, vk, T, pos, rope_ptr, rope_len, _norm_weight(g_q, "g_q", D), _norm_weight(g_k, "g_k", D),
-            _ptr(q_out, "q_out", dt, (T, self.heads, D)), k_ptr, _current_stream(self.device)), "engram_qk_norm_rope")
+            self._h, vq, vk, T, pos, rope_ptr, rope_len, _norm_weight(g_q, "g_q", D, dev),
+            _norm_weight(g_k, "g_k", D, dev), _ptr(q_out, "q_out", dt, (T, self.heads, D), dev), k_ptr,
+            _current_stream(dev)), "engram_qk_norm_rope")
         return q_out, k_out
 
 
@@ -182,8 +193,14 @@ class SequenceBatch:
         self.start, self.length, self.table, self.max_new = start, length, table, int(max_new)
         self._fixed = (_dev(start, "start", torch.int32, (B + 1,)), _dev(length, "length", torch.int32, (B,)),
                        _dev(table, "table", torch.int32, (B, table.shape[1])), B, table.shape[1])
+        self.device = start.get_device()
+        for t, name in ((length, "length"), (table, "table")):
+            if t.get_device() != self.device:
+                raise _off_device(t, name, self.device)
 
-    def _struct(self, tokens: int) -> bytes:
+    def _struct(self, tokens: int, device: int) -> bytes:
+        if self.device != device:
+            raise _off_device(self.start, "batch", device)
         return _pack_sequences(*self._fixed, tokens, self.max_new)
 
 
@@ -196,13 +213,14 @@ class PagedCache:
         self.plan, self.k, self.v = plan, k, v
         self._lib = plan._lib
         self._h = ctypes.c_void_p()
-        _lib.check(self._lib.engram_kv_cache_create(plan._h, _dev(k, "k", plan.torch_dtype, shape),
-                                                    _dev(v, "v", plan.torch_dtype, shape), k.shape[0],
+        _lib.check(self._lib.engram_kv_cache_create(plan._h, _ptr(k, "k", plan.torch_dtype, shape, plan.device),
+                                                    _ptr(v, "v", plan.torch_dtype, shape, plan.device), k.shape[0],
                                                     ctypes.byref(self._h)), "engram_kv_cache_create")
 
     @classmethod
-    def empty(cls, plan: AttentionPlan, pages: int, device="cuda") -> "PagedCache":
+    def empty(cls, plan: AttentionPlan, pages: int, device=None) -> "PagedCache":
         shape = (pages, plan.heads_kv, plan.page, plan.head_dim)
+        device = torch.device("cuda", plan.device) if device is None else device
         return cls(plan, torch.empty(shape, dtype=plan.torch_dtype, device=device),
                    torch.empty(shape, dtype=plan.torch_dtype, device=device))
 
@@ -224,18 +242,18 @@ class PagedCache:
         [tokens, heads_kv, D]; with q, also its norm and rotation in the same launch
         (engram_kv_append).  Returns the queries, or None."""
         p = self.plan
-        D, dt, T = p.head_dim, p.torch_dtype, k.shape[0]
-        vk, vv = _view(k, "k", dt, p.heads_kv, D), _view(v, "v", dt, p.heads_kv, D, T)
+        D, dt, dev, T = p.head_dim, p.torch_dtype, p.device, k.shape[0]
+        vk, vv = _view(k, "k", dt, p.heads_kv, D, dev), _view(v, "v", dt, p.heads_kv, D, dev, T)
         vq, q_ptr = None, 0
         if q is not None:
-            vq = _view(q, "q", dt, p.heads, D, T)
+            vq = _view(q, "q", dt, p.heads, D, dev, T)
             if q_out is None:
                 q_out = torch.empty(T, p.heads, D, dtype=dt, device=q.device)
-            q_ptr = _ptr(q_out, "q_out", dt, (T, p.heads, D))
+            q_ptr = _ptr(q_out, "q_out", dt, (T, p.heads, D), dev)
         rope_ptr, rope_len = p._rope(rope)
         _lib.check(self._lib.engram_kv_append(
-            self._h, batch._struct(T), vk, vv, rope_ptr, rope_len, _norm_weight(g_k, "g_k", D), vq,
-            _norm_weight(g_q, "g_q", D), q_ptr, _current_stream(p.device)), "engram_kv_append")
+            self._h, batch._struct(T, dev), vk, vv, rope_ptr, rope_len, _norm_weight(g_k, "g_k", D, dev), vq,
+            _norm_weight(g_q, "g_q", D, dev), q_ptr, _current_stream(dev)), "engram_kv_append")
         return q_out if q is not None else None
 
     def attend(self, batch: SequenceBatch, q: torch.Tensor, *, causal: bool = True, window: int = 0,
@@ -244,21 +262,21 @@ class PagedCache:
         """Attention of the queries [tokens, heads, D] over the cache (engram_paged_attention):
         (out, lse float32 [tokens, heads]).  Without a ``workspace`` the plan keeps one per stream."""
         p = self.plan
-        D, dt, T = p.head_dim, p.torch_dtype, q.shape[0]
-        vq = _view(q, "q", dt, p.heads, D)
+        D, dt, dev, T = p.head_dim, p.torch_dtype, p.device, q.shape[0]
+        vq = _view(q, "q", dt, p.heads, D, dev)
         if out is None:
             out = torch.empty(T, p.heads, D, dtype=dt, device=q.device)
         if lse is None:
             lse = torch.empty(T, p.heads, dtype=torch.float32, device=q.device)
-        s = _current_stream(p.device)
+        s = _current_stream(dev)
         if workspace is None:
             ws = p._workspace(s)
             ws_ptr, ws_bytes = ws.data_ptr(), p.workspace_bytes
         else:
-            ws_ptr, ws_bytes = _dev(workspace, "workspace", torch.uint8), workspace.numel()
+            ws_ptr, ws_bytes = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
         _lib.check(self._lib.engram_paged_attention(
-            self._h, batch._struct(T), vq, int(causal), int(window), _ptr(out, "out", dt, (T, p.heads, D)),
-            _ptr(lse, "lse", torch.float32, (T, p.heads)), ws_ptr, ws_bytes, s), "engram_paged_attention")
+            self._h, batch._struct(T, dev), vq, int(causal), int(window), _ptr(out, "out", dt, (T, p.heads, D), dev),
+            _ptr(lse, "lse", torch.float32, (T, p.heads), dev), ws_ptr, ws_bytes, s), "engram_paged_attention")
         return out, lse
 
 
@@ -273,17 +291,21 @@ def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, u: torch.Tensor, *
     if not isinstance(target, torch.Tensor) or target.dtype not in (torch.float32, torch.bfloat16) or target.dim() != 3:
         raise ValueError("target: expected float32 or bfloat16 [B, S+1, V]")
     B, S1, V = target.shape
-    S = S1 - 1
+    S, dev = S1 - 1, target.get_device()
+    if dev < 0:
+        raise ValueError("target: must be a CUDA tensor")
+    if dev != _current_device():                      # which the launch goes to
+        raise _off_device(target, "target", _current_device())
     if tokens is None:
         tokens = torch.empty(B, S1, dtype=torch.int32, device=target.device)
     if accepted is None:
         accepted = torch.empty(B, dtype=torch.int32, device=target.device)
     i32 = torch.int32
     _lib.check(_lib._lib().engram_verify_drafts(
-        _ptr(target, "target", target.dtype, target.shape),
-        0 if draft_probs is None else _ptr(draft_probs, "draft_probs", target.dtype, (B, S, V)),
-        _lib.F32 if target.dtype is torch.float32 else _lib.BF16, _ptr(drafts, "drafts", i32, (B, S)),
-        0 if n_drafts is None else _ptr(n_drafts, "n_drafts", i32, (B,)), _ptr(u, "u", torch.float32, (B, S1)), B, S, V,
-        _ptr(tokens, "tokens", i32, (B, S1)), _ptr(accepted, "accepted", i32, (B,)),
-        _current_stream(target.device.index)), "engram_verify_drafts")
+        _ptr(target, "target", target.dtype, target.shape, dev),
+        0 if draft_probs is None else _ptr(draft_probs, "draft_probs", target.dtype, (B, S, V), dev),
+        _lib.F32 if target.dtype is torch.float32 else _lib.BF16, _ptr(drafts, "drafts", i32, (B, S), dev),
+        0 if n_drafts is None else _ptr(n_drafts, "n_drafts", i32, (B,), dev), _ptr(u, "u", torch.float32, (B, S1), dev),
+        B, S, V, _ptr(tokens, "tokens", i32, (B, S1), dev), _ptr(accepted, "accepted", i32, (B,), dev),
+        _current_stream(dev)), "engram_verify_drafts")
     return tokens, accepted
