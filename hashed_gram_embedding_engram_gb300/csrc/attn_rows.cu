@@ -183,9 +183,13 @@ __global__ void __launch_bounds__(kNT, 2)
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.ptr) + (w.q.row0 + rr / a.group) * a.q.ts +
                                      (w.h * a.group + rr % a.group) * a.q.hs + qc;
 #pragma unroll
-          for (int k = 0; k < NK; ++k) {
-            qf[t][k][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16)) : 0u;
-            qf[t][k][2 + e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16 + 8)) : 0u;
+          for (int k = 0; k < NK; ++k) qf[t][k][e] = qf[t][k][2 + e] = 0u;
+          if (live) {
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+              qf[t][k][e] = ptx::ld_after_wait(reinterpret_cast<const int32_t*>(src + k * 16));
+              qf[t][k][2 + e] = ptx::ld_after_wait(reinterpret_cast<const int32_t*>(src + k * 16 + 8));
+            }
           }
         }
 #pragma unroll

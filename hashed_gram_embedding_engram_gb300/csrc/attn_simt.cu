@@ -30,18 +30,15 @@ using namespace at;
 constexpr int kNT = 256;
 constexpr int kCost = 2;           // steps that a tile's queries, output and joins are worth
 
-// Volatile: the loads of a step stay where they are issued, before the work on
-// the step before (as plain read-only loads the compiler may sink them past it).
+// The loads of a step also stay where they are issued, before the work on the step
+// before (ordinary ones the compiler may sink past it).
 __device__ __forceinline__ float4 load4(const float* p) {
-  float4 v;
-  asm volatile("ld.global.nc.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
-  return v;
+  return ptx::ld_after_wait(reinterpret_cast<const float4*>(p));
 }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  uint32_t x, y;
-  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "l"(p));
-  return make_float4(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u), __uint_as_float(y << 16),
-                     __uint_as_float(y & 0xFFFF0000u));
+  const uint2 x = ptx::ld_after_wait(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
+                     __uint_as_float(x.y & 0xFFFF0000u));
 }
 
 // DP: D padded to 64, 128 or 256 (the padding is zeros in shared memory).

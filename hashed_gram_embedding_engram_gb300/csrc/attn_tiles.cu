@@ -111,7 +111,8 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Walk& w, u
     const int offset = i * (32 / kLanes) + lane / kLanes;
     const RowMap at = row_at(a, map, offset);
     x[i] = make_uint4(0, 0, 0, 0);
-    if (base + offset < n_rows) x[i] = __ldg(reinterpret_cast<const uint4*>(from + at.token * a.q.ts + at.g * a.q.hs));
+    if (base + offset < n_rows)
+      x[i] = ptx::ld_after_wait(reinterpret_cast<const uint4*>(from + at.token * a.q.ts + at.g * a.q.hs));
   }
 #pragma unroll
   for (int i = 0; i < kLanes / 2; ++i) {

@@ -31,11 +31,11 @@ __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.w
 
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Plain 32-bit loads that keep their place after grid_dep_wait.  A read-only
-// load (__ldg) counts as one of memory that nothing writes while the kernel
-// runs, so the compiler may move it before the wait; under programmatic launch
-// the previous kernel still writes then.  Loads whose addresses come from one
-// of these follow them.
+// Plain loads that keep their place after grid_dep_wait.  A read-only load
+// (__ldg, ld.global.nc, or one that the compiler makes of a const __restrict__
+// pointer) is for memory that nothing writes while the kernel runs; under
+// programmatic launch the kernel runs, up to the wait, while the previous one
+// still writes.  So what an earlier kernel may have written comes by these.
 __device__ __forceinline__ int32_t ld_after_wait(const int32_t* p) {
   int32_t v;
   asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
@@ -44,6 +44,26 @@ __device__ __forceinline__ int32_t ld_after_wait(const int32_t* p) {
 __device__ __forceinline__ float ld_after_wait(const float* p) {
   float v;
   asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_after_wait(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_after_wait(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_after_wait(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ld_after_wait(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
   return v;
 }
 

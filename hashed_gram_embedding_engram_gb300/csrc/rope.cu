@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kNT, 8)
         const float* row = a.rope + static_cast<int64_t>(place.pos) * a.rotary + lane * E;
 #pragma unroll
         for (int c = 0; c < E / 4; ++c) {              // four angles, eight elements
-          const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + c * 4));
-          const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + a.rotary / 2 + c * 4));
+          const float4 c4 = ptx::ld_after_wait(reinterpret_cast<const float4*>(row + c * 4));
+          const float4 s4 = ptx::ld_after_wait(reinterpret_cast<const float4*>(row + a.rotary / 2 + c * 4));
           if (adjacent) {
             const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll

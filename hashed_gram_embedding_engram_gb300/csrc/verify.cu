@@ -31,8 +31,10 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxParts = kMaxCluster * kWarps;
 constexpr int kSteps = 4;         // vectors of a lane in flight, of p and of q
 
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float load_one(const float* p) { return ptx::ld_after_wait(p); }
+__device__ __forceinline__ float load_one(const __nv_bfloat16* p) {
+  return __uint_as_float(static_cast<uint32_t>(ptx::ld_after_wait(reinterpret_cast<const uint16_t*>(p))) << 16);
+}
 
 // floor(x clamped to [0, 1] * 2^38); NaN: 0.  From the binary32 fields: the
 // significand m (24 bits) of 1.0 stands at bit 38, so m << 15, then right by
@@ -60,9 +62,9 @@ __device__ __forceinline__ uint32_t fix_small(float x) {
 template <typename T, int VEC>
 __device__ __forceinline__ void load(const T* p, float (&x)[VEC]) {
   if constexpr (VEC == 1) {
-    x[0] = as_float(*p);
+    x[0] = load_one(p);
   } else {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 v = ptx::ld_after_wait(reinterpret_cast<const uint4*>(p));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -128,9 +130,8 @@ __device__ __forceinline__ uint64_t weight_sum(const float (&x)[VEC], const floa
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kNT, 2)
-    verify_kernel(const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ drafts,
-                  const int32_t* __restrict__ n_drafts, const float* __restrict__ u, int S, int V,
-                  int32_t* __restrict__ tokens, int32_t* __restrict__ accepted, int cluster) {
+    verify_kernel(const T* target, const T* draft, const int32_t* drafts, const int32_t* n_drafts, const float* u,
+                  int S, int V, int32_t* tokens, int32_t* accepted, int cluster) {
   __shared__ uint64_t sums[kMaxParts];      // of every warp of the cluster
   __shared__ uint64_t inner[kWarps];        // of the goal's piece, once more divided
   __shared__ uint64_t s_goal, s_before;
@@ -151,8 +152,8 @@ __global__ void __launch_bounds__(kNT, 2)
         const int x = ptx::ld_after_wait(drafts + static_cast<int64_t>(b) * S + i);
         ok = false;
         if (x >= 0 && x < V) {
-          const uint64_t p = fix(as_float(target[(static_cast<int64_t>(b) * (S + 1) + i) * V + x]));
-          const uint64_t q = draft ? fix(as_float(draft[(static_cast<int64_t>(b) * S + i) * V + x])) : 1ull << 38;
+          const uint64_t p = fix(load_one(target + (static_cast<int64_t>(b) * (S + 1) + i) * V + x));
+          const uint64_t q = draft ? fix(load_one(draft + (static_cast<int64_t>(b) * S + i) * V + x)) : 1ull << 38;
           ok = fix_u(ptx::ld_after_wait(u + static_cast<int64_t>(b) * (S + 1) + i)) * q < p << 24;
         }
       }

@@ -2,6 +2,7 @@
 oracle's own pins."""
 import ctypes
 import os
+import re
 
 import numpy as np
 import pytest
@@ -94,3 +95,15 @@ def test_oracle_verify_draws_the_target_distribution():
                 t, _ = O.verify(target, q[None, None], np.array([[x]]), None, np.array([[(i + .5) / m, (j + .5) / m]]))
                 count[t[0, 0]] += q[x]
     assert np.allclose(count / (m * m), p, atol=1e-9)
+
+
+@pytest.mark.parametrize("source", ["attn_rows.cu", "attn_tiles.cu", "attn_simt.cu", "attn_sched.cuh", "attn_tma.cuh",
+                                    "rope.cu", "verify.cu"])
+def test_no_read_only_loads_under_programmatic_launch(source):
+    """These kernels start while the one before them may still write their inputs (the append the
+    queries and pages, a projection all of them): a read-only load, or a const __restrict__ pointer
+    of which the compiler may make one, is for memory that is not written meanwhile."""
+    from hashed_gram_embedding_engram_gb300 import build
+    with open(os.path.join(build.CSRC, source)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert re.findall(r"__ldg|ld\.global\.nc|__restrict__", code) == []
