@@ -292,7 +292,9 @@ engram_status_t engram_verify_drafts(const void* target, const void* draft_probs
   if (dtype != ENGRAM_F32 && dtype != ENGRAM_BF16) return ENGRAM_ERR_UNSUPPORTED;
   if (B < 0 || B > 65535 || S < 1 || S > 64 || V < 1 || V > (1 << 24)) return ENGRAM_ERR_INVALID_ARG;
   if (B == 0) return ENGRAM_OK;
-  if (!target || !aligned16(target) || !aligned16(draft_probs) || !drafts || !u || !tokens || !accepted)
+  if (!target || !drafts || !u || !tokens || !accepted) return ENGRAM_ERR_INVALID_ARG;
+  const uintptr_t elem = static_cast<uintptr_t>(elem_bytes(dtype));
+  if (reinterpret_cast<uintptr_t>(target) % elem || reinterpret_cast<uintptr_t>(draft_probs) % elem)
     return ENGRAM_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -340,11 +340,13 @@ cudaError_t launch_verify(const void* target, const void* draft, bool is_f32, co
                           const int32_t* n_drafts, const float* u, int B, int S, int V, int32_t* tokens,
                           int32_t* accepted, int num_sms, cudaStream_t s) {
   // 16-byte loads where every row starts on a 16-byte boundary; else one element a lane
+  const bool wide = ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) & 15u) == 0;
   if (is_f32) {
-    if (V % 4 == 0) return run<float, 4>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
+    if (wide && V % 4 == 0)
+      return run<float, 4>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
     return run<float, 1>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
   }
-  if (V % 8 == 0)
+  if (wide && V % 8 == 0)
     return run<__nv_bfloat16, 8>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
   return run<__nv_bfloat16, 1>(target, draft, drafts, n_drafts, u, B, S, V, tokens, accepted, num_sms, s);
 }

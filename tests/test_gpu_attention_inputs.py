@@ -9,8 +9,9 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
-from hashed_gram_embedding_engram_gb300 import PagedCache, SequenceBatch, _lib  # noqa: E402
-from test_gpu_attention import Case  # noqa: E402
+from hashed_gram_embedding_engram_gb300 import _lib, verify_drafts  # noqa: E402
+from oracle import attention_oracle as O  # noqa: E402
+from test_gpu_attention import Case, draft_inputs  # noqa: E402
 
 # one set of sequences for each attention kernel: few rows, chunks, and both of the CUDA cores'
 KERNELS = [dict(new=(1, 2, 1), length=(200, 40, 77), heads=8, heads_kv=2, D=128),
@@ -71,3 +72,24 @@ def test_append_and_attention_leave_out_the_same_sequences(what):
     dropped[c.start[b]:c.start[b + 1]] = True
     assert torch.equal(torch.isneginf(lse).all(1).cpu(), dropped)
     assert c.plan.get_error()[0] == _lib.ERR_INDEX_RANGE
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [257, 1000, 1001])
+def test_draft_check_of_a_slice_of_a_batch(V, dtype):
+    """Probabilities that begin anywhere, as those of some sequences of a batch do where a row is
+    not a multiple of 16 bytes."""
+    target, draft, drafts, u = draft_inputs(6, 2, V, 3, dtype)
+    t, d = target.cuda(), draft.cuda()
+    for b in range(6):
+        x = slice(b, b + 1)
+        want = O.verify(target[x].float().numpy(), draft[x].float().numpy(), drafts[x].numpy(), None, u[x].numpy())
+        for draft_at in (d[x], d[x].clone()):
+            tokens, accepted = verify_drafts(t[x], drafts[x].cuda(), u[x].cuda(), draft_probs=draft_at)
+            assert np.array_equal(tokens.cpu().numpy(), want[0]) and np.array_equal(accepted.cpu().numpy(), want[1])
+        # moved by one element from an aligned place, rows that are a multiple of 16 bytes among them
+        flat = torch.empty(target[x].numel() + 1, dtype=dtype, device="cuda")
+        off = flat[1:].view_as(target[x])
+        off.copy_(t[x])
+        tokens, accepted = verify_drafts(off, drafts[x].cuda(), u[x].cuda(), draft_probs=d[x])
+        assert np.array_equal(tokens.cpu().numpy(), want[0]) and np.array_equal(accepted.cpu().numpy(), want[1])
