@@ -2,7 +2,8 @@
 
 Argument marshalling only, as in engram.py: every step runs in the library's
 CUDA kernels on the current stream, tensors are passed by pointer.  Outputs are
-allocated unless given.
+allocated unless given.  The operators are forward only: in grad mode an input
+that requires a gradient is refused.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ _pack_view = struct.Struct("@Pqq").pack
 _pack_sequences = struct.Struct("@PPPiiqi4x").pack
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+_grad_mode = torch.is_grad_enabled
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -45,6 +47,15 @@ def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: i
         return t.data_ptr()
     _dev(t, name, dtype, shape)
     raise _off_device(t, name, device)
+
+
+def _forward_only(**tensors: Optional[torch.Tensor]) -> None:
+    """In grad mode: the operators record nothing for a backward pass, so an input that asks for a
+    gradient would silently get none.  (The calls look first by themselves: a loop costs a microsecond.)"""
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{name}: requires a gradient, which this operator does not compute; "
+                             "detach it, or call under torch.no_grad()")
 
 
 def _view(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, head_dim: int, device: int,
@@ -160,6 +171,10 @@ class AttentionPlan:
                      ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
         """Per-head norm (where a weight is given) and rotation of q [T, heads, D] and k
         [T, heads_kv, D] in one launch (engram_qk_norm_rope): dense outputs (q, k)."""
+        if _grad_mode() and (q.requires_grad or k is not None and k.requires_grad
+                             or rope is not None and rope.requires_grad or g_q is not None and g_q.requires_grad
+                             or g_k is not None and g_k.requires_grad):
+            _forward_only(q=q, k=k, rope=rope, g_q=g_q, g_k=g_k)
         D, dt, dev = self.head_dim, self.torch_dtype, self.device
         T = q.shape[0]
         vq = _view(q, "q", dt, self.heads, D, dev)
@@ -242,6 +257,10 @@ class PagedCache:
         [tokens, heads_kv, D]; with q, also its norm and rotation in the same launch
         (engram_kv_append).  Returns the queries, or None."""
         p = self.plan
+        if _grad_mode() and (k.requires_grad or v.requires_grad or q is not None and q.requires_grad
+                             or rope is not None and rope.requires_grad or g_q is not None and g_q.requires_grad
+                             or g_k is not None and g_k.requires_grad):
+            _forward_only(k=k, v=v, rope=rope, g_k=g_k, q=q, g_q=g_q)
         D, dt, dev, T = p.head_dim, p.torch_dtype, p.device, k.shape[0]
         vk, vv = _view(k, "k", dt, p.heads_kv, D, dev), _view(v, "v", dt, p.heads_kv, D, dev, T)
         vq, q_ptr = None, 0
@@ -262,6 +281,8 @@ class PagedCache:
         """Attention of the queries [tokens, heads, D] over the cache (engram_paged_attention):
         (out, lse float32 [tokens, heads]).  Without a ``workspace`` the plan keeps one per stream."""
         p = self.plan
+        if _grad_mode() and q.requires_grad:
+            _forward_only(q=q)
         D, dt, dev, T = p.head_dim, p.torch_dtype, p.device, q.shape[0]
         vq = _view(q, "q", dt, p.heads, D, dev)
         if out is None:
@@ -290,6 +311,8 @@ def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, u: torch.Tensor, *
     [B, S+1], accepted int32 [B])."""
     if not isinstance(target, torch.Tensor) or target.dtype not in (torch.float32, torch.bfloat16) or target.dim() != 3:
         raise ValueError("target: expected float32 or bfloat16 [B, S+1, V]")
+    if _grad_mode():
+        _forward_only(target=target, draft_probs=draft_probs, u=u)
     B, S1, V = target.shape
     S, dev = S1 - 1, target.get_device()
     if dev < 0:

@@ -144,3 +144,19 @@ def test_the_plans_own_workspace_is_on_its_device(lib, monkeypatch):
     p.new_workspace()
     p._workspace(0)
     assert made == [torch.device("cuda", 1)] * 2
+
+
+@pytest.mark.parametrize("name,arg", [(n, k) for n, k in NAMES if k in ("q", "k", "v", "rope", "g_q", "g_k", "target",
+                                                                       "draft_probs", "u")])
+def test_inputs_that_require_a_gradient_are_refused(lib, name, arg):
+    call, args = calls()[name]
+    x = args()
+    x[arg].requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        call(**x)
+    assert name not in [n for n, _ in lib.calls]
+    with torch.no_grad():
+        call(**x)
+    with torch.inference_mode():
+        call(**x)
+    assert [n for n, _ in lib.calls].count(name) == 2
