@@ -19,6 +19,8 @@ from .engram import _ACT_DTYPES, _dev, _stream
 _ROPE_STYLES = {"halves": 0, "adjacent": 1}
 _COUNTER_BYTES = 16384      # of a workspace, zero when it is new (engram_attn_workspace_bytes)
 
+_INT_MAX = 2 ** 31 - 1      # ctypes cuts larger whole numbers to their low 32 bits
+
 # engram_heads_view_t and engram_sequences_t as bytes of the call's own: a step's calls take a few
 # microseconds on the device, so the front end must not take longer (a ctypes structure costs three times this)
 _pack_view = struct.Struct("@Pqq").pack
@@ -279,7 +281,8 @@ class PagedCache:
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Attention of the queries [tokens, heads, D] over the cache (engram_paged_attention):
-        (out, lse float32 [tokens, heads]).  Without a ``workspace`` the plan keeps one per stream."""
+        (out, lse float32 [tokens, heads]).  ``window``: keys that a query sees, its own the last
+        (0: all).  Without a ``workspace`` the plan keeps one per stream."""
         p = self.plan
         if _grad_mode() and q.requires_grad:
             _forward_only(q=q)
@@ -296,7 +299,7 @@ class PagedCache:
         else:
             ws_ptr, ws_bytes = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
         _lib.check(self._lib.engram_paged_attention(
-            self._h, batch._struct(T, dev), vq, int(causal), int(window), _ptr(out, "out", dt, (T, p.heads, D), dev),
+            self._h, batch._struct(T, dev), vq, int(causal), min(int(window), _INT_MAX), _ptr(out, "out", dt, (T, p.heads, D), dev),
             _ptr(lse, "lse", torch.float32, (T, p.heads), dev), ws_ptr, ws_bytes, s), "engram_paged_attention")
         return out, lse
 

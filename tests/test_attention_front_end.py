@@ -160,3 +160,13 @@ def test_inputs_that_require_a_gradient_are_refused(lib, name, arg):
     with torch.inference_mode():
         call(**x)
     assert [n for n, _ in lib.calls].count(name) == 2
+
+
+@pytest.mark.parametrize("window,passed", [(0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                           (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 63 - 1, 2 ** 31 - 1)])
+def test_windows_of_any_size_reach_the_library(lib, window, passed):
+    """One longer than any sequence is not cut to its low 32 bits."""
+    call, args = calls()["engram_paged_attention"]
+    call(**args(), window=window)
+    name, at = lib.calls[-1]
+    assert name == "engram_paged_attention" and at[4] == passed
