@@ -99,8 +99,8 @@ class AttentionPlan:
             raise ValueError(f"rope_style: {rope_style!r}, expected one of {sorted(_ROPE_STYLES)}")
         if dtype not in _ACT_DTYPES:
             raise ValueError(f"dtype: {dtype!r}, expected one of {sorted(_ACT_DTYPES)}")
-        if scale is not None and not scale > 0:
-            raise ValueError("scale: must be positive")
+        if scale is not None and not ctypes.c_float(scale).value > 0:     # 0 would mean the default
+            raise ValueError("scale: must be positive as a float32")
         self.heads, self.heads_kv, self.head_dim, self.page = heads, heads_kv, head_dim, page
         self.dtype, self.rope_style, self.eps, self.scale = dtype, rope_style, eps, scale
         self.rotary_dim = head_dim if rotary_dim is None else rotary_dim

@@ -170,3 +170,11 @@ def test_windows_of_any_size_reach_the_library(lib, window, passed):
     call(**args(), window=window)
     name, at = lib.calls[-1]
     assert name == "engram_paged_attention" and at[4] == passed
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), 1e-50])
+def test_scales_that_are_not_positive_floats_are_refused(lib, scale):
+    """1e-50 is 0 as a float32, which would stand for the default scale."""
+    with pytest.raises(ValueError, match="scale"):
+        A.AttentionPlan(heads=H, heads_kv=HKV, head_dim=D, scale=scale)
+    assert lib.calls == []
