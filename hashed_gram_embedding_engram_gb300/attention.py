@@ -259,6 +259,8 @@ class PagedCache:
         [tokens, heads_kv, D]; with q, also its norm and rotation in the same launch
         (engram_kv_append).  Returns the queries, or None."""
         p = self.plan
+        if not p._h:
+            raise ValueError("cache: its plan is closed")
         if _grad_mode() and (k.requires_grad or v.requires_grad or q is not None and q.requires_grad
                              or rope is not None and rope.requires_grad or g_q is not None and g_q.requires_grad
                              or g_k is not None and g_k.requires_grad):
@@ -284,6 +286,8 @@ class PagedCache:
         (out, lse float32 [tokens, heads]).  ``window``: keys that a query sees, its own the last
         (0: all).  Without a ``workspace`` the plan keeps one per stream."""
         p = self.plan
+        if not p._h:
+            raise ValueError("cache: its plan is closed")
         if _grad_mode() and q.requires_grad:
             _forward_only(q=q)
         D, dt, dev, T = p.head_dim, p.torch_dtype, p.device, q.shape[0]

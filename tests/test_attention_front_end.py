@@ -1,5 +1,7 @@
 """The attention sub-block's front end without a GPU: tensors that say they are on a GPU, and a
 stand-in for the library that keeps what it is called with."""
+import ctypes
+
 import pytest
 import torch
 
@@ -50,6 +52,7 @@ I32, F32 = torch.int32, torch.float32
 def plan():
     p = A.AttentionPlan(heads=H, heads_kv=HKV, head_dim=D, page=PAGE)
     p.workspace_bytes = 1 << 16
+    p._h = ctypes.c_void_p(1)
     return p
 
 
@@ -178,3 +181,16 @@ def test_scales_that_are_not_positive_floats_are_refused(lib, scale):
     with pytest.raises(ValueError, match="scale"):
         A.AttentionPlan(heads=H, heads_kv=HKV, head_dim=D, scale=scale)
     assert lib.calls == []
+
+
+@pytest.mark.parametrize("name,args", [("append", append_args), ("attend", attend_args)])
+def test_a_cache_of_a_closed_plan_is_refused(lib, name, args):
+    """The cache's handle points at the plan's."""
+    p = plan()
+    c = cache(p)
+    getattr(c, name)(**args())
+    p.close()
+    n = len(lib.calls)
+    with pytest.raises(ValueError, match="closed"):
+        getattr(c, name)(**args())
+    assert len(lib.calls) == n
