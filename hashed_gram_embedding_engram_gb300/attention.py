@@ -44,9 +44,11 @@ def _off_device(t: torch.Tensor, name: str, device: int) -> ValueError:
 
 def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
     """_dev with its checks in one test where all hold, on the device that the call runs on."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:      # no tensor
+        pass
     _dev(t, name, dtype, shape)
     raise _off_device(t, name, device)
 
@@ -63,13 +65,14 @@ def _forward_only(**tensors: Optional[torch.Tensor]) -> None:
 def _view(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, head_dim: int, device: int,
           tokens: Optional[int] = None) -> bytes:
     """A [tokens, heads, head_dim] device tensor whose last dimension is dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.get_device() != device:
+    try:
+        at, shape = t.get_device(), t.shape
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
+    if at != device:
         raise _off_device(t, name, device)
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or (tokens is not None and shape[0] != tokens):
         raise ValueError(f"{name}: shape {tuple(shape)}, expected "
                          f"({'tokens' if tokens is None else tokens}, {heads}, {head_dim})")
@@ -318,7 +321,8 @@ def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, u: torch.Tensor, *
     [B, S+1], accepted int32 [B])."""
     if not isinstance(target, torch.Tensor) or target.dtype not in (torch.float32, torch.bfloat16) or target.dim() != 3:
         raise ValueError("target: expected float32 or bfloat16 [B, S+1, V]")
-    if _grad_mode():
+    if _grad_mode() and (target.requires_grad or u.requires_grad
+                         or draft_probs is not None and draft_probs.requires_grad):
         _forward_only(target=target, draft_probs=draft_probs, u=u)
     B, S1, V = target.shape
     S, dev = S1 - 1, target.get_device()
