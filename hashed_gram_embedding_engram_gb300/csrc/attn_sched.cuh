@@ -92,13 +92,53 @@ __device__ __forceinline__ RowMap row_at(const AttnArgs& a, const RowMap& m, int
   return {m.token + n, x - n * a.group};
 }
 
-// What a block works on: places [u0, u1) of U, beginning inside tile (b, h, r).
-struct Range {
-  int64_t u0, U;
+// U places cut into C ranges, as equal as they can be: range c is the places from
+// floor(cU / C) to floor((c + 1)U / C).  A 64-bit quotient is a chain of some 700 clocks, so
+// where U has 31 bits (all but absurd calls) quotients are taken in 32.
+struct Cut {
+  int64_t U;
   unsigned each, extra;   // U / C, U % C (where U has 31 bits)
+  int C;
+};
+
+__host__ __device__ __forceinline__ bool cut_small(const Cut& g) { return g.U < 0x7FFFFFFF; }
+
+__host__ __device__ __forceinline__ Cut make_cut(int64_t U, int C) {
+  Cut g{U, 0, 0, C};
+  if (cut_small(g)) {
+    g.each = static_cast<unsigned>(U) / static_cast<unsigned>(C);
+    g.extra = static_cast<unsigned>(U) - g.each * static_cast<unsigned>(C);
+  }
+  return g;
+}
+
+__host__ __device__ __forceinline__ int64_t cut_begin(const Cut& g, unsigned c) {
+  return cut_small(g) ? c * g.each + c * g.extra / static_cast<unsigned>(g.C) : c * g.U / g.C;
+}
+
+// The range that has place u.  In 32 bits an estimate in float is put right by whole-number compares.
+__host__ __device__ __forceinline__ int cut_find(const Cut& g, int64_t u) {
+  if (!cut_small(g)) return static_cast<int>(((u + 1) * g.C - 1) / g.U);
+  auto begin = [&](unsigned c) { return c * g.each + c * g.extra / static_cast<unsigned>(g.C); };
+  const unsigned x = static_cast<unsigned>(u);
+  const float top = static_cast<float>(x) * g.C, all = static_cast<float>(g.U);
+#ifdef __CUDA_ARCH__
+  const float near = __fdividef(top, all);
+#else
+  const float near = top / all;
+#endif
+  unsigned c = near < static_cast<float>(g.C) ? static_cast<unsigned>(near) : static_cast<unsigned>(g.C - 1);
+  while (c + 1 < g.C && begin(c + 1) <= x) ++c;
+  while (c > 0 && begin(c) > x) --c;
+  return static_cast<int>(c);
+}
+
+// What a block works on: places [u0, u1) of the cut, beginning inside tile (b, h, r).
+struct Range {
+  Cut cut;           // into as many ranges as blocks have work
+  int64_t u0;
   int places;        // u1 - u0
   int at;            // the tile's first place, from u0 (not positive)
-  int C;             // blocks that have work
   int b, h, r;
 };
 
@@ -222,25 +262,15 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
   }
   const int C = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));
   const int c = blockIdx.x;
-  const bool small = U < 0x7FFFFFFF;       // quotients in 32 bits (see block_of)
   int64_t u0 = 0, u1 = 0;
-  unsigned each = 0, extra = 0;
+  Cut cut{U, 0, 0, C};
   if (c < C) {
-    if (small) {
-      each = static_cast<unsigned>(U) / static_cast<unsigned>(C);
-      extra = static_cast<unsigned>(U) - each * static_cast<unsigned>(C);
-      u0 = c * each + c * extra / static_cast<unsigned>(C);
-      u1 = (c + 1) * each + (c + 1) * extra / static_cast<unsigned>(C);
-    } else {
-      u0 = c * U / C;
-      u1 = (c + 1) * U / C;
-    }
+    cut = make_cut(U, C);
+    u0 = cut_begin(cut, c);
+    u1 = cut_begin(cut, c + 1);
   }
   if (tid == 0) {
-    out->each = each;
-    out->extra = extra;
-    out->U = U;
-    out->C = C;
+    out->cut = cut;
     out->u0 = u0;
     out->places = static_cast<int>(u1 - u0);
   }
@@ -255,7 +285,7 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
       if (before + upto - mine <= u0 && u0 < before + upto) {   // one thread: sequence base + tid
         const int64_t in = u0 - (before + upto - mine);
         out->b = base + tid;
-        if (small) {
+        if (cut_small(cut)) {
           const unsigned per = static_cast<unsigned>(mine) / static_cast<unsigned>(a.heads_kv);
           const unsigned h = static_cast<unsigned>(in) / per;
           out->h = static_cast<int>(h);
@@ -297,28 +327,14 @@ __device__ void find_range(const AttnArgs& a, Range* out) {
   __syncthreads();
 }
 
-// Block that has place u: the c with floor(cU / C) <= u < floor((c + 1)U / C).
-// A 64-bit quotient is a chain of some 700 clocks, so where U has 31 bits (all
-// but absurd calls) an estimate in float is put right by whole-number compares.
-__device__ __forceinline__ int block_of(const Range& g, int64_t u) {
-  if (g.U >= 0x7FFFFFFF) return static_cast<int>(((u + 1) * g.C - 1) / g.U);
-  auto begin = [&](unsigned c) { return c * g.each + c * g.extra / static_cast<unsigned>(g.C); };
-  const unsigned x = static_cast<unsigned>(u);
-  unsigned c = min(static_cast<unsigned>(__fdividef(static_cast<float>(x) * g.C, static_cast<float>(g.U))),
-                   static_cast<unsigned>(g.C - 1));
-  while (c + 1 < g.C && begin(c + 1) <= x) ++c;
-  while (c > 0 && begin(c) > x) --c;
-  return static_cast<int>(c);
-}
-
 // First and last block with steps of the tile at place `at` of the range.
 template <int kCost>
 __device__ __forceinline__ int first_block(const Range& g, int at) {
-  return block_of(g, g.u0 + at + kCost);
+  return cut_find(g.cut, g.u0 + at + kCost);
 }
 template <int kCost>
 __device__ __forceinline__ int last_block(const Range& g, int at, const Walk& w) {
-  return block_of(g, g.u0 + at + kCost + w.units - 1);
+  return cut_find(g.cut, g.u0 + at + kCost + w.units - 1);
 }
 
 // Partial tiles: slot 2c holds block c's piece of a tile that an earlier block
