@@ -203,8 +203,8 @@ class AttentionPlan:
 class SequenceBatch:
     """The sequences of a step (engram_sequences_t): ``start`` int32 [B+1] rows of the packed
     new tokens, ``length`` int32 [B] tokens in the cache once they are appended, ``table``
-    int32 [B, pages] page ids.  ``max_new``: the most new tokens of a sequence, a launch hint.
-    ``tokens``: rows of the packed arrays, where it is known (else the arrays' own)."""
+    int32 [B, pages] page ids.  ``max_new``: the most new tokens of a sequence, a launch hint
+    (0: unknown).  The tensors are read when a call runs; they are those given here."""
 
     def __init__(self, start: torch.Tensor, length: torch.Tensor, table: torch.Tensor, max_new: int = 0):
         if length.dim() != 1 or table.dim() != 2:

@@ -110,9 +110,9 @@ cudaError_t launch_attention_simt(const engram_attn_plan* p, const AttnArgs& a, 
 // Attention of at most 32 rows a sequence and cache head (new tokens x group) on
 // the tensor cores, where the cache has tensor maps; more rows make more tiles.
 // 16 sequences over 16384 tokens, 8 cache heads, D 128, against the tiles kernel:
-// 16 rows 183 us / 188, 32 rows 188 / 188, 36 rows (two tiles, the keys read
-// twice) 348 / 190; 64 sequences over 2000: 109 / 124, 117 / 124, 213 / 127;
-// ragged drafts of 4 to 24 rows over 100 to 8192: 108 / 116.
+// 16 rows 166 us / 186, 32 rows 179 / 186, 36 rows (two tiles, the keys read
+// twice) 338 / 188; 64 sequences over 2000: 91 / 123, 108 / 124, 202 / 127;
+// ragged drafts of 4 to 24 rows over 100 to 8192: 102 / 115.
 bool attention_rows_applies(const engram_kv_cache* c, int64_t rows);
 cudaError_t launch_attention_rows(const engram_kv_cache* c, const AttnArgs& a, int64_t rows, cudaStream_t s);
 // Attention of longer chunks on the tensor cores, 256 rows a tile.

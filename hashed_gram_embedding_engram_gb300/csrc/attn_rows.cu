@@ -20,9 +20,9 @@
 // Slots past a length hold anything: their scores are replaced by -inf and
 // their values by zeros before the product (0 * NaN is NaN).
 // Measured (32 query heads, 8 cache heads, D 128): single tokens of 256
-// sequences over 1 to 4096 keys 327 us (6.5 TB/s, 0.96 of a plain copy's rate),
-// of three over 30k to 131k 154 us (6.4 TB/s); drafts of 4 to 24 rows over 100
-// to 8192 keys 108 us (5.0 TB/s: the ends of the many short tiles).
+// sequences over 1 to 4096 keys 325 us (6.5 TB/s, 0.96 of a plain copy's rate),
+// of three over 30k to 131k 155 us (6.4 TB/s); drafts of 4 to 24 rows over 100
+// to 8192 keys 102 us (5.3 TB/s: the ends of the many short tiles).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

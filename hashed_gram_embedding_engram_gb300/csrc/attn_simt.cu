@@ -13,9 +13,9 @@
 // on.  Four rows by four keys a thread: with two keys the shared-memory reads
 // (8 cycles of them for 32 products a warp, four warps at a time) were the
 // bound.  Work is divided and joined as attn_sched.cuh says.  What bounds it:
-// the FMA pipe and the shared-memory reads on chunks (RT = 64; fp32, D 128: 33
+// the FMA pipe and the shared-memory reads on chunks (RT = 64; fp32, D 128: 35
 // TFLOP/s, D 64 with a window of 512: 25), the latency of the one or two warps
-// that hold the rows on single tokens (RT = 16; fp32, D 128: 3.5 TB/s).
+// that hold the rows on single tokens (RT = 16; fp32, D 128: 3.6 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

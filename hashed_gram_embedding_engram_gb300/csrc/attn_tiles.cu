@@ -21,13 +21,18 @@
 // The accumulator is brought to a new maximum only when that exceeds the one
 // in use by 2^8 (weights then are at most 2^8, far inside bf16 and float), so
 // the round trip of O through the registers is rare.
+// Weights come from ex2.approx.ftz: its error, 2^-22 of the value, is far below the
+// weights' rounding to bf16 for the second product, and what it flushes to zero
+// (below 2^-126) adds nothing.
 // Slots past a length hold anything: their scores are replaced by -inf, and
 // the issuing warp zeroes their values in shared memory (0 * NaN is NaN).
 // Measured (32 query heads, 8 cache heads, D 128): 4096 tokens behind 4096
-// 295 us (1.40 PFLOP/s, 0.72 of a library product's peak); bound by the step of
-// 128 keys, 2700 clocks against 2048 of products: the score products read both
-// operands from shared memory at its full rate beside the copies that fill it.
-// 16 x 24 tokens over 16384 keys 194 us (5.5 TB/s).
+// 297 us in a graph, 308 as single calls (1.39 and 1.34 PFLOP/s, 0.72 and 0.69 of
+// a library product's peak); bound by the step of 128 keys, 2700 clocks against
+// 2048 of products: the score products read both operands from shared memory at
+// its full rate beside the copies that fill it.  16 and 4 heads of 64, the same
+// tokens: 136 us (0.76 PFLOP/s): half the products a step, the same exponentials.
+// 16 x 24 tokens over 16384 keys 192 us (5.6 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -12,9 +12,10 @@
 // one kind (queries, keys or values): its pointers, strides and norm weights
 // are the same for all its lanes.  All arithmetic is float; the outputs are
 // rounded once.  What bounds it: device memory on long inputs (append of 16388
-// tokens of 32 + 8 heads with their queries 74 us, 5.6 TB/s; 16385 fp32 tokens
-// of 16 + 4 heads of 64 29 us, 5.8 TB/s), the launch and the chain of dependent
-// loads (sequence, page, row of the table) on a decode step (2 and 3 us).
+// tokens of 32 + 8 heads with their queries 74.7 us, 5.5 TB/s; 16385 fp32 tokens
+// of 16 + 4 heads of 64 29.6 us, 5.7 TB/s), the launch and the chain of dependent
+// loads (sequence, page, row of the table) on a decode step (norm 2.3 us, append
+// 3.5 us in a graph).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -114,7 +114,8 @@ engram_status_t engram_qk_norm_rope(const engram_attn_plan_t* plan, const engram
 /* Norm (g_k, or NULL), rotation (at each token's position; rope NULL: none)
  * and append of k, and append of v, in one launch; with q.ptr, the queries'
  * norm and rotation to q_out (dense) in the same launch.  A padding token's
- * query is normed and not rotated. */
+ * query is normed and not rotated.  A position past rope's last row sets
+ * INDEX_RANGE; its token is appended unrotated. */
 engram_status_t engram_kv_append(engram_kv_cache_t* cache, const engram_sequences_t* seq, const engram_heads_view_t* k,
                                  const engram_heads_view_t* v, const float* rope, int rope_len, const float* g_k,
                                  const engram_heads_view_t* q, const float* g_q, void* q_out, engram_stream_t stream);
@@ -125,16 +126,19 @@ engram_status_t engram_kv_append(engram_kv_cache_t* cache, const engram_sequence
  * a length, and in pages that no query sees, does not matter.  A key of the
  * sequence that this query does not see has weight 0 for it; its value has to
  * be finite (0 times infinity or NaN is NaN).  out: dense [tokens, heads, D],
- * rows of no sequence are not written; lse: float [tokens, heads] or NULL.  The scores, the running maximum and
- * sum and the accumulated output are float; for BF16 the weights exp(s - max)
- * are rounded to bf16 for the product with v (their sum is of the unrounded). */
+ * rows of no sequence are not written; lse: float [tokens, heads] or NULL.  The
+ * scores, the running maximum and sum and the accumulated output are float.  For
+ * BF16 with heads of 64 or 128 the weights exp(s - max) are rounded to bf16 for the
+ * product with v (their sum is of the unrounded): with the output's own rounding,
+ * 1.3 to 1.4 times the error of that rounding alone. */
 engram_status_t engram_paged_attention(const engram_kv_cache_t* cache, const engram_sequences_t* seq,
                                        const engram_heads_view_t* q, int causal, int window, void* out, float* lse,
                                        void* workspace, size_t workspace_bytes, engram_stream_t stream);
 
 /* Check of up to S drafted tokens per sequence against the target.
  *   target [B, S+1, V], draft_probs [B, S, V] or NULL (each draft is certain):
- *   F32 or BF16 probabilities, dense.  drafts int32 [B, S]; n_drafts int32 [B]
+ *   F32 or BF16 probabilities, dense, aligned to an element (rows that all start
+ *   on 16 bytes are read faster).  drafts int32 [B, S]; n_drafts int32 [B]
  *   (clamped to [0, S]) or NULL for S each.  u float [B, S+1]: u[b, i] decides
  *   draft i, u[b, S] draws the last token.
  * In whole numbers: fix(x) = floor(x clamped to [0, 1] * 2^38) (NaN: 0), U =
