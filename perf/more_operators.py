@@ -480,7 +480,7 @@ def _plain_sample(s):
     upto = w.cumsum(1)
     total = upto[:, -1]
     goal = _share((s["u"].clamp(0, 1 - 2.0 ** -24) * 2.0 ** 24).to(torch.int64), total, False)
-    token = (upto <= goal[:, None]).sum(1)
+    token = torch.where(temperature > 0, (upto <= goal[:, None]).sum(1), order[:, 0])
     return torch.where(total > 0, token, torch.full_like(token, -1)).to(torch.int32)
 
 
@@ -671,6 +671,8 @@ def _exact_sample(s):
         order = np.lexsort((np.arange(V), -x.astype(np.float64)))
         if 0 < k[r] < V:
             order = order[:int(k[r])]
+        if not t[r] > 0:
+            order = order[:1]
         upto = np.concatenate(([0], np.cumsum(w[order])))
         if p[r] < 1:
             share = math.floor(float(f32(max(p[r], 0))) * 2 ** 24) * int(upto[-1])
