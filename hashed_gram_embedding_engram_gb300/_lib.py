@@ -27,7 +27,9 @@ EXPORTS = ("engram_status_string", "engram_plan_create", "engram_plan_destroy", 
            "engram_forward_split", "engram_stage_a_e4m3", "engram_stage_a_layers_e4m3", "engram_stage_b_e4m3",
            "engram_attn_plan_create", "engram_attn_plan_destroy", "engram_attn_get_error", "engram_attn_workspace_bytes",
            "engram_kv_cache_create", "engram_kv_cache_destroy", "engram_qk_norm_rope", "engram_kv_append",
-           "engram_paged_attention", "engram_verify_drafts")
+           "engram_paged_attention", "engram_verify_drafts", "engram_tree_build", "engram_tree_attention",
+           "engram_tree_accept", "engram_kv_compact", "engram_kv_copy_pages", "engram_pool_free", "engram_pool_fork",
+           "engram_pool_reserve", "engram_pool_workspace_bytes", "engram_sample_tokens")
 
 
 class Config(ctypes.Structure):
@@ -130,6 +132,17 @@ def _lib() -> ctypes.CDLL:
         lib.engram_kv_append.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp]
         lib.engram_paged_attention.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
         lib.engram_verify_drafts.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]
+        # trees, pools and settings as bytes too
+        lib.engram_tree_build.argtypes = [vp, vp, vp, vp, vp]
+        lib.engram_tree_attention.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.engram_tree_accept.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp]
+        lib.engram_kv_compact.argtypes = [vp, vp, vp, i32, vp, vp]
+        lib.engram_kv_copy_pages.argtypes = [vp, vp, i64, vp]
+        lib.engram_pool_free.argtypes = [vp, vp, vp, vp, i64, vp]
+        lib.engram_pool_fork.argtypes = [vp, vp, vp, vp, vp, i64, vp]
+        lib.engram_pool_reserve.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.engram_pool_workspace_bytes.argtypes = [vp, ctypes.POINTER(sz)]
+        lib.engram_sample_tokens.argtypes = [vp, i32, i64, vp, vp, i64, i64, vp, vp]
         for name in EXPORTS:
             if name not in ("engram_status_string", "engram_sm_split_stream"):   # those two return pointers
                 getattr(lib, name).restype = i32

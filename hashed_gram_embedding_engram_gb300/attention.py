@@ -9,12 +9,15 @@ from __future__ import annotations
 
 import ctypes
 import struct
-from typing import Optional, Tuple
+from typing import TYPE_CHECKING, Optional, Tuple
 
 import torch
 
 from . import _lib
 from .engram import _ACT_DTYPES, _dev, _stream
+
+if TYPE_CHECKING:
+    from .decoding import DraftTree
 
 _ROPE_STYLES = {"halves": 0, "adjacent": 1}
 _COUNTER_BYTES = 16384      # of a workspace, zero when it is new (engram_attn_workspace_bytes)
@@ -209,7 +212,7 @@ class SequenceBatch:
     def __init__(self, start: torch.Tensor, length: torch.Tensor, table: torch.Tensor, max_new: int = 0):
         if length.dim() != 1 or table.dim() != 2:
             raise ValueError("length: expected [B]; table: expected [B, pages]")
-        B = length.shape[0]
+        B = self.B = length.shape[0]
         self.start, self.length, self.table, self.max_new = start, length, table, int(max_new)
         self._fixed = (_dev(start, "start", torch.int32, (B + 1,)), _dev(length, "length", torch.int32, (B,)),
                        _dev(table, "table", torch.int32, (B, table.shape[1])), B, table.shape[1])
@@ -309,6 +312,64 @@ class PagedCache:
             self._h, batch._struct(T, dev), vq, int(causal), min(int(window), _INT_MAX), _ptr(out, "out", dt, (T, p.heads, D), dev),
             _ptr(lse, "lse", torch.float32, (T, p.heads), dev), ws_ptr, ws_bytes, s), "engram_paged_attention")
         return out, lse
+
+    def attend_tree(self, tree: "DraftTree", q: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                    ) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Attention of a tree's tokens [tokens, heads, D] over the cache (engram_tree_attention), their
+        keys and values appended before: each sees the cached text and the tokens it descends from.
+        Returns (out, lse) as ``attend`` does."""
+        p = self.plan
+        if not p._h:
+            raise ValueError("cache: its plan is closed")
+        if _grad_mode() and q.requires_grad:
+            _forward_only(q=q)
+        D, dt, dev, T = p.head_dim, p.torch_dtype, p.device, q.shape[0]
+        vq = _view(q, "q", dt, p.heads, D, dev, tree.tokens)
+        packed = tree._struct(dev)
+        if out is None:
+            out = torch.empty(T, p.heads, D, dtype=dt, device=q.device)
+        if lse is None:
+            lse = torch.empty(T, p.heads, dtype=torch.float32, device=q.device)
+        s = _current_stream(dev)
+        if workspace is None:
+            ws = p._workspace(s)
+            ws_ptr, ws_bytes = ws.data_ptr(), p.workspace_bytes
+        else:
+            ws_ptr, ws_bytes = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
+        _lib.check(self._lib.engram_tree_attention(
+            self._h, tree.batch._struct(T, dev), packed, vq, _ptr(out, "out", dt, (T, p.heads, D), dev),
+            _ptr(lse, "lse", torch.float32, (T, p.heads), dev), ws_ptr, ws_bytes, s), "engram_tree_attention")
+        return out, lse
+
+    def compact(self, batch: SequenceBatch, path: torch.Tensor, count: torch.Tensor) -> None:
+        """Move the kept rows of each sequence together, in place: the keys and values of new token
+        ``path[b, i]`` (int32 [B, width], ascending) to the slot of new token i, for i < ``count[b]``
+        (int32 [B]) (engram_kv_compact)."""
+        p = self.plan
+        if not p._h:
+            raise ValueError("cache: its plan is closed")
+        dev, B = p.device, batch.B
+        if not isinstance(path, torch.Tensor) or path.dim() != 2:
+            raise ValueError("path: expected int32 [B, width]")
+        width = path.shape[1]
+        if width > _INT_MAX:
+            raise ValueError("path: more columns than 31 bits count")
+        _lib.check(self._lib.engram_kv_compact(
+            self._h, batch._struct(0, dev), _ptr(path, "path", torch.int32, (B, width), dev), width,
+            _ptr(count, "count", torch.int32, (B,), dev), _current_stream(dev)), "engram_kv_compact")
+
+    def copy_pages(self, pairs: torch.Tensor) -> None:
+        """Copy pages ``pairs[i, 0]`` to ``pairs[i, 1]`` (int32 [n, 2]; a pair with a negative member is left
+        out), keys and values (engram_kv_copy_pages).  No page may be written twice, nor written and read."""
+        p = self.plan
+        if not p._h:
+            raise ValueError("cache: its plan is closed")
+        if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2:
+            raise ValueError("pairs: expected int32 [n, 2]")
+        n = pairs.shape[0]
+        _lib.check(self._lib.engram_kv_copy_pages(self._h, _ptr(pairs, "pairs", torch.int32, (n, 2), p.device), n,
+                                                  _current_stream(p.device)), "engram_kv_copy_pages")
 
 
 def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, u: torch.Tensor, *,

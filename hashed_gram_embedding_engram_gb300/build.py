@@ -21,7 +21,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]
 SOURCES = ["api.cu", "hash.cu", "gather.cu", "gemm.cu", "gemm_pair.cu", "fusion.cu", "tma.cu", "noalloc.cu", "cache.cu", "stage_b.cu", "decode.cu", "quant.cu", "smsplit.cu",
-           "attention.cu", "rope.cu", "attn_simt.cu", "attn_rows.cu", "attn_tiles.cu", "verify.cu"]
+           "attention.cu", "rope.cu", "attn_simt.cu", "attn_rows.cu", "attn_tiles.cu", "verify.cu",
+           "serving.cu", "tree.cu", "pages.cu", "sample.cu"]
 
 
 def nvcc() -> str:

@@ -6,54 +6,11 @@
 #include <cstdint>
 #include <new>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "attn_internal.h"
+#include "attn_host.h"
 
 namespace {
 
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-int elem_bytes(engram_dtype_t t) { return t == ENGRAM_F32 ? 4 : 2; }
-engram_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? ENGRAM_OK : ENGRAM_ERR_CUDA; }
-
-// A plan's calls launch on the current device, which has to be the plan's: its error word,
-// and what its kernels may use, are that device's.
-engram_status_t device_ok(const engram_attn_plan* p) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ENGRAM_ERR_CUDA;
-  return dev == p->device ? ENGRAM_OK : ENGRAM_ERR_INVALID_ARG;
-}
-
-bool view_ok(const engram_heads_view_t* v, engram_dtype_t t) {
-  if (!v || !v->ptr || !aligned16(v->ptr)) return false;
-  const int64_t step = 16 / elem_bytes(t);
-  return v->token_stride >= 0 && v->head_stride >= 0 && v->token_stride % step == 0 && v->head_stride % step == 0;
-}
-
-engram::HeadsView view_of(const engram_heads_view_t* v) {
-  return v ? engram::HeadsView{v->ptr, v->token_stride, v->head_stride} : engram::HeadsView{nullptr, 0, 0};
-}
-
-bool tokens_ok(const engram_attn_plan* p, int64_t tokens) {
-  return tokens >= 0 && tokens * p->cfg.heads <= INT32_MAX;
-}
-
-bool seq_ok(const engram_attn_plan* p, const engram_sequences_t* s) {
-  if (!s || s->B < 0 || s->max_new < 0 || !tokens_ok(p, s->tokens)) return false;
-  if (s->table_pages < 1 || (static_cast<int64_t>(s->table_pages) << p->page_shift) > (1 << 30)) return false;
-  return s->B == 0 || s->tokens == 0 || (s->start && s->length && s->table);
-}
-
-engram::SeqArgs seq_of(const engram_attn_plan* p, const engram_sequences_t* s) {
-  return {s->start, s->length, s->table, s->B, s->table_pages, p->page_shift, static_cast<int>(s->tokens)};
-}
+using namespace engram;
 
 bool rope_ok(const engram_attn_plan* p, const float* rope, int rope_len) {
   return !rope || (aligned16(rope) && rope_len > 0 && p->cfg.rotary_dim > 0);
@@ -257,32 +214,10 @@ engram_status_t engram_paged_attention(const engram_kv_cache_t* cache, const eng
   if (!workspace || workspace_bytes < engram::attn_workspace_bytes(plan)) return ENGRAM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ENGRAM_ERR_INVALID_ARG;
   if (engram_status_t e = device_ok(plan)) return e;
-  engram::AttnArgs a{};
-  a.q = view_of(q);
-  a.k = cache->k;
-  a.v = cache->v;
-  a.pages = cache->pages;
-  a.out = out;
-  a.lse = lse;
-  a.seq = seq_of(plan, seq);
-  a.heads = plan->cfg.heads;
-  a.heads_kv = plan->cfg.heads_kv;
-  a.group = plan->group;
-  a.group_recip = (65536 + plan->group - 1) / plan->group;
-  a.D = plan->cfg.head_dim;
-  a.causal = causal != 0;
+  AttnArgs a = attn_args(cache, seq, q, out, lse, workspace);
+  a.causal = causal != 0 ? kSeesCausal : kSeesAll;
   a.window = window;
-  a.scale_log2 = static_cast<float>(plan->scale * 1.4426950408889634);
-  a.counters = static_cast<uint32_t*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + engram::kAttnCounters * 4);
-  a.err = plan->err;
-  int64_t max_new = seq->max_new > 0 ? seq->max_new : seq->tokens;
-  if (max_new > seq->tokens) max_new = seq->tokens;
-  const int64_t rows = max_new * plan->group;
-  if (engram::attention_rows_applies(cache, rows))
-    return cuda_status(engram::launch_attention_rows(cache, a, rows, (cudaStream_t)stream));
-  if (cache->maps) return cuda_status(engram::launch_attention_tiles(cache, a, (cudaStream_t)stream));
-  return cuda_status(engram::launch_attention_simt(plan, a, static_cast<int>(max_new), (cudaStream_t)stream));
+  return cuda_status(launch_attention(cache, a, seq, (cudaStream_t)stream));
 }
 
 engram_status_t engram_verify_drafts(const void* target, const void* draft_probs, engram_dtype_t dtype,

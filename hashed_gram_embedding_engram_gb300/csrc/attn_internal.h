@@ -17,6 +17,7 @@ struct engram_attn_plan {
   int device;
   int num_sms;
   int simt_grid[2];           // blocks of the CUDA-core kernel, with 16 and with 64 rows a tile
+  int simt_grid_tree[2];      // the same for trees of drafts
   uint32_t* err;              // device error word
 };
 
@@ -78,12 +79,19 @@ struct AttnArgs {
   SeqArgs seq;
   int heads, heads_kv, group, D;
   int group_recip;            // ceil(2^16 / group)
-  int causal, window;
+  int causal, window;         // causal: kSeesAll, kSeesCausal or kSeesTree
   float scale_log2;           // scale * log2(e): scores in powers of two
   uint32_t* counters;         // kAttnCounters words, zero between calls
   float* parts;               // partial tiles (attn_sched.cuh)
   uint32_t* err;
+  const uint32_t* mask;       // trees of drafts: [tokens, words] who sees whom, and [tokens] positions
+  const int32_t* positions;
+  int words;
 };
+
+// Which keys a new token sees: all, those up to its own, or the cached ones and its row of the mask.
+enum Sees { kSeesAll = 0, kSeesCausal = 1, kSeesTree = 2 };
+constexpr int kTreeWords = 8;            // of a row of the mask, at most (32 new tokens each)
 
 constexpr int kAttnCounters = 4096;      // at least the blocks of any attention grid (16384 bytes, as the header says)
 constexpr int kAttnPartRows = 256;       // rows of partial tiles per SM, twice (workspace bound)
@@ -117,6 +125,27 @@ bool attention_rows_applies(const engram_kv_cache* c, int64_t rows);
 cudaError_t launch_attention_rows(const engram_kv_cache* c, const AttnArgs& a, int64_t rows, cudaStream_t s);
 // Attention of longer chunks on the tensor cores, 256 rows a tile.
 cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s);
+// csrc/tree.cu, pages.cu, sample.cu
+cudaError_t launch_tree_build(const SeqArgs& s, const int32_t* parent, const engram_tree_t& t, uint32_t* err,
+                              cudaStream_t stream);
+cudaError_t launch_tree_accept(const SeqArgs& s, const int32_t* parent, const int32_t* tokens, const int32_t* sampled,
+                               int width, int32_t* path, int32_t* count, int32_t* emitted, int32_t* length_out,
+                               uint32_t* err, cudaStream_t stream);
+int64_t copy_pages_blocks(const engram_kv_cache* c);       // of a pair
+cudaError_t launch_copy_pages(const engram_kv_cache* c, const int32_t* pairs, int64_t n, cudaStream_t s);
+cudaError_t launch_compact(const engram_kv_cache* c, const SeqArgs& seq, const int32_t* path, int width,
+                           const int32_t* count, cudaStream_t s);
+cudaError_t launch_pool_free(const engram_attn_plan* plan, const engram_pool_t& p, const int32_t* rows,
+                             const int32_t* keep, int64_t n, cudaStream_t s);
+cudaError_t launch_pool_fork(const engram_attn_plan* plan, const engram_pool_t& p, const int32_t* src,
+                             const int32_t* dst, const int32_t* length, int64_t n, cudaStream_t s);
+size_t pool_workspace_bytes(const engram_pool_t& p);
+cudaError_t launch_pool_reserve(const engram_attn_plan* plan, const engram_pool_t& p, const int32_t* before,
+                                const int32_t* after, int32_t* pairs, int32_t* missing, void* workspace,
+                                cudaStream_t s);
+cudaError_t launch_sample(const void* logits, bool is_f32, int64_t stride, const float* u,
+                          const engram_sampling_t& settings, int64_t R, int V, int32_t* tokens, int num_sms,
+                          cudaStream_t s);
 cudaError_t launch_verify(const void* target, const void* draft, bool is_f32, const int32_t* drafts,
                           const int32_t* n_drafts, const float* u, int B, int S, int V, int32_t* tokens,
                           int32_t* accepted, int num_sms, cudaStream_t s);

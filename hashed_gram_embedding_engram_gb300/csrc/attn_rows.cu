@@ -77,7 +77,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // MT: 16-row groups of a tile.
-template <int D, int MT>
+template <int D, int MT, bool kTree>
 __global__ void __launch_bounds__(kNT, 2)
     attn_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
@@ -108,10 +108,10 @@ __global__ void __launch_bounds__(kNT, 2)
   }
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  find_range<kNT, RT, kKT, kCost>(a, &sh.range);   // ends with a block barrier
+  find_range<kNT, RT, kKT, kCost, kTree>(a, &sh.range);   // ends with a block barrier
   const Range& range = sh.range;
   if (range.places == 0) return;
-  Walk w = walk_begin<RT, kKT>(a, range);
+  Walk w = walk_begin<RT, kKT, kTree>(a, range);
   int u = 0, at = range.at;
 
   if (warp == kWarps) {
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kNT, 2)
       u = piece.next;
       if (u >= range.places) break;
       at = u;
-      walk_next<RT, kKT>(a, w);
+      walk_next<RT, kKT, kTree>(a, w);
     }
     if (*reinterpret_cast<volatile int*>(&sh.abort)) {     // copies in flight land before the block ends
       for (int i = 0; i < filled; ++i) {
@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kNT, 2)
       const int r0 = w.r * RT;
       uint32_t qf[MT][NK][4];
       int lo[MT][2], hi[MT][2];
+      TreeRow tree[kTree ? MT : 1][2];
       float m[MT][2], l[MT][2], o[MT][NC / 8][4];
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kNT, 2)
           const int p = w.q.len - w.q.n + rr / a.group;
           hi[t][e] = !live || p < 0 ? 0 : (a.causal ? p + 1 : w.q.len);
           lo[t][e] = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
+          if constexpr (kTree) tree[t][e] = tree_row(a, w.q, rr / a.group, live);
           m[t][e] = -INFINITY;
           l[t][e] = 0.f;
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.ptr) + (w.q.row0 + rr / a.group) * a.q.ts +
@@ -227,13 +229,16 @@ __global__ void __launch_bounds__(kNT, 2)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float x = -INFINITY;
+            uint32_t sees = 0;
+            if constexpr (kTree) sees = tree_sees(tree[t][e], j0 + warp * 16) >> qc;
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int j = j0 + warp * 16 + n * 8 + qc + i;
                 float& v = s[t][n][e * 2 + i];
-                v = j >= lo[t][e] && j < hi[t][e] ? v * a.scale_log2 : -INFINITY;
+                const bool in = kTree ? sees >> (n * 8 + i) & 1 : j >= lo[t][e] && j < hi[t][e];
+                v = in ? v * a.scale_log2 : -INFINITY;
                 x = fmaxf(x, v);
               }
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
@@ -352,21 +357,24 @@ __global__ void __launch_bounds__(kNT, 2)
     u = piece.next;
     if (u >= range.places) break;
     at = u;
-    walk_next<RT, kKT>(a, w);
+    walk_next<RT, kKT, kTree>(a, w);
   }
 }
 
 template <int D, int MT>
 cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
-  return launch_pdl(attn_rows_kernel<D, MT>, dim3(p->num_sms * 2), dim3(kNT), Cfg<D>::kSmem, s, a, c->k64, c->v64);
+  auto* kernel = a.causal == kSeesTree ? attn_rows_kernel<D, MT, true> : attn_rows_kernel<D, MT, false>;
+  return launch_pdl(kernel, dim3(p->num_sms * 2), dim3(kNT), Cfg<D>::kSmem, s, a, c->k64, c->v64);
 }
 
 template <int D>
 cudaError_t prepare() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_rows_kernel<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_rows_kernel<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  for (auto* kernel : {attn_rows_kernel<D, 1, false>, attn_rows_kernel<D, 2, false>, attn_rows_kernel<D, 1, true>,
+                       attn_rows_kernel<D, 2, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace

@@ -53,14 +53,14 @@ struct KeyRange {
   int lo, hi;
 };
 
-template <int RT>
+template <int RT, bool kTree>
 __device__ __forceinline__ KeyRange key_range(const Seq& q, int G, int r, int causal, int window) {
-  const int i0 = r * RT / G;
+  const int i0 = kTree ? 0 : r * RT / G;     // a tree's tokens are in no order of position
   const int i1 = min(q.n - 1, (r * RT + RT - 1) / G);
   const int p0 = max(q.len - q.n + i0, 0), p1 = q.len - q.n + i1;
   KeyRange k{0, 0};
-  if (p1 < 0) return k;
-  k.hi = causal ? p1 + 1 : q.len;
+  if (p1 < 0 || (kTree && q.len < q.n)) return k;
+  k.hi = !kTree && causal ? p1 + 1 : q.len;
   if (window > 0) k.lo = max(0, p0 - window + 1);
   return k;
 }
@@ -73,6 +73,43 @@ __device__ __forceinline__ int units_of(KeyRange k) {
 template <int RT>
 __device__ __forceinline__ int row_tiles(const Seq& q, int G) {
   return static_cast<int>((static_cast<int64_t>(q.n) * G + RT - 1) / RT);
+}
+
+// What new token i of a tree sees: cached keys [lo, base), and base + j for the set
+// bits j of its row of the mask (none of either if it does not see itself).
+struct TreeRow {
+  const uint32_t* bits;
+  int lo, base, end;  // end: one past the sequence's last key
+  int words;          // 0: no key
+};
+
+__device__ __forceinline__ TreeRow tree_row(const AttnArgs& a, const Seq& q, int i, bool live) {
+  TreeRow t{a.mask, 0, 0, 0, 0};
+  if (!live || q.len < q.n || q.n > 32 * a.words) return t;
+  const int64_t row = static_cast<int64_t>(q.row0) + i;
+  t.bits = a.mask + row * a.words;
+  if (!(ptx::ld_after_wait(reinterpret_cast<const int32_t*>(t.bits) + (i >> 5)) >> (i & 31) & 1)) return t;
+  t.words = a.words;
+  t.base = q.len - q.n;
+  t.end = q.len;
+  // positions below the cached text's end are taken for it: the tile's keys begin where those see
+  if (a.window > 0) t.lo = max(0, max(ptx::ld_after_wait(a.positions + row), t.base) - a.window + 1);
+  return t;
+}
+
+// Bit k, k < 32: whether the token sees key j0 + k.
+__device__ __forceinline__ uint32_t tree_sees(const TreeRow& t, int j0) {
+  const int from = min(max(t.lo - j0, 0), 32), to = min(max(t.base - j0, 0), 32);
+  uint32_t m = to > from ? (to == 32 ? ~0u : (1u << to) - 1) & (~0u << from) : 0u;
+  const int bit = j0 - t.base, w = bit >> 5;       // of the mask's row; words before the first and after the last are 0
+  if (bit > -32) {
+    const int32_t* bits = reinterpret_cast<const int32_t*>(t.bits);
+    const uint32_t lo = w >= 0 && w < t.words ? ptx::ld_after_wait(bits + w) : 0;
+    const uint32_t hi = (bit & 31) && w + 1 < t.words ? ptx::ld_after_wait(bits + w + 1) : 0;
+    const int left = min(max(t.end - j0, 0), 32);
+    m |= __funnelshift_r(lo, hi, bit & 31) & (left == 32 ? ~0u : (1u << left) - 1);
+  }
+  return m;
 }
 
 // New token and head of the group of rows base, base + 1, .. base + 127: one
@@ -151,13 +188,13 @@ struct Walk {
 };
 
 // The tile at (w.b, w.h, w.r); w.q holds sequence w.b.
-template <int RT, int KT>
+template <int RT, int KT, bool kTree = false>
 __device__ __forceinline__ void walk_tile(const AttnArgs& a, Walk& w) {
-  w.k = key_range<RT>(w.q, a.group, w.r, a.causal, a.window);
+  w.k = key_range<RT, kTree>(w.q, a.group, w.r, a.causal, a.window);
   w.units = units_of<KT>(w.k);
 }
 
-template <int RT, int KT>
+template <int RT, int KT, bool kTree = false>
 __device__ __forceinline__ Walk walk_begin(const AttnArgs& a, const Range& g) {
   Walk w;
   w.b = g.b;
@@ -165,11 +202,11 @@ __device__ __forceinline__ Walk walk_begin(const AttnArgs& a, const Range& g) {
   w.r = g.r;
   w.q = load_seq(a.seq, w.b, nullptr);
   w.tiles = row_tiles<RT>(w.q, a.group);
-  walk_tile<RT, KT>(a, w);
+  walk_tile<RT, KT, kTree>(a, w);
   return w;
 }
 
-template <int RT, int KT>
+template <int RT, int KT, bool kTree = false>
 __device__ __forceinline__ void walk_next(const AttnArgs& a, Walk& w) {
   if (++w.r == w.tiles) {
     w.r = 0;
@@ -181,7 +218,7 @@ __device__ __forceinline__ void walk_next(const AttnArgs& a, Walk& w) {
       w.tiles = row_tiles<RT>(w.q, a.group);
     }
   }
-  walk_tile<RT, KT>(a, w);
+  walk_tile<RT, KT, kTree>(a, w);
 }
 
 // The steps [a, b) of a tile that lie in a block's range (none: b <= a), the
@@ -204,13 +241,13 @@ __device__ __forceinline__ Piece piece_of(const Walk& w, const Range& g, int u, 
 // all lengths; the sums are whole numbers, so all blocks agree.  A thread has a
 // sequence; one with several row tiles is summed by the lanes of its warp (as a
 // loop of the one thread, 64 tiles took 80 us).
-template <int NT, int RT, int KT, int kCost>
+template <int NT, int RT, int KT, int kCost, bool kTree = false>
 __device__ void find_range(const AttnArgs& a, Range* out) {
   __shared__ int64_t warp_sum[NT / 32];
   __shared__ int64_t rest;     // places before u0 in its sequence and head
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto tile_units = [&](const Seq& q, int r) {
-    return kCost + units_of<KT>(key_range<RT>(q, a.group, r, a.causal, a.window));
+    return kCost + units_of<KT>(key_range<RT, kTree>(q, a.group, r, a.causal, a.window));
   };
   auto units_per_head = [&](int b, uint32_t* err) -> int64_t {
     Seq q{0, 0, 0};

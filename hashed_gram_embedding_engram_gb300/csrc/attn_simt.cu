@@ -49,7 +49,7 @@ struct Cfg {
   static constexpr int kSmem = (RT * DP + kKT * (DP + 4) + kKT * DP + RT * kKT) * 4;
 };
 
-template <typename T, int DP, int RT>
+template <typename T, int DP, int RT, bool kTree>
 __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 : 1)
     attn_simt_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kKT = Cfg<DP, RT>::kKT;
@@ -68,9 +68,9 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  find_range<kNT, RT, kKT, kCost>(a, &range);
+  find_range<kNT, RT, kKT, kCost, kTree>(a, &range);
   if (range.places == 0) return;
-  Walk w = walk_begin<RT, kKT>(a, range);
+  Walk w = walk_begin<RT, kKT, kTree>(a, range);
   int u = 0, at = range.at;
 
   while (true) {
@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
         *reinterpret_cast<float4*>(Qs + row * DP + d) = v;
       }
       int lo[R], hi[R];
+      TreeRow tree[kTree ? R : 1];
       float m[R], l[R], o[R][CV][4];
 #pragma unroll
       for (int k = 0; k < R; ++k) {
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
         const bool sees = rr < n_rows && p >= 0;
         hi[k] = !sees ? 0 : (a.causal ? p + 1 : w.q.len);
         lo[k] = sees && a.window > 0 ? max(0, p - a.window + 1) : 0;
+        if constexpr (kTree) tree[k] = tree_row(a, w.q, rr / a.group, rr < n_rows);
         m[k] = -INFINITY;
         l[k] = 0.f;
 #pragma unroll
@@ -172,10 +174,18 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
 #pragma unroll
         for (int k = 0; k < R; ++k) {
           float top = m[k];
+          uint32_t sees[K];
+          if constexpr (kTree) {
+#pragma unroll
+            for (int i = 0; i < K; i += 2) {
+              sees[i] = tree_sees(tree[k], j0 + 16 * i) >> tx;
+              sees[i + 1] = sees[i] >> 16;
+            }
+          }
 #pragma unroll
           for (int i = 0; i < K; ++i) {
             const int j = j0 + tx + 16 * i;
-            s[k][i] = j >= lo[k] && j < hi[k] ? s[k][i] * a.scale_log2 : -INFINITY;
+            s[k][i] = (kTree ? (sees[i] & 1) != 0 : j >= lo[k] && j < hi[k]) ? s[k][i] * a.scale_log2 : -INFINITY;
             top = fmaxf(top, s[k][i]);
           }
 #pragma unroll
@@ -269,33 +279,40 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
     u = piece.next;
     if (u >= range.places) break;
     at = u;
-    walk_next<RT, kKT>(a, w);
+    walk_next<RT, kKT, kTree>(a, w);
   }
 }
 
 template <typename T, int DP, int RT>
 cudaError_t run(const engram_attn_plan* p, const AttnArgs& a, cudaStream_t s) {
-  return launch_pdl(attn_simt_kernel<T, DP, RT>, dim3(p->simt_grid[RT == 64]), dim3(kNT), Cfg<DP, RT>::kSmem, s, a);
+  if (a.causal == kSeesTree)
+    return launch_pdl(attn_simt_kernel<T, DP, RT, true>, dim3(p->simt_grid_tree[RT == 64]), dim3(kNT),
+                      Cfg<DP, RT>::kSmem, s, a);
+  return launch_pdl(attn_simt_kernel<T, DP, RT, false>, dim3(p->simt_grid[RT == 64]), dim3(kNT), Cfg<DP, RT>::kSmem, s,
+                    a);
 }
 
-template <typename T, int DP, int RT>
+template <typename T, int DP, int RT, bool kTree>
 cudaError_t prepare(engram_attn_plan* p) {
   constexpr int smem = Cfg<DP, RT>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto* kernel = attn_simt_kernel<T, DP, RT, kTree>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   int n = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_simt_kernel<T, DP, RT>, kNT, smem);
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kNT, smem);
   if (e != cudaSuccess) return e;
   // the workspace holds kAttnPartRows rows of partials an SM, twice
   const int fit = kAttnPartRows / RT;
-  p->simt_grid[RT == 64] = p->num_sms * (n < 1 ? 1 : (n > fit ? fit : n));
+  (kTree ? p->simt_grid_tree : p->simt_grid)[RT == 64] = p->num_sms * (n < 1 ? 1 : (n > fit ? fit : n));
   return cudaSuccess;
 }
 
 template <typename T, int DP>
 cudaError_t prepare_rows(engram_attn_plan* p) {
-  const cudaError_t e = prepare<T, DP, 16>(p);
-  return e != cudaSuccess ? e : prepare<T, DP, 64>(p);
+  cudaError_t e = prepare<T, DP, 16, false>(p);
+  if (e == cudaSuccess) e = prepare<T, DP, 64, false>(p);
+  if (e == cudaSuccess) e = prepare<T, DP, 16, true>(p);
+  return e != cudaSuccess ? e : prepare<T, DP, 64, true>(p);
 }
 
 template <typename T>

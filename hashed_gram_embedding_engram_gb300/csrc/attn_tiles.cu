@@ -127,7 +127,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Walk& w, u
   }
 }
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kNT, 1)
     attn_tiles_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
@@ -169,13 +169,13 @@ __global__ void __launch_bounds__(kNT, 1)
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   ptx::tc_fence_before();
-  find_range<kNT, kRT, kKT, kCost>(a, &sh.range);   // ends with a block barrier
+  find_range<kNT, kRT, kKT, kCost, kTree>(a, &sh.range);   // ends with a block barrier
   ptx::tc_fence_after();
   const Range& range = sh.range;
   const uint32_t tmem = sh.tmem;
 
   if (range.places > 0) {
-    Walk w = walk_begin<kRT, kKT>(a, range);
+    Walk w = walk_begin<kRT, kKT, kTree>(a, range);
     int u = 0, at = range.at;
     // the block starts with 96 registers a thread (640 x 96 = 61440): the last warpgroup gives some of
     // its own to the softmax warps, which hold 64 scores a thread (512 x 112 + 128 x 32 = 61440)
@@ -203,6 +203,8 @@ __global__ void __launch_bounds__(kNT, 1)
           // not sent through the masks of every step (96 rows of 128 took 237 us where 128 took 197)
           const int hi = !live ? 0x7FFFFFFF : (p < 0 ? 0 : (a.causal ? p + 1 : w.q.len));
           const int lo = live && p >= 0 && a.window > 0 ? max(0, p - a.window + 1) : 0;
+          TreeRow tree;
+          if constexpr (kTree) tree = tree_row(a, w.q, at_row.token, live);
           float m = -INFINITY, l = 0.f;
           if (work) {
             ptx::named_barrier(10 + t, 256);       // the tile's warps have read their output from here
@@ -220,7 +222,17 @@ __global__ void __launch_bounds__(kNT, 1)
               ptx::tmem_ld_32x32b_x32(ts + half * 64 + 32, s[1]);
               ptx::tmem_ld_wait();
               const int j1 = j0 + half * 64;
-              if (__any_sync(~0u, j1 < lo || j1 + 64 > hi)) {
+              if constexpr (kTree) {
+                if (__any_sync(~0u, live && (j1 < tree.lo || j1 + 64 > tree.base))) {
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const uint32_t sees = live ? tree_sees(tree, j1 + c * 32) : ~0u;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                      if (!(sees >> i & 1)) s[c][i] = 0xFF800000u;     // -inf
+                  }
+                }
+              } else if (__any_sync(~0u, j1 < lo || j1 + 64 > hi)) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -361,7 +373,7 @@ __global__ void __launch_bounds__(kNT, 1)
         u = piece.next;
         if (u >= range.places) break;
         at = u;
-        walk_next<kRT, kKT>(a, w);
+        walk_next<kRT, kKT, kTree>(a, w);
       }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(kNT, 1)
           u = piece.next;
           if (u >= range.places) break;
           at = u;
-          walk_next<kRT, kKT>(a, w);
+          walk_next<kRT, kKT, kTree>(a, w);
         }
         if (*reinterpret_cast<volatile int*>(&sh.abort)) {     // copies in flight land before the block ends
           for (int i = 0; i < filled; ++i) {
@@ -481,7 +493,7 @@ __global__ void __launch_bounds__(kNT, 1)
           u = piece.next;
           if (u >= range.places) break;
           at = u;
-          walk_next<kRT, kKT>(a, w);
+          walk_next<kRT, kKT, kTree>(a, w);
         }
         if (ptx::elect_one()) ptx::mma_commit(&sh.drain);
         __syncwarp();
@@ -499,15 +511,23 @@ __global__ void __launch_bounds__(kNT, 1)
 
 template <int D>
 cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
-  return launch_pdl(attn_tiles_kernel<D>, dim3(p->num_sms), dim3(kNT), Cfg<D>::kSmem, s, a, c->k128, c->v128);
+  auto* kernel = a.causal == kSeesTree ? attn_tiles_kernel<D, true> : attn_tiles_kernel<D, false>;
+  return launch_pdl(kernel, dim3(p->num_sms), dim3(kNT), Cfg<D>::kSmem, s, a, c->k128, c->v128);
+}
+
+template <int D>
+cudaError_t prepare() {
+  for (auto* kernel : {attn_tiles_kernel<D, false>, attn_tiles_kernel<D, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t prepare_attention_tiles(const engram_attn_plan* p) {
-  if (p->cfg.head_dim == 64)
-    return cudaFuncSetAttribute(attn_tiles_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<64>::kSmem);
-  return cudaFuncSetAttribute(attn_tiles_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::kSmem);
+  return p->cfg.head_dim == 64 ? prepare<64>() : prepare<128>();
 }
 
 cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {

@@ -1,0 +1,358 @@
+// The pages of a cache and the table that names them: rows of pages freed,
+// shared, extended (copy on write), whole pages copied, kept tokens' rows moved
+// together.
+//
+// The state is a count for each page of the table's entries that name it.  A
+// page with count 0 is unused, and pages are taken lowest first, so every call
+// has one result whatever the order of its blocks: there is no list of free
+// pages whose order would depend on it, sums of whole numbers do not, and where
+// two threads could take the same entry an exchange gives it to one.
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "attn_sched.cuh"
+#include "ptx.cuh"
+
+namespace engram {
+namespace {
+
+// ---------------------------------------------------------------- pages copied
+constexpr int kCopyNT = 256;
+constexpr int kCopyVecs = 8;        // 16-byte vectors of a thread, all in flight
+
+// Block (chunk, pair): a chunk of the page's keys, or of its values.
+__global__ void __launch_bounds__(kCopyNT) copy_pages_kernel(uint4* k, uint4* v, int64_t pages, int64_t page_vecs,
+                                                             const int32_t* pairs, int chunks, uint32_t* err) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int64_t pair = blockIdx.x / (2 * chunks);
+  const int part = blockIdx.x - pair * (2 * chunks);
+  const int src = ptx::ld_after_wait(pairs + 2 * pair), dst = ptx::ld_after_wait(pairs + 2 * pair + 1);
+  if (src < 0 || dst < 0) return;
+  if (src >= pages || dst >= pages) {
+    if (threadIdx.x == 0) atomicOr(err, kErrIndexRange);
+    return;
+  }
+  uint4* base = part >= chunks ? v : k;
+  const int64_t first = static_cast<int64_t>(part >= chunks ? part - chunks : part) * (kCopyNT * kCopyVecs);
+  const uint4* from = base + src * page_vecs;
+  uint4* to = base + dst * page_vecs;
+  uint4 x[kCopyVecs];
+#pragma unroll
+  for (int i = 0; i < kCopyVecs; ++i) {
+    const int64_t at = first + i * kCopyNT + threadIdx.x;
+    if (at < page_vecs) x[i] = ptx::ld_after_wait(from + at);
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyVecs; ++i) {
+    const int64_t at = first + i * kCopyNT + threadIdx.x;
+    if (at < page_vecs) to[at] = x[i];
+  }
+}
+
+// ---------------------------------------------------------------- rows moved together
+constexpr int kMoveNT = 256;
+constexpr int kMoveRows = 4;        // rows a thread has in flight
+
+// Block (sequence, cache head, keys or values): rows move in ascending order, a
+// group of them at a time, all read before any is written.  Row i comes from
+// path[i] >= i, and later rows from later places still, so what a group writes
+// no later group reads.
+__global__ void __launch_bounds__(kMoveNT)
+    compact_kernel(uint4* k, uint4* v, int64_t pages, int heads_kv, int row_vecs, SeqArgs s, const int32_t* path,
+                   int width, const int32_t* count, uint32_t* err) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x / (2 * heads_kv), part = blockIdx.x - b * (2 * heads_kv);
+  const int h = part % heads_kv;
+  uint4* cache = part < heads_kv ? k : v;
+  const at::Seq q = at::load_seq(s, b, tid == 0 ? err : nullptr);
+  const int n = ptx::ld_after_wait(count + b);
+  const int32_t* row = path + static_cast<int64_t>(b) * width;
+  bool bad = n < 0 || n > width || (n > 0 && q.len < q.n);
+  for (int i = tid; i < n && !bad; i += kMoveNT) {
+    const int x = ptx::ld_after_wait(row + i);
+    bad = x < 0 || x >= q.n || (i > 0 && ptx::ld_after_wait(row + i - 1) >= x);
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0 && n != 0) atomicOr(err, kErrIndexRange);
+    return;
+  }
+  const int base = q.len - q.n, page = 1 << s.page_shift;
+  const int32_t* table = s.table + static_cast<int64_t>(b) * s.table_pages;
+  auto place = [&](int slot) -> uint4* {
+    const int pid = ptx::ld_after_wait(table + (slot >> s.page_shift));
+    if (pid < 0 || pid >= pages) {
+      atomicOr(err, kErrIndexRange);
+      return nullptr;
+    }
+    return cache + (((static_cast<int64_t>(pid) * heads_kv + h) << s.page_shift) + (slot & (page - 1))) * row_vecs;
+  };
+  const int lanes = kMoveNT / row_vecs, at = tid / row_vecs, vec = tid - at * row_vecs;    // row_vecs <= 64
+  for (int i0 = 0; i0 < n; i0 += lanes * kMoveRows) {
+    uint4 x[kMoveRows];
+    uint4* to[kMoveRows];
+#pragma unroll
+    for (int r = 0; r < kMoveRows; ++r) {
+      const int i = i0 + r * lanes + at;
+      to[r] = nullptr;
+      if (at >= lanes || i >= n) continue;
+      const int from = ptx::ld_after_wait(row + i);
+      if (from == i) continue;
+      const uint4* p = place(base + from);
+      to[r] = place(base + i);
+      if (!p) to[r] = nullptr;
+      if (to[r]) x[r] = ptx::ld_after_wait(p + vec);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kMoveRows; ++r)
+      if (to[r]) to[r][vec] = x[r];
+  }
+}
+
+// ---------------------------------------------------------------- the table
+constexpr int kRowNT = 128;
+
+// One block a row.
+__global__ void __launch_bounds__(kRowNT) pool_free_kernel(engram_pool_t p, int page_shift, const int32_t* rows,
+                                                           const int32_t* keep, uint32_t* err) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int r = ptx::ld_after_wait(rows + blockIdx.x), n = ptx::ld_after_wait(keep + blockIdx.x);
+  if (r < 0 || r >= p.rows || n < 0) {
+    if (threadIdx.x == 0) atomicOr(err, kErrIndexRange);
+    return;
+  }
+  int32_t* row = p.table + static_cast<int64_t>(r) * p.table_pages;
+  const int first = (n >> page_shift) + ((n & ((1 << page_shift) - 1)) != 0);
+  for (int g = first + threadIdx.x; g < p.table_pages; g += kRowNT) {
+    const int e = ptx::ld_after_wait(row + g);
+    if (e < 0) continue;
+    if (e >= p.pages) {
+      atomicOr(err, kErrIndexRange);
+      continue;
+    }
+    if (atomicExch(row + g, -1) != e) continue;       // the row is named twice, and the other block has it
+    if (atomicSub(p.ref + e, 1) <= 0) {
+      atomicAdd(p.ref + e, 1);
+      atomicOr(err, kErrIndexRange);
+    }
+  }
+}
+
+// One block a pair.  What makes a pair good is read from src, dst and its own row alone, so no
+// block's answer depends on how far another is.
+__global__ void __launch_bounds__(kRowNT) pool_fork_kernel(engram_pool_t p, int page_shift, const int32_t* src,
+                                                           const int32_t* dst, const int32_t* length, int n,
+                                                           uint32_t* err) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int a = ptx::ld_after_wait(src + i), d = ptx::ld_after_wait(dst + i), len = ptx::ld_after_wait(length + i);
+  bool bad = a < 0 || a >= p.rows || d < 0 || d >= p.rows || a == d || len < 0 ||
+             len > static_cast<int64_t>(p.table_pages) << page_shift;
+  for (int j = tid; j < n; j += kRowNT) {
+    const int x = ptx::ld_after_wait(src + j), y = ptx::ld_after_wait(dst + j);
+    bad = bad || x == d || y == a || (j != i && y == d);
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) atomicOr(err, kErrIndexRange);
+    return;
+  }
+  const int32_t* from = p.table + static_cast<int64_t>(a) * p.table_pages;
+  int32_t* to = p.table + static_cast<int64_t>(d) * p.table_pages;
+  const int used = (len >> page_shift) + ((len & ((1 << page_shift) - 1)) != 0);
+  for (int g = tid; g < p.table_pages; g += kRowNT) {
+    bad = bad || ptx::ld_after_wait(to + g) >= 0;
+    if (g < used) {
+      const int e = ptx::ld_after_wait(from + g);
+      bad = bad || e < 0 || e >= p.pages;
+    }
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) atomicOr(err, kErrIndexRange);
+    return;
+  }
+  for (int g = tid; g < used; g += kRowNT) {
+    const int e = ptx::ld_after_wait(from + g);
+    to[g] = e;
+    atomicAdd(p.ref + e, 1);
+  }
+}
+
+constexpr int kReserveNT = 1024;
+constexpr int kReserveWarps = kReserveNT / 32;
+
+// Sum over the block, and each thread's share before it.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& total, int64_t* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += t;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+  for (int w = 0; w < kReserveWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  return before + inc - v;
+}
+
+// One block, so that its barriers part the steps: count what each row needs,
+// find as many unused pages, hand them out, drop the counts of those replaced
+// (all rows look at the counts that the call began with).
+// first: [rows] of a row's place in the line of taken pages; taken, old: [pages].
+__global__ void __launch_bounds__(kReserveNT)
+    pool_reserve_kernel(engram_pool_t p, int page_shift, const int32_t* before, const int32_t* after, int32_t* pairs,
+                        int32_t* missing, int64_t* first, int32_t* taken, int32_t* old, uint32_t* err) {
+  __shared__ int64_t warp_sum[kReserveWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  // the pages [lo, hi) of row r that will be written
+  auto range = [&](int r, int& lo, int& hi, int& n0, bool tell) {
+    n0 = ptx::ld_after_wait(before + r);
+    const int n1 = ptx::ld_after_wait(after + r);
+    lo = hi = 0;
+    if (n1 <= n0) return;
+    if (n0 < 0 || n1 > static_cast<int64_t>(p.table_pages) << page_shift) {
+      if (tell) atomicOr(err, kErrIndexRange);
+      return;
+    }
+    lo = n0 >> page_shift;
+    hi = ((n1 - 1) >> page_shift) + 1;
+  };
+  // 0: the entry stays; 1: a page is taken; 2: in place of a shared one
+  auto needs = [&](int e, bool tell) {
+    if (e < 0) return 1;
+    if (e >= p.pages) {
+      if (tell) atomicOr(err, kErrIndexRange);
+      return 0;
+    }
+    return ptx::ld_after_wait(p.ref + e) > 1 ? 2 : 0;
+  };
+  for (int r = warp; r < p.rows; r += kReserveWarps) {
+    int lo, hi, n0, n = 0;
+    range(r, lo, hi, n0, lane == 0);
+    const int32_t* row = p.table + static_cast<int64_t>(r) * p.table_pages;
+    for (int g0 = lo; g0 < hi; g0 += 32) {
+      const int g = g0 + lane;
+      const bool need = g < hi && needs(ptx::ld_after_wait(row + min(g, hi - 1)), true) != 0;
+      n += __popc(__ballot_sync(~0u, need));
+    }
+    if (lane == 0) first[r] = n;
+  }
+  __syncthreads();
+  int64_t wanted = 0;
+  for (int r0 = 0; r0 < p.rows; r0 += kReserveNT) {
+    const int r = r0 + tid;
+    int64_t total;
+    const int64_t n = r < p.rows ? first[r] : 0;
+    const int64_t at = wanted + block_scan(n, total, warp_sum);
+    if (r < p.rows) first[r] = at;
+    wanted += total;
+  }
+  int64_t found = 0;
+  for (int64_t g0 = 0; g0 < p.pages && found < wanted; g0 += kReserveNT) {
+    const int64_t g = g0 + tid;
+    int64_t total;
+    const bool unused = g < p.pages && ptx::ld_after_wait(p.ref + g) <= 0;
+    const int64_t at = found + block_scan(unused, total, warp_sum);
+    if (unused) taken[at] = static_cast<int32_t>(g);
+    found += total;
+  }
+  const bool enough = found >= wanted;
+  if (tid == 0) *missing = enough ? 0 : static_cast<int32_t>(min(wanted - found, static_cast<int64_t>(INT32_MAX)));
+  __syncthreads();
+  for (int r = warp; r < p.rows; r += kReserveWarps) {
+    int lo, hi, n0;
+    range(r, lo, hi, n0, false);
+    int32_t* row = p.table + static_cast<int64_t>(r) * p.table_pages;
+    int from = -1, to = -1;
+    int64_t at = enough ? first[r] : 0;
+    for (int g0 = enough ? lo : hi; g0 < hi; g0 += 32) {
+      const int g = g0 + lane;
+      const int e = ptx::ld_after_wait(row + min(g, hi - 1));
+      const int need = g < hi ? needs(e, false) : 0;
+      const uint32_t some = __ballot_sync(~0u, need != 0);
+      if (need) {
+        const int64_t x = at + __popc(some & ((1u << lane) - 1));
+        const int fresh = taken[x];
+        old[x] = need == 2 ? e : -1;
+        row[g] = fresh;
+        if (need == 2 && (static_cast<int64_t>(g) << page_shift) < n0) from = e, to = fresh;   // lane 0 of the first turn
+      }
+      at += __popc(some);
+    }
+    if (lane == 0) {
+      pairs[2 * static_cast<int64_t>(r)] = from;
+      pairs[2 * static_cast<int64_t>(r) + 1] = to;
+    }
+  }
+  __syncthreads();
+  if (!enough) return;
+  for (int64_t x = tid; x < wanted; x += kReserveNT) {
+    atomicAdd(p.ref + taken[x], 1);
+    if (old[x] >= 0) atomicSub(p.ref + old[x], 1);
+  }
+}
+
+}  // namespace
+
+static int64_t page_vecs(const engram_attn_config_t& g) {
+  return static_cast<int64_t>(g.heads_kv) * g.page * g.head_dim * (g.dtype == ENGRAM_F32 ? 4 : 2) / 16;
+}
+
+int64_t copy_pages_blocks(const engram_kv_cache* c) {
+  return 2 * ((page_vecs(c->plan->cfg) + kCopyNT * kCopyVecs - 1) / (kCopyNT * kCopyVecs));
+}
+
+cudaError_t launch_copy_pages(const engram_kv_cache* c, const int32_t* pairs, int64_t n, cudaStream_t s) {
+  const int64_t blocks = copy_pages_blocks(c);
+  return launch_pdl(copy_pages_kernel, dim3(static_cast<unsigned>(blocks * n)), dim3(kCopyNT), 0, s,
+                    static_cast<uint4*>(c->k), static_cast<uint4*>(c->v), c->pages, page_vecs(c->plan->cfg), pairs,
+                    static_cast<int>(blocks / 2), c->plan->err);
+}
+
+cudaError_t launch_compact(const engram_kv_cache* c, const SeqArgs& seq, const int32_t* path, int width,
+                           const int32_t* count, cudaStream_t s) {
+  const engram_attn_config_t& g = c->plan->cfg;
+  const int vecs = g.head_dim * (g.dtype == ENGRAM_F32 ? 4 : 2) / 16;
+  return launch_pdl(compact_kernel, dim3(static_cast<unsigned>(seq.B) * 2 * g.heads_kv), dim3(kMoveNT), 0, s, static_cast<uint4*>(c->k),
+                    static_cast<uint4*>(c->v), c->pages, g.heads_kv, vecs, seq, path, width, count, c->plan->err);
+}
+
+cudaError_t launch_pool_free(const engram_attn_plan* plan, const engram_pool_t& p, const int32_t* rows,
+                             const int32_t* keep, int64_t n, cudaStream_t s) {
+  return launch_pdl(pool_free_kernel, dim3(static_cast<unsigned>(n)), dim3(kRowNT), 0, s, p, plan->page_shift, rows,
+                    keep, plan->err);
+}
+
+cudaError_t launch_pool_fork(const engram_attn_plan* plan, const engram_pool_t& p, const int32_t* src,
+                             const int32_t* dst, const int32_t* length, int64_t n, cudaStream_t s) {
+  return launch_pdl(pool_fork_kernel, dim3(static_cast<unsigned>(n)), dim3(kRowNT), 0, s, p, plan->page_shift, src, dst,
+                    length, static_cast<int>(n), plan->err);
+}
+
+size_t pool_workspace_bytes(const engram_pool_t& p) {
+  return static_cast<size_t>(p.rows) * 8 + static_cast<size_t>(p.pages) * 8;
+}
+
+cudaError_t launch_pool_reserve(const engram_attn_plan* plan, const engram_pool_t& p, const int32_t* before,
+                                const int32_t* after, int32_t* pairs, int32_t* missing, void* workspace,
+                                cudaStream_t s) {
+  int64_t* first = static_cast<int64_t*>(workspace);
+  int32_t* taken = reinterpret_cast<int32_t*>(first + p.rows);
+  return launch_pdl(pool_reserve_kernel, dim3(1), dim3(kReserveNT), 0, s, p, plan->page_shift, before, after, pairs,
+                    missing, first, taken, taken + p.pages, plan->err);
+}
+
+}  // namespace engram

@@ -15,6 +15,10 @@
  *                     keys j, lse = ln sum_j exp(scale q.k_j)
  *   draft check       accept drafts while u < p(x) / q(x); then one more token
  *                     from the rest of the target's probability
+ *   trees of drafts   attention of tokens that see the cached text and the drafts
+ *                     they descend from; the path that sampled tokens take
+ *   pages             freed, shared, extended (copy on write), copied, compacted
+ *   sampling          a token from logits: temperature, top-k, top-p, min-p
  *
  * Conventions are those of engram.h: stream-ordered calls, host-checked
  * arguments, caller-owned buffers, status codes, an error word per plan.
@@ -154,6 +158,154 @@ engram_status_t engram_paged_attention(const engram_kv_cache_t* cache, const eng
 engram_status_t engram_verify_drafts(const void* target, const void* draft_probs, engram_dtype_t dtype,
                                      const int32_t* drafts, const int32_t* n_drafts, const float* u, int B, int S,
                                      int V, int32_t* tokens, int32_t* accepted, engram_stream_t stream);
+
+/* ---- Trees of drafted tokens -------------------------------------------------
+ * A sequence's new tokens may be a tree instead of a chain: new token i (in slot
+ * length[b] - n_b + i of the cache, as engram_kv_append puts it) follows new
+ * token parent[i] < i of its sequence, or the cached text (parent -1).  It sees
+ * the cached tokens, the tokens it descends from and itself, and its position
+ * is length[b] - n_b + its depth, the number of new tokens before it.  A
+ * sequence with length[b] < n_b is idle: its tokens have position 0 and see no
+ * key.  A step: engram_tree_build; for each layer engram_qk_norm_rope at
+ * `positions`, engram_kv_append without a rope table, engram_tree_attention;
+ * then engram_sample_tokens at every new token, engram_tree_accept, and for
+ * each layer engram_kv_compact. */
+
+/* Who sees whom, and where: device arrays that engram_tree_build fills. */
+typedef struct {
+  uint32_t* mask;               /* [tokens, words]: bit j & 31 of word j >> 5 of row start[b] + i: new token i sees new
+                                   token j.  A token that does not see itself sees no key at all */
+  int32_t* positions;           /* [tokens] */
+  int words;                    /* 1 <= words <= 8; a sequence has at most 32 words new tokens */
+  int window;                   /* >= 0: as in engram_paged_attention, between positions */
+} engram_tree_t;
+
+/* Fill tree's mask and positions from parent, int32 [tokens].  A parent outside
+ * [-1, i) sets INDEX_RANGE; its token and those below it see no key and have
+ * position 0, as have all tokens of a sequence with more than 32 words of them
+ * (INDEX_RANGE too).  Rows of no sequence are not written. */
+engram_status_t engram_tree_build(const engram_attn_plan_t* plan, const engram_sequences_t* seq, const int32_t* parent,
+                                  const engram_tree_t* tree, engram_stream_t stream);
+
+/* engram_paged_attention with the tree's mask in place of the causal one: new
+ * token i sees cached key j < length[b] - n_b if j > positions[i] - window
+ * (window > 0), and the new tokens of its mask's row.  Positions count from
+ * length[b] - n_b at least: smaller ones are taken for that.  The rest is as
+ * there: workspace, rows without keys, values that have to be finite. */
+engram_status_t engram_tree_attention(const engram_kv_cache_t* cache, const engram_sequences_t* seq,
+                                      const engram_tree_t* tree, const engram_heads_view_t* q, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, engram_stream_t stream);
+
+/* The path that sampled tokens take down the tree.  New token 0 is the text's
+ * last token and is kept; while the path has fewer than `width` tokens, it goes
+ * from token i to the lowest j > i with parent[j] = i and tokens[j] = sampled[i].
+ * parent, tokens, sampled: int32 [tokens], the new tokens and what was drawn
+ * after each.  path int32 [B, width]: the kept tokens' numbers, then -1; count
+ * int32 [B]: how many (0 for an idle sequence or one without new tokens);
+ * emitted int32 [B, width]: sampled at each of them, then -1: the step's text,
+ * its last token not yet in the cache; length_out int32 [B]: length[b] - n_b +
+ * count (at least 0).  1 <= width <= 256. */
+engram_status_t engram_tree_accept(const engram_attn_plan_t* plan, const engram_sequences_t* seq, const int32_t* parent,
+                                   const int32_t* tokens, const int32_t* sampled, int width, int32_t* path,
+                                   int32_t* count, int32_t* emitted, int32_t* length_out, engram_stream_t stream);
+
+/* Move kept rows together, in place: keys and values of slot length[b] - n_b +
+ * path[b, i] to slot length[b] - n_b + i, for i < count[b], as if all were read
+ * before the first is written.  path int32 [B, width], rows strictly ascending
+ * from at least 0 and below n_b; a row that is not, or a count outside [0,
+ * width], sets INDEX_RANGE and moves nothing of its sequence; a page id outside
+ * the cache sets INDEX_RANGE and its tokens are left out.  Other slots are not
+ * written.  Two sequences that share a written page give either's rows there.
+ * With n_b = length[b] it is the whole sequence that is thinned out.  seq->tokens
+ * and max_new are not looked at. */
+engram_status_t engram_kv_compact(engram_kv_cache_t* cache, const engram_sequences_t* seq, const int32_t* path,
+                                  int width, const int32_t* count, engram_stream_t stream);
+
+/* Copy whole pages, keys and values: page pairs[2 i] to page pairs[2 i + 1], i <
+ * n.  Pairs with a negative member are left out; one with a member past the cache
+ * sets INDEX_RANGE and is left out.  No page may be written twice, nor written
+ * and read, in one call (such pages' contents are then undefined). */
+engram_status_t engram_kv_copy_pages(engram_kv_cache_t* cache, const int32_t* pairs, int64_t n, engram_stream_t stream);
+
+/* ---- Pages shared among sequences -------------------------------------------
+ * The caller owns the page table that engram_sequences_t reads and a count of
+ * the rows' entries that name each page; these calls keep the two in step.  An
+ * entry below 0 names no page, a page with count 0 is unused.  All layers' caches
+ * share one table: copies that a call asks for are made in each.  Pages are
+ * taken lowest first, so the result does not depend on the launch.  Calls on one
+ * pool run one after another. */
+typedef struct {
+  int32_t* table;               /* [rows, table_pages] */
+  int32_t* ref;                 /* [pages] */
+  int rows;                     /* >= 0 */
+  int table_pages;              /* >= 1, table_pages * page <= 2^30 */
+  int64_t pages;                /* 1 <= pages < 2^31 */
+} engram_pool_t;
+
+/* Entries of row rows[i] from page ceil(keep[i] / page) on become -1 and their
+ * pages' counts drop by one.  rows, keep: int32 [n]; a row outside the table, a
+ * negative keep and an entry past the pool set INDEX_RANGE and change nothing; a
+ * page whose count is 0 already sets it and keeps that.  A row named twice keeps
+ * the lesser. */
+engram_status_t engram_pool_free(const engram_attn_plan_t* plan, const engram_pool_t* pool, const int32_t* rows,
+                                 const int32_t* keep, int64_t n, engram_stream_t stream);
+
+/* Row dst[i] gets the first ceil(length[i] / page) entries of row src[i]; each
+ * page's count rises by one.  Row dst[i] has to be without pages.  INDEX_RANGE,
+ * and the pair is left out: a row outside the table, dst[i] named by any other
+ * dst or any src, a dst with an entry, a length outside [0, table_pages * page]
+ * or past src's pages, or an entry past the pool. */
+engram_status_t engram_pool_fork(const engram_attn_plan_t* plan, const engram_pool_t* pool, const int32_t* src,
+                                 const int32_t* dst, const int32_t* length, int64_t n, engram_stream_t stream);
+
+/* Make every row's pages ready for its tokens before[r] .. after[r] - 1 to be
+ * written (before, after: int32 [rows]; after <= before: nothing).  A page of
+ * these that the row does not have is taken, and so is one in place of a page
+ * whose count was above 1 when the call began; if that page holds earlier tokens
+ * of the row, pairs[r] is (its id, the new one) for engram_kv_copy_pages, else
+ * (-1, -1).  pairs int32 [rows, 2].  missing int32 [1]: 0, or the pages that were
+ * too few; then nothing else is changed and no pair is given.  A negative before
+ * or an after past the table's row sets INDEX_RANGE and leaves its row out; an
+ * entry past the pool sets it and stays.  workspace: engram_pool_workspace_bytes,
+ * 16-byte aligned, contents irrelevant. */
+engram_status_t engram_pool_reserve(const engram_attn_plan_t* plan, const engram_pool_t* pool, const int32_t* before,
+                                    const int32_t* after, int32_t* pairs, int32_t* missing, void* workspace,
+                                    size_t workspace_bytes, engram_stream_t stream);
+engram_status_t engram_pool_workspace_bytes(const engram_pool_t* pool, size_t* bytes);
+
+/* ---- Tokens from logits -------------------------------------------------------
+ * Each setting: float (top_k int32) [R] in device memory, or NULL: the value
+ * beside it for all rows. */
+typedef struct {
+  const float* temperature;     /* > 0, else greedy: the lowest index of the largest logits */
+  const int32_t* top_k;         /* < 1 or > V: off */
+  const float* top_p;           /* >= 1 or NaN: off */
+  const float* min_p;           /* <= 0 or NaN: off */
+  float temperature_all;
+  int top_k_all;
+  float top_p_all;
+  float min_p_all;
+} engram_sampling_t;
+
+/* One token of each row of logits [R, V] (F32 or BF16, aligned to an element, rows
+ * row_stride >= V elements apart), drawn with u [R].  NaN counts as -inf.  With m the row's
+ * largest logit l_j, in float operations that each round to nearest:
+ *   a_j = 0 where l_j = m, else min((m - l_j) (log2(e) / temperature), 64) (a NaN: 64)
+ *   n_j = a_j rounded to a whole number (halves to even), f = a_j - n_j,
+ *   E_j = P(f) 2^-n_j, P the polynomial of degree 6 evaluated as ((c6 f + c5) f + ..) f + 1
+ *         (csrc/sample_parts.cuh) with P(f) = 2^-f to 1.0e-7
+ * and then in whole numbers, which do not depend on the order of sums:
+ *   w_j = floor(2^38 E_j) (0 where l_j = -inf);
+ *   top-k: the first top_k tokens by (l descending, index ascending) are kept;
+ *   top-p: of these, in that order, those with fewer than max(1, ceil(p total)) of
+ *          weight before them, total all of the kept weight, p = floor(2^24 top_p) / 2^24;
+ *   min-p: of these, those with w_j >= floor(2^38 min_p);
+ *   the token: the lowest j of the kept with w_0 + .. + w_j > floor(U total / 2^24),
+ *          U = floor(u clamped to [0, 1 - 2^-24] * 2^24) (NaN: 0).
+ * tokens int32 [R]; -1 where every logit is -inf.  0 <= R < 2^24, 1 <= V <= 2^24. */
+engram_status_t engram_sample_tokens(const void* logits, engram_dtype_t dtype, int64_t row_stride, const float* u,
+                                     const engram_sampling_t* settings, int64_t R, int64_t V, int32_t* tokens,
+                                     engram_stream_t stream);
 
 #ifdef __cplusplus
 }
