@@ -4,14 +4,25 @@
 // Weights are whole numbers (sample_parts.cuh), so sums have one value in any
 // order and the token does not depend on how a row is split over threads, warps
 // and blocks.  What is kept is a prefix of the tokens in the order (logit
-// descending, index ascending): all logits above a border, and the first so many
-// that equal it.  Borders are found digit by digit of the logits' order-keeping
-// bits, from the top: a histogram of one digit over the tokens that share the
-// digits before it, by count (top-k) or by weight (top-p).
+// descending, index ascending); finding where it ends without sorting the row is
+// the work.
 //
 // A cluster of 1 to 8 blocks has a row, every warp a contiguous piece of it (so
 // that sums over pieces are in the order of the indexes).  The row is read from
-// device memory once and kept in shared memory where it fits.
+// device memory once and kept in shared memory where it fits.  Then, by settings:
+//   * none, or min-p: each warp's weight; the warp whose piece holds the goal finds
+//     the index.
+//   * top-k: every thread's largest logit is known from the load.  The j-th largest
+//     of a block's 512, j = ceil(k / blocks), is exceeded j times in each block,
+//     so the least of the blocks' bounds lies below the k-th logit, and little
+//     below it: what reaches it (about 1.2 k tokens) goes to the first block, which
+//     sorts it; top-p and the draw happen on that list.
+//   * top-p alone: a histogram of weights over a, in steps of 2^(1/128), says to
+//     within 2^-13 where the running weight reaches its goal; the few tokens of that
+//     band go to the first block, which sorts them and has the exact end.
+//   * what is too much for the list (thousands of ties, a large k, a goal in the
+//     far tail): borders digit by digit of the logits' order-keeping bits, from the
+//     top, a histogram of one digit over the tokens that share the digits before it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,7 +39,11 @@ constexpr int kNT = 512;
 constexpr int kWarps = kNT / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxParts = kMaxCluster * kWarps;
-constexpr int kCachedBytes = 200 * 1024;     // of a row's piece in a block's shared memory
+constexpr int kCachedBytes = 190 * 1024;     // of a row's piece in a block's shared memory
+constexpr int kPairBytes = 72 * 1024;        // of that, where two blocks share an SM
+constexpr int kList = 2048;                  // tokens that the first block sorts
+constexpr int kBins = 4096;                  // of a in [0, 32)
+constexpr float kBinScale = 128.f;
 
 struct Args {
   const void* logits;
@@ -95,19 +110,38 @@ struct Elem<__nv_bfloat16> {
 };
 
 struct Shared {
-  float top[kMaxCluster];
+  float top[kMaxCluster];           // of every block: its largest logit,
+  float bound[kMaxCluster];         // and its bound for top-k
   float warp_top[kWarps];
-  uint64_t sums[kMaxParts];         // of every warp of the cluster: weight above the border,
-  uint32_t ties[kMaxParts];         // tokens at it
+  uint64_t sums[kMaxParts];         // of every warp of the cluster: weight (above the border),
+  uint64_t kept[kMaxParts];         // that of tokens that min-p keeps,
+  uint32_t ties[kMaxParts];         // tokens at the border, or for the list
   uint32_t best[kMaxCluster];
-  uint32_t count[256], lo[256], hi[256];   // histogram: tokens, or weights as 64 bits in two words
-  uint64_t scan[8];
+  uint64_t scan[kWarps + 1];
   uint32_t digit;
   uint64_t left;
   int found;                        // part that holds the goal
   uint64_t goal, before;
+  uint64_t border;                  // place of the last kept token
   uint32_t ties_before;
+  uint32_t lo, hi;                  // bins of the band
+  union {
+    struct {
+      uint32_t count[256], lo[256], hi[256];   // histogram of a digit: tokens, or weights as 64 bits in two words
+    } digits;
+    uint32_t bins[kBins];           // histogram of weights over a
+    uint64_t list[kList];           // places of tokens, in the order of the indexes
+    float tops[kNT];                // the threads' largest logits
+  } u;
+  uint64_t sorted[kList];
 };
+
+// A token's place in the order: larger is earlier.
+__device__ __forceinline__ uint64_t place_of(float x, int j) {
+  return static_cast<uint64_t>(key_of(x)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(j));
+}
+__device__ __forceinline__ float logit_at(uint64_t place) { return logit_of(static_cast<uint32_t>(place >> 32)); }
+__device__ __forceinline__ int index_at(uint64_t place) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(place)); }
 
 // The border: logits above it are kept, and the first `ties` tokens at it.
 struct Border {
@@ -248,7 +282,7 @@ __device__ uint32_t descend(const R& row, const Scale& s, uint32_t floor, uint64
   uint32_t prefix = 0;
 #pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kNT) sh.count[i] = sh.lo[i] = sh.hi[i] = 0;
+    for (int i = tid; i < 256; i += kNT) sh.u.digits.count[i] = sh.u.digits.lo[i] = sh.u.digits.hi[i] = 0;
     __syncthreads();
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
@@ -261,11 +295,11 @@ __device__ uint32_t descend(const R& row, const Scale& s, uint32_t floor, uint64
         const uint32_t d = (k >> shift) & 255u;
         if (kByWeight) {
           const uint64_t w = weight_of(s, x[i]);
-          const uint32_t lo = static_cast<uint32_t>(w), was = atomicAdd(&sh.lo[d], lo);
+          const uint32_t lo = static_cast<uint32_t>(w), was = atomicAdd(&sh.u.digits.lo[d], lo);
           const uint32_t hi = static_cast<uint32_t>(w >> 32) + (was + lo < was);
-          if (hi) atomicAdd(&sh.hi[d], hi);
+          if (hi) atomicAdd(&sh.u.digits.hi[d], hi);
         } else {
-          atomicAdd(&sh.count[d], 1u);
+          atomicAdd(&sh.u.digits.count[d], 1u);
         }
       }
     }
@@ -274,10 +308,10 @@ __device__ uint32_t descend(const R& row, const Scale& s, uint32_t floor, uint64
     if (tid < 256) {
       for (int c = 0; c < cluster; ++c) {
         if (kByWeight) {
-          const uint64_t lo = ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.lo[255 - tid]), c));
-          mine += lo | static_cast<uint64_t>(ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.hi[255 - tid]), c))) << 32;
+          const uint64_t lo = ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.u.digits.lo[255 - tid]), c));
+          mine += lo | static_cast<uint64_t>(ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.u.digits.hi[255 - tid]), c))) << 32;
         } else {
-          mine += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.count[255 - tid]), c));
+          mine += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.u.digits.count[255 - tid]), c));
         }
       }
     }
@@ -305,8 +339,323 @@ __device__ uint32_t descend(const R& row, const Scale& s, uint32_t floor, uint64
   return prefix;
 }
 
+// Sum over the block of one value a thread, and the threads' share before each.
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t& total, Shared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t t = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += t;
+  }
+  __syncthreads();                  // what was there has been read
+  if (lane == 31) sh.scan[warp] = inc;
+  __syncthreads();
+  uint64_t w = sh.scan[lane % kWarps];
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const uint64_t t = __shfl_up_sync(~0u, w, o, kWarps);
+    if (lane % kWarps >= o) w += t;
+  }
+  total = __shfl_sync(~0u, w, kWarps - 1);
+  const uint64_t before = __shfl_sync(~0u, w, max(warp - 1, 0));
+  return (warp > 0 ? before : 0) + inc - v;
+}
+
+// The block's threads sort n2 (a power of two, at least 64) places in descending order.
+__device__ void sort_places(uint64_t* x, int n2) {
+  const int tid = threadIdx.x;
+  for (int k = 2; k <= n2; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int p = tid; p < n2 / 2; p += kNT) {
+        const int i = 2 * p - (p & (j - 1));
+        const uint64_t a = x[i], b = x[i + j];
+        const bool down = (i & k) == 0;
+        if (down ? a < b : a > b) x[i] = b, x[i + j] = a;
+      }
+      // a warp's pairs lie in 64 places of its own while j is at most 32
+      if (j > 32 || (j == 1 && k >= 64))
+        __syncthreads();
+      else
+        __syncwarp();
+    }
+  }
+  __syncthreads();
+}
+
+// The j-th largest (j >= 1) of the block's values, one a thread.
+__device__ float nth_largest(float v, int j, Shared& sh) {
+  const int tid = threadIdx.x;
+  uint32_t mine = key_of(v);
+  uint32_t* x = reinterpret_cast<uint32_t*>(sh.u.tops);
+  for (int k = 2; k <= kNT; k <<= 1) {
+    for (int s = k >> 1; s > 0; s >>= 1) {
+      uint32_t other;
+      if (s >= 32) {
+        __syncthreads();
+        x[tid] = mine;
+        __syncthreads();
+        other = x[tid ^ s];
+      } else {
+        other = __shfl_xor_sync(~0u, mine, s);
+      }
+      const bool larger = ((tid & s) == 0) == ((tid & k) == 0);   // this thread keeps the larger of the two
+      mine = larger ? max(mine, other) : min(mine, other);
+    }
+  }
+  __syncthreads();
+  x[tid] = mine;
+  __syncthreads();
+  return logit_of(x[j - 1]);
+}
+
+// Each warp's tokens of the list, in the order of the indexes, to the first
+// block: `in(x)` says which.  Their number, or -1 if they are more than fit (then
+// nothing is sent).  All threads of the cluster; ends with its barrier.  extra(x):
+// called once with every vector's logits.
+template <typename R, typename In, typename Extra>
+__device__ int send_list(const R& row, int cluster, int rank, Shared& sh, const In& in, Extra& extra) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = rank * kWarps + warp, parts = cluster * kWarps;
+  uint32_t mine = 0;
+  for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+    float x[R::VEC];
+    row.get(q0, lane, x);
+    extra(x);
+#pragma unroll
+    for (int i = 0; i < R::VEC; ++i) mine += in(x[i]);
+  }
+  mine = __reduce_add_sync(~0u, mine);
+  extra.send(part, cluster, lane, sh);
+  if (lane < cluster) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.ties[part]), lane), mine);
+  ptx::cluster_sync();
+  uint32_t before = 0, n = 0;
+  for (int i = lane; i < parts; i += 32) {
+    const uint32_t c = sh.ties[i];
+    n += c;
+    before += i < part ? c : 0;
+  }
+  n = __reduce_add_sync(~0u, n);
+  before = __reduce_add_sync(~0u, before);
+  if (n > kList) return -1;
+  if (mine) {
+    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(sh.u.list), 0);
+    for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+      float x[R::VEC];
+      row.get(q0, lane, x);
+      uint32_t c = 0;
+#pragma unroll
+      for (int i = 0; i < R::VEC; ++i) c += in(x[i]);
+      if (!__any_sync(~0u, c)) continue;
+      uint32_t inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += t;
+      }
+      uint32_t at = before + inc - c;
+#pragma unroll
+      for (int i = 0; i < R::VEC; ++i)
+        if (in(x[i])) st_cluster_u64(to + 8 * at++, place_of(x[i], (q0 + lane) * R::VEC - row.off + i));
+      before += __shfl_sync(~0u, inc, 31);
+    }
+  }
+  ptx::cluster_sync();
+  return static_cast<int>(n);
+}
+
+// The first block: how many of the list's tokens, in their order, come before the
+// running weight (from `above` on) has reached its goal, at most `most`; sorts
+// the list's copy.  goal_of(weight of the first `most`): the goal.
+template <typename GoalOf>
+__device__ int list_end(int n, int most, uint64_t above, const Scale& s, Shared& sh, const GoalOf& goal_of) {
+  const int tid = threadIdx.x;
+  int n2 = 64;
+  while (n2 < n) n2 <<= 1;
+  for (int i = tid; i < n2; i += kNT) sh.sorted[i] = i < n ? sh.u.list[i] : 0;
+  __syncthreads();
+  sort_places(sh.sorted, n2);
+  constexpr int kEach = kList / kNT;
+  uint64_t w[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int at = tid * kEach + i;
+    w[i] = at < most ? weight_of(s, logit_at(sh.sorted[at])) : 0;
+    sum += w[i];
+  }
+  uint64_t total;
+  uint64_t before = above + block_scan(sum, total, sh);
+  const uint64_t goal = goal_of(total);
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    mine += tid * kEach + i < most && before < goal;
+    before += w[i];
+  }
+  uint64_t end;
+  block_scan(mine, end, sh);
+  return static_cast<int>(end);
+}
+
+struct NoExtra {
+  template <int VEC>
+  __device__ __forceinline__ void operator()(const float (&)[VEC]) {}
+  __device__ __forceinline__ void send(int, int, int, Shared&) {}
+};
+
+// Weights above the band, of each warp.
+struct AboveBand {
+  Scale s;
+  float lo;            // a of the band's first bin
+  uint64_t least;
+  uint64_t sum = 0, kept = 0;
+  template <int VEC>
+  __device__ __forceinline__ void operator()(const float (&x)[VEC]) {
+    float2 a[VEC / 2];
+    float nearest = kFar;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      a[i] = exponents(s, x[2 * i], x[2 * i + 1]);
+      nearest = fminf(nearest, fminf(a[i].x, a[i].y));
+    }
+    if (nearest >= lo) return;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      const float2 y = weights38(a[i]);
+      const uint64_t w0 = a[i].x < lo ? whole(y.x) : 0, w1 = a[i].y < lo ? whole(y.y) : 0;
+      sum += w0 + w1;
+      kept += (w0 >= least ? w0 : 0) + (w1 >= least ? w1 : 0);
+    }
+  }
+  __device__ __forceinline__ void send(int part, int cluster, int lane, Shared& sh) {
+    sum = warp_sum(sum);
+    kept = warp_sum(kept);
+    if (lane < cluster) {
+      st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
+      st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.kept[part]), lane), kept);
+    }
+  }
+};
+
+// The warp whose piece holds the goal finds the index.  keep(x, j, w): the token's weight, or 0.
+template <typename R, typename Keep>
+__device__ void draw(const R& row, const Scale& s, uint64_t at, uint64_t goal, int32_t* token, Keep& keep) {
+  const int lane = threadIdx.x & 31;
+  for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+    float x[R::VEC];
+    uint64_t w[R::VEC], sum = 0;
+    row.get(q0, lane, x);
+    weigh(s, x, w);
+    keep(x, (q0 + lane) * R::VEC - row.off, w);
+#pragma unroll
+    for (int i = 0; i < R::VEC; ++i) sum += w[i];
+    uint64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t v = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const uint32_t hit = __ballot_sync(~0u, at + inc > goal);
+    if (hit) {
+      if (lane == __ffs(hit) - 1) {
+        uint64_t upto = at + inc - sum;
+        int pick = -1;
+#pragma unroll
+        for (int i = 0; i < R::VEC; ++i) {
+          upto += w[i];
+          if (pick < 0 && upto > goal) pick = i;
+        }
+        *token = (q0 + lane) * R::VEC - row.off + pick;
+      }
+      return;
+    }
+    at += __shfl_sync(~0u, inc, 31);
+  }
+}
+
+// What the draws keep.
+struct KeepLeast {       // of at least `least`
+  uint64_t least;
+  template <int VEC>
+  __device__ __forceinline__ void operator()(const float (&)[VEC], int, uint64_t (&w)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[i] = w[i] >= least ? w[i] : 0;
+  }
+};
+struct KeepPlaces {      // and not after the border
+  uint64_t least, border;
+  template <int VEC>
+  __device__ __forceinline__ void operator()(const float (&x)[VEC], int j, uint64_t (&w)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[i] = w[i] >= least && place_of(x[i], j + i) >= border ? w[i] : 0;
+  }
+};
+struct KeepTies {        // above the border, and the first ties at it
+  uint64_t least;
+  Border border;
+  uint32_t ties;         // before this step
+  template <int VEC>
+  __device__ __forceinline__ void operator()(const float (&x)[VEC], int, uint64_t (&w)[VEC]) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) mine += key_of(x[i]) == border.key;
+    uint32_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += t;
+    }
+    uint32_t t = ties + inc - mine;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const uint32_t k = key_of(x[i]);
+      const bool in = k > border.key || (k == border.key && t++ < border.ties);
+      if (!in || w[i] < least) w[i] = 0;
+    }
+    ties += __shfl_sync(~0u, inc, 31);
+  }
+};
+
+__device__ __forceinline__ uint64_t goal_of(float u, uint64_t total) {
+  return share(static_cast<uint64_t>(fminf(fmaxf(u, 0.f), 1.f - 0x1p-24f) * 0x1p24f), total, false);
+}
+
+// One warp: which part of the running sums of value(i) holds the goal that u makes of them (-1: they
+// are all 0), into sh.found, sh.goal and sh.before.
+template <typename Value>
+__device__ void find_part(int parts, float u, Shared& sh, const Value& value) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kEach = kMaxParts / 32;
+  uint64_t v[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    v[i] = lane * kEach + i < parts ? value(lane * kEach + i) : 0;
+    sum += v[i];
+  }
+  uint64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t t = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += t;
+  }
+  const uint64_t goal = goal_of(u, __shfl_sync(~0u, inc, 31));
+  uint64_t before = inc - sum;
+  if (lane == 0) sh.found = -1, sh.goal = goal;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (goal >= before && goal < before + v[i]) {      // one lane, once
+      sh.found = lane * kEach + i;
+      sh.before = before;
+    }
+    before += v[i];
+  }
+  __syncwarp();
+}
+
 template <typename T, bool kCached>
-__global__ void __launch_bounds__(kNT) sample_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __grid_constant__ Args a) {
   extern __shared__ uint4 smem[];
   __shared__ Shared sh;
   using R = Row<T, kCached>;
@@ -314,6 +663,7 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const __grid_constant__ Arg
   const int64_t r = blockIdx.x / a.cluster;
   const int rank = static_cast<int>(ptx::cluster_ctarank()), part = rank * kWarps + warp;
   const int parts = a.cluster * kWarps;
+  ptx::cluster_arrive();           // waited for before the first write to another block's shared memory
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
@@ -325,6 +675,11 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const __grid_constant__ Arg
   row.v0 = static_cast<int>(min(static_cast<int64_t>(part) * a.piece, static_cast<int64_t>(row.nv)));
   row.v1 = static_cast<int>(min(static_cast<int64_t>(part + 1) * a.piece, static_cast<int64_t>(row.nv)));
   row.kept = smem + (kCached ? warp * a.piece : 0);
+  const float temperature = a.set.temperature ? ptx::ld_after_wait(a.set.temperature + r) : a.set.temperature_all;
+  const int top_k = a.set.top_k ? ptx::ld_after_wait(a.set.top_k + r) : a.set.top_k_all;
+  const float top_p = a.set.top_p ? ptx::ld_after_wait(a.set.top_p + r) : a.set.top_p_all;
+  const float min_p = a.set.min_p ? ptx::ld_after_wait(a.set.min_p + r) : a.set.min_p_all;
+  const float u = ptx::ld_after_wait(a.u + r);
 
   // the row, once, and its largest logit
   float top = -INFINITY;
@@ -344,6 +699,14 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const __grid_constant__ Arg
       for (int e = 0; e < R::VEC; ++e) top = fmaxf(top, x[e]);
     }
   }
+  const bool greedy = !(temperature > 0.f), by_k = !greedy && top_k > 0 && top_k < a.V;
+  // the blocks whose threads nearly all have logits share top-k's bound (the last ones may have few, or none)
+  const int chunk = kWarps * a.piece;
+  const int sharing = max(1, min(a.cluster, (row.nv + chunk / 2) / chunk));
+  const int each = (top_k + sharing - 1) / sharing;
+  const bool listed = by_k && each <= kNT / 4;
+  float bound = INFINITY;
+  if (listed && rank < sharing) bound = nth_largest(top, each, sh);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) sh.warp_top[warp] = top;
@@ -351,24 +714,32 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const __grid_constant__ Arg
   top = sh.warp_top[lane % kWarps];
 #pragma unroll
   for (int o = kWarps / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  ptx::cluster_sync();             // all blocks have started
-  if (tid < a.cluster) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.top[rank]), tid), __float_as_uint(top));
+  ptx::cluster_wait();             // all blocks have started
+  if (tid < a.cluster) {
+    st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.top[rank]), tid), __float_as_uint(top));
+    st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.bound[rank]), tid), __float_as_uint(bound));
+  }
   ptx::cluster_sync();
-  for (int c = 0; c < a.cluster; ++c) top = fmaxf(top, sh.top[c]);
+  for (int c = 0; c < a.cluster; ++c) {
+    top = fmaxf(top, sh.top[c]);
+    bound = fminf(bound, sh.bound[c]);
+  }
+  int32_t* token = a.tokens + r;
   if (top == -INFINITY) {          // the same in all blocks
-    if (rank == 0 && tid == 0) a.tokens[r] = -1;
+    if (rank == 0 && tid == 0) *token = -1;
     return;
   }
 
-  const float temperature = a.set.temperature ? ptx::ld_after_wait(a.set.temperature + r) : a.set.temperature_all;
-  if (!(temperature > 0.f)) {
+  if (greedy) {
     uint32_t best = 0xFFFFFFFFu;
-    for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
-      float x[R::VEC];
-      row.get(q0, lane, x);
+    if (sh.top[rank] == top) {     // the block has one
+      for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+        float x[R::VEC];
+        row.get(q0, lane, x);
 #pragma unroll
-      for (int i = R::VEC - 1; i >= 0; --i)
-        if (x[i] == top) best = min(best, static_cast<uint32_t>((q0 + lane) * R::VEC - row.off + i));
+        for (int i = R::VEC - 1; i >= 0; --i)
+          if (x[i] == top) best = min(best, static_cast<uint32_t>((q0 + lane) * R::VEC - row.off + i));
+      }
     }
     best = __reduce_min_sync(~0u, best);
     if (lane == 0) sh.ties[warp] = best;
@@ -378,134 +749,240 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const __grid_constant__ Arg
     ptx::cluster_sync();
     if (rank == 0 && tid == 0) {
       for (int c = 0; c < a.cluster; ++c) best = min(best, sh.best[c]);
-      a.tokens[r] = static_cast<int32_t>(best);
+      *token = static_cast<int32_t>(best);
     }
     return;
   }
   const Scale scale = make_scale(top, temperature);
-  const int top_k = a.set.top_k ? ptx::ld_after_wait(a.set.top_k + r) : a.set.top_k_all;
-  const float top_p = a.set.top_p ? ptx::ld_after_wait(a.set.top_p + r) : a.set.top_p_all;
-  const float min_p = a.set.min_p ? ptx::ld_after_wait(a.set.min_p + r) : a.set.min_p_all;
   const uint64_t least = static_cast<uint64_t>(__float2ull_rz(fminf(fmaxf(min_p, 0.f), 1.f) * 0x1p38f));
+  const bool by_p = top_p < 1.f;
+  const uint64_t p24 = static_cast<uint64_t>(fmaxf(top_p, 0.f) * 0x1p24f);
+  auto p_goal = [&](uint64_t total) { return max(share(p24, total, true), static_cast<uint64_t>(1)); };
 
+  if (!by_k && !by_p) {
+    uint64_t sum = 0;
+    for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+      float x[R::VEC];
+      uint64_t w[R::VEC];
+      row.get(q0, lane, x);
+      weigh(scale, x, w);
+#pragma unroll
+      for (int i = 0; i < R::VEC; ++i) sum += w[i] >= least ? w[i] : 0;
+    }
+    sum = warp_sum(sum);
+    if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
+    ptx::cluster_sync();
+    if (warp == 0) find_part(parts, u, sh, [&](int i) { return sh.sums[i]; });
+    __syncthreads();
+    KeepLeast keep{least};
+    if (sh.found == part) draw(row, scale, sh.before, sh.goal, token, keep);
+    return;
+  }
+
+  if (listed) {
+    NoExtra none;
+    const int n = send_list(row, a.cluster, rank, sh, [&](float x) { return x >= bound && x > -INFINITY; }, none);
+    if (n >= 0) {
+      if (rank != 0) return;
+      // fewer than top_k only where the row has no more above -inf
+      const int end = list_end(n, min(n, top_k), 0, scale, sh, [&](uint64_t total) { return by_p ? p_goal(total) : ~0ull; });
+      const uint64_t border = sh.sorted[end - 1];
+      constexpr int kEach = kList / kNT;
+      uint64_t w[kEach], sum = 0, total;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int at = tid * kEach + i;
+        w[i] = 0;
+        if (at < n && sh.u.list[at] >= border) w[i] = weight_of(scale, logit_at(sh.u.list[at]));
+        if (w[i] < least) w[i] = 0;
+        sum += w[i];
+      }
+      uint64_t upto = block_scan(sum, total, sh);
+      const uint64_t goal = goal_of(u, total);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (goal >= upto && goal < upto + w[i]) *token = index_at(sh.u.list[tid * kEach + i]);
+        upto += w[i];
+      }
+      return;
+    }
+  } else if (kCached && !by_k) {     // (a piece that fits has too few tokens for a bin to pass 32 bits)
+    // weights over a: each as 14 to 15 bits of the size that its bin has
+    for (int i = tid; i < kBins; i += kNT) sh.u.bins[i] = 0;
+    __syncthreads();
+    uint64_t sum = 0;
+    for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+      float x[R::VEC];
+      row.get(q0, lane, x);
+#pragma unroll
+      for (int i = 0; i < R::VEC; i += 2) {
+        const float2 e = exponents(scale, x[i], x[i + 1]);
+        const float2 y = weights38(e);
+        const float ee[2] = {e.x, e.y}, yy[2] = {y.x, y.y};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (ee[h] >= kBins / kBinScale) {
+            sum += __float2uint_rz(yy[h]);
+            continue;
+          }
+          const uint64_t w = whole(yy[h]);
+          sum += w;
+          const int bin = static_cast<int>(ee[h] * kBinScale);
+          atomicAdd(&sh.u.bins[bin], static_cast<uint32_t>(w >> max(23 - (bin >> 7), 0)));
+        }
+      }
+    }
+    sum = warp_sum(sum);
+    if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
+    ptx::cluster_sync();
+    // every block has a share of the bins: its sums over the cluster, and (in the first block) all of them
+    const int share_bins = kBins / a.cluster;
+    uint64_t mine[kBins / kNT], all = 0;
+    uint64_t goal;
+    {
+      uint64_t t = 0;
+      for (int i = lane; i < parts; i += 32) t += sh.sums[i];
+      goal = p_goal(warp_sum(t));
+    }
+    const int per = share_bins / kNT;        // 8 bins a thread with one block, 1 with eight
+#pragma unroll
+    for (int i = 0; i < kBins / kNT; ++i) {
+      mine[i] = 0;
+      if (i < per) {
+        const int bin = rank * share_bins + tid * per + i;
+        const uint32_t at = ptx::smem_u32(&sh.u.bins[bin]);
+        for (int c = 0; c < a.cluster; ++c) mine[i] += ld_cluster_u32(ptx::mapa_shared(at, c));
+        mine[i] <<= max(23 - (bin >> 7), 0);
+        all += mine[i];
+      }
+    }
+    uint64_t total;
+    uint64_t before = block_scan(all, total, sh);
+    if (tid < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.kept[rank]), tid), total);
+    if (tid == 0) sh.lo = sh.hi = kBins;
+    ptx::cluster_sync();
+    for (int c = 0; c < rank; ++c) before += sh.kept[c];
+    // the running weight after a bin is between its sum and 1 + 2^-13 of it
+#pragma unroll
+    for (int i = 0; i < kBins / kNT; ++i) {
+      if (i < per) {
+        const uint64_t after = before + mine[i];
+        const uint32_t bin = rank * share_bins + tid * per + i;
+        auto most = [](uint64_t x) { return x + (x >> 13) + kBins; };
+        const bool first = most(after) >= goal && (bin == 0 || most(before) < goal);
+        const bool last = after >= goal && before < goal;
+        if (first || last) {
+          for (int c = 0; c < a.cluster; ++c) {
+            if (first) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.lo), c), bin);
+            if (last) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.hi), c), bin);
+          }
+        }
+        before = after;
+      }
+    }
+    ptx::cluster_sync();
+    if (sh.hi < kBins) {
+      const float lo = static_cast<float>(sh.lo) * (1.f / kBinScale), hi = static_cast<float>(sh.hi + 1) * (1.f / kBinScale);
+      AboveBand above{scale, lo, least};
+      const int n = send_list(row, a.cluster, rank, sh, [&](float x) {
+        const float e = exponents(scale, x, x).x;
+        return e >= lo && e < hi;
+      }, above);
+      if (n >= 0) {
+        if (rank == 0) {
+          uint64_t t = 0;
+          for (int i = lane; i < parts; i += 32) t += sh.sums[i];
+          const int end = list_end(n, n, warp_sum(t), scale, sh, [&](uint64_t) { return goal; });
+          const uint64_t border = sh.sorted[end - 1];
+          // the band's kept weights, summed over the list, are added to those of their warps
+          constexpr int kEach = kList / kNT;
+          uint64_t w[kEach], sum = 0, rest;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            const int at = tid * kEach + i;
+            w[i] = 0;
+            if (at < n && sh.u.list[at] >= border) w[i] = weight_of(scale, logit_at(sh.u.list[at]));
+            if (w[i] < least) w[i] = 0;
+            sum += w[i];
+          }
+          uint64_t upto = block_scan(sum, rest, sh);         // its barriers: the border has been read
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            sh.sorted[tid * kEach + i] = upto;
+            upto += w[i];
+          }
+          uint64_t listed_all;
+          const uint64_t from = block_scan(tid < parts ? sh.ties[tid] : 0, listed_all, sh);
+          if (tid < parts) {
+            const uint64_t to = from + sh.ties[tid];
+            sh.kept[tid] += (to < kList ? sh.sorted[to] : rest) - (from < kList ? sh.sorted[from] : rest);
+          }
+          __syncthreads();
+          if (warp == 0) {
+            find_part(parts, u, sh, [&](int i) { return sh.kept[i]; });
+            if (lane > 0 && lane < a.cluster) {
+              st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.found), lane), sh.found);
+              st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.goal), lane), sh.goal);
+              st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.before), lane), sh.before);
+            }
+            if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.border), lane), border);
+          }
+        }
+        ptx::cluster_sync();
+        KeepPlaces keep{least, sh.border};
+        if (sh.found == part) draw(row, scale, sh.before, sh.goal, token, keep);
+        return;
+      }
+    }
+  }
+
+  // digit by digit
+  __syncthreads();
   Border border{0, 0};
-  if (top_k > 0 && top_k < a.V) {
+  if (by_k) {
     uint64_t left;
     border.key = descend<false>(row, scale, 0, top_k, a.cluster, sh, left);
     border.ties = static_cast<uint32_t>(left);
   }
-  if (top_p < 1.f) {
+  if (by_p) {
     part_sums(row, scale, border, 0, a.cluster, rank, sh);
     const uint64_t tie = weight_of(scale, logit_of(border.key));
     const uint64_t total = total_of(sh, parts, border.ties, border.ties ? tie : 0, lane);
-    const uint64_t p = static_cast<uint64_t>(fmaxf(top_p, 0.f) * 0x1p24f);
-    const uint64_t goal = max(share(p, total, true), static_cast<uint64_t>(1));
     uint64_t left;
-    const uint32_t key = descend<true>(row, scale, border.key, goal, a.cluster, sh, left);
+    const uint32_t key = descend<true>(row, scale, border.key, p_goal(total), a.cluster, sh, left);
     const uint64_t w = weight_of(scale, logit_of(key));       // above 0: the goal is reached at it
     const uint64_t ties = (left + w - 1) / w;
     border.ties = static_cast<uint32_t>(key == border.key ? min(ties, static_cast<uint64_t>(border.ties)) : ties);
     border.key = key;
   }
-
   part_sums(row, scale, border, least, a.cluster, rank, sh);
   uint64_t tie = border.ties ? weight_of(scale, logit_of(border.key)) : 0;
   if (tie < least) tie = 0;
-  // first warp of every block: the goal and the part that holds it
   if (warp == 0) {
-    const uint64_t total = total_of(sh, parts, border.ties, tie, lane);
-    const float uf = ptx::ld_after_wait(a.u + r);
-    const uint64_t U = static_cast<uint64_t>(fminf(fmaxf(uf, 0.f), 1.f - 0x1p-24f) * 0x1p24f);
-    const uint64_t goal = share(U, total, false);
-    uint64_t at = 0;
-    uint32_t ties = 0;
-    int found = -1;
-    for (int i0 = 0; i0 < parts && found < 0; i0 += 32) {
-      const int i = i0 + lane;
-      const uint64_t sum = i < parts ? sh.sums[i] : 0;
-      const uint32_t mine = i < parts ? sh.ties[i] : 0;
-      uint32_t t_inc = mine;
-      uint64_t s_inc = sum;
+    // the ties of each part that are among the first border.ties
+    uint32_t ties_before = 0;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const uint32_t mine = i0 + lane < parts ? sh.ties[i0 + lane] : 0;
+      uint32_t inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(~0u, t_inc, o);
-        const uint64_t v = __shfl_up_sync(~0u, s_inc, o);
-        if (lane >= o) t_inc += t, s_inc += v;
+        const uint32_t t = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += t;
       }
-      const uint64_t upto = at + s_inc + min(ties + t_inc, border.ties) * tie -
-                            min(ties, border.ties) * tie;
-      const uint32_t hit = __ballot_sync(~0u, upto > goal);
-      if (hit) {
-        found = i0 + __ffs(hit) - 1;
-        if (lane == __ffs(hit) - 1) {
-          const uint32_t tb = ties + t_inc - mine;
-          sh.before = at + s_inc - sum + (min(tb, border.ties) - min(ties, border.ties)) * tie;
-          sh.ties_before = tb;
-        }
+      const uint32_t from = ties_before + inc - mine;
+      if (i0 + lane < parts) {
+        sh.kept[i0 + lane] = sh.sums[i0 + lane] + (min(from + mine, border.ties) - min(from, border.ties)) * tie;
+        sh.ties[i0 + lane] = from;
       }
-      at = __shfl_sync(~0u, upto, 31);
-      ties += __shfl_sync(~0u, t_inc, 31);
+      ties_before += __shfl_sync(~0u, inc, 31);
     }
-    if (lane == 0) {
-      sh.found = found;
-      sh.goal = goal;
-      if (found < 0 && rank == 0) a.tokens[r] = -1;
-    }
+    __syncwarp();
+    find_part(parts, u, sh, [&](int i) { return sh.kept[i]; });
   }
   __syncthreads();
   if (sh.found != part) return;
-
-  // the warp of that part finds the index
-  uint64_t at = sh.before;
-  uint32_t ties = sh.ties_before;
-  const uint64_t goal = sh.goal;
-  for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
-    float x[R::VEC];
-    uint64_t w[R::VEC], sum = 0;
-    uint32_t mine = 0;
-    row.get(q0, lane, x);
-    weigh(scale, x, w);
-#pragma unroll
-    for (int i = 0; i < R::VEC; ++i) mine += key_of(x[i]) == border.key;
-    uint32_t t_inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_up_sync(~0u, t_inc, o);
-      if (lane >= o) t_inc += t;
-    }
-    uint32_t t = ties + t_inc - mine;
-#pragma unroll
-    for (int i = 0; i < R::VEC; ++i) {
-      const uint32_t k = key_of(x[i]);
-      const bool in = k > border.key || (k == border.key && t++ < border.ties);
-      if (!in || w[i] < least) w[i] = 0;
-      sum += w[i];
-    }
-    uint64_t inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t v = __shfl_up_sync(~0u, inc, o);
-      if (lane >= o) inc += v;
-    }
-    const uint32_t hit = __ballot_sync(~0u, at + inc > goal);
-    if (hit) {
-      if (lane == __ffs(hit) - 1) {
-        uint64_t c = at + inc - sum;
-        int pick = 0;
-#pragma unroll
-        for (int i = R::VEC - 1; i >= 0; --i) {
-          uint64_t upto = c;
-#pragma unroll
-          for (int e = 0; e <= i; ++e) upto += w[e];
-          if (upto > goal) pick = i;
-        }
-        a.tokens[r] = (q0 + lane) * R::VEC - row.off + pick;
-      }
-      return;
-    }
-    at += __shfl_sync(~0u, inc, 31);
-    ties += __shfl_sync(~0u, t_inc, 31);
-  }
+  KeepTies keep{least, border, sh.ties[part]};
+  draw(row, scale, sh.before, sh.goal, token, keep);
 }
 
 template <typename T, bool kCached>
@@ -535,11 +1012,10 @@ cudaError_t pick(Args a, int64_t R, int num_sms, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
   const int64_t nv = (static_cast<int64_t>(a.V) + 2 * VEC - 2) / VEC;       // at the worst alignment
   auto piece = [&](int c) { return (nv + c * kWarps * 32 - 1) / (c * kWarps * 32) * 32; };
-  // blocks of a row: as many as leave each warp 256 vectors, while all rows fit beside one another
+  // blocks of a row: as few as let two blocks be resident on an SM; more while all of them fit beside one another
+  const int64_t resident = 2 * num_sms;
   int c = 1;
-  while (c < kMaxCluster && (piece(c) > 256 || piece(c) * kWarps * 16 > kCachedBytes) &&
-         (R * c * 2 <= 2 * num_sms || piece(c) * kWarps * 16 > kCachedBytes))
-    c *= 2;
+  while (c < kMaxCluster && (piece(c) * kWarps * 16 > kPairBytes || (piece(c) > 32 && R * c * 2 <= resident))) c *= 2;
   a.cluster = c;
   a.piece = static_cast<int>(piece(c));
   const int64_t smem = piece(c) * kWarps * 16;
