@@ -26,6 +26,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "attn_internal.h"
 #include "ptx.cuh"
 #include "sample_parts.cuh"
@@ -79,10 +81,6 @@ struct Elem;
 template <>
 struct Elem<float> {
   static constexpr uint32_t kLowest = 0xFF800000u;
-  // NaN to -inf, -0 to 0
-  static __device__ __forceinline__ uint32_t norm(uint32_t x) {
-    return __float_as_uint(fmaxf(__uint_as_float(x), -INFINITY) + 0.f);
-  }
   static __device__ __forceinline__ void get(const uint4& v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
@@ -91,11 +89,6 @@ struct Elem<float> {
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr uint32_t kLowest = 0xFF80FF80u;
-  static __device__ __forceinline__ uint32_t norm(uint32_t x) {
-    const __nv_bfloat162 low = __floats2bfloat162_rn(-INFINITY, -INFINITY), zero = __floats2bfloat162_rn(0.f, 0.f);
-    const __nv_bfloat162 r = __hadd2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x), low), zero);
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
   static __device__ __forceinline__ void get(const uint4& v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -159,7 +152,7 @@ struct Row {
   int v0, v1;           // of this warp
   uint4* kept;          // of this warp, in shared memory
 
-  // Vector q from device memory, normalised; what is not of the row is -inf.
+  // Vector q from device memory; what is not of the row is -inf.
   __device__ __forceinline__ uint4 fetch(int q) const {
     const int j = q * VEC - off;
     uint4 v;
@@ -180,7 +173,7 @@ struct Row {
       }
       v = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return make_uint4(Elem<T>::norm(v.x), Elem<T>::norm(v.y), Elem<T>::norm(v.z), Elem<T>::norm(v.w));
+    return v;
   }
   // Logits of the vector this lane has at step q0 (of v0, v0 + 32, ..); past the piece: -inf.
   __device__ __forceinline__ void get(int q0, int lane, float (&x)[VEC]) const {
@@ -194,27 +187,63 @@ struct Row {
   }
 };
 
-// Weights of a vector's logits.
+// a of a vector's logits; the least of them.
 template <int VEC>
-__device__ __forceinline__ void weigh(const Scale& s, const float (&x)[VEC], uint64_t (&w)[VEC]) {
-  float2 a[VEC / 2];
+__device__ __forceinline__ float exponents(const Scale& s, const float (&x)[VEC], float2 (&a)[VEC / 2]) {
   float least = kFar;
 #pragma unroll
   for (int i = 0; i < VEC / 2; ++i) {
     a[i] = exponents(s, x[2 * i], x[2 * i + 1]);
     least = fminf(least, fminf(a[i].x, a[i].y));
   }
+  return least;
+}
+
+// Weights of a vector's logits.
+template <int VEC>
+__device__ __forceinline__ void weigh(const Scale& s, const float (&x)[VEC], uint64_t (&w)[VEC]) {
+  float2 a[VEC / 2];
+  const float nearest = exponents(s, x, a);
+  if (nearest >= kNone) {
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) {
-    const float2 y = weights38(a[i]);
-    if (least >= kSmall) {
-      w[2 * i] = __float2uint_rz(y.x);
-      w[2 * i + 1] = __float2uint_rz(y.y);
-    } else {
-      w[2 * i] = whole(y.x);
-      w[2 * i + 1] = whole(y.y);
+    for (int i = 0; i < VEC; ++i) w[i] = 0;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) a[i] = weights38(a[i]);
+  if (nearest >= kSmall) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[i] = whole_small(i & 1 ? a[i / 2].y : a[i / 2].x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[i] = whole(i & 1 ? a[i / 2].y : a[i / 2].x);
+  }
+}
+
+// The sum of a vector's weights of at least `least`.
+template <int VEC>
+__device__ __forceinline__ uint64_t weight_sum(const Scale& s, const float (&x)[VEC], uint64_t least) {
+  float2 a[VEC / 2];
+  const float nearest = exponents(s, x, a);
+  if (nearest >= kNone) return 0;
+  uint64_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) a[i] = weights38(a[i]);
+  if (nearest >= kSmall) {
+    const uint32_t low = static_cast<uint32_t>(min(least, static_cast<uint64_t>(0xFFFFFFFFu)));    // such a weight is below 2^32 - 1
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const uint32_t w = whole_small(i & 1 ? a[i / 2].y : a[i / 2].x);
+      sum += w >= low ? w : 0;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const uint64_t w = whole(i & 1 ? a[i / 2].y : a[i / 2].x);
+      sum += w >= least ? w : 0;
     }
   }
+  return sum;
 }
 
 // All threads of the cluster: each warp's weight above the border (of at least
@@ -512,13 +541,7 @@ struct AboveBand {
   template <int VEC>
   __device__ __forceinline__ void operator()(const float (&x)[VEC]) {
     float2 a[VEC / 2];
-    float nearest = kFar;
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
-      a[i] = exponents(s, x[2 * i], x[2 * i + 1]);
-      nearest = fminf(nearest, fminf(a[i].x, a[i].y));
-    }
-    if (nearest >= lo) return;
+    if (exponents(s, x, a) >= lo) return;
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) {
       const float2 y = weights38(a[i]);
@@ -763,11 +786,8 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
     uint64_t sum = 0;
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
-      uint64_t w[R::VEC];
       row.get(q0, lane, x);
-      weigh(scale, x, w);
-#pragma unroll
-      for (int i = 0; i < R::VEC; ++i) sum += w[i] >= least ? w[i] : 0;
+      sum += weight_sum(scale, x, least);
     }
     sum = warp_sum(sum);
     if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
@@ -814,23 +834,34 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
       row.get(q0, lane, x);
+      float2 e[R::VEC / 2];
+      const float nearest = exponents(scale, x, e);
+      if (nearest >= kNone) continue;
+      auto count = [&](auto small) {
 #pragma unroll
-      for (int i = 0; i < R::VEC; i += 2) {
-        const float2 e = exponents(scale, x[i], x[i + 1]);
-        const float2 y = weights38(e);
-        const float ee[2] = {e.x, e.y}, yy[2] = {y.x, y.y};
+        for (int i = 0; i < R::VEC / 2; ++i) {
+          const float2 y = weights38(e[i]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (ee[h] >= kBins / kBinScale) {
-            sum += __float2uint_rz(yy[h]);
-            continue;
+          for (int h = 0; h < 2; ++h) {
+            const float at = h ? e[i].y : e[i].x, v = h ? y.y : y.x;
+            // the bin, from the low bits of at + 1.5 2^16 (steps of 2^-7) rounded down
+            const int bin = __float_as_uint(__fadd_rd(at, 98304.f)) & 0x3FFFu;
+            if constexpr (decltype(small)::value) {
+              const uint32_t w = whole_small(v);
+              sum += w;
+              if (bin < kBins) atomicAdd(&sh.u.bins[bin], w >> max(23 - (bin >> 7), 0));
+            } else {
+              const uint64_t w = whole(v);
+              sum += w;
+              if (bin < kBins) atomicAdd(&sh.u.bins[bin], static_cast<uint32_t>(w >> max(23 - (bin >> 7), 0)));
+            }
           }
-          const uint64_t w = whole(yy[h]);
-          sum += w;
-          const int bin = static_cast<int>(ee[h] * kBinScale);
-          atomicAdd(&sh.u.bins[bin], static_cast<uint32_t>(w >> max(23 - (bin >> 7), 0)));
         }
-      }
+      };
+      if (nearest >= kSmall)
+        count(std::true_type());
+      else
+        count(std::false_type());
     }
     sum = warp_sum(sum);
     if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
