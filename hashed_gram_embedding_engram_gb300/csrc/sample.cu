@@ -12,14 +12,15 @@
 // device memory once and kept in shared memory where it fits.  Then, by settings:
 //   * none, or min-p: each warp's weight; the warp whose piece holds the goal finds
 //     the index.
-//   * top-k: every thread's largest logit is known from the load.  The j-th largest
-//     of a block's 512, j = ceil(k / blocks), is exceeded j times in each block,
-//     so the least of the blocks' bounds lies below the k-th logit, and little
-//     below it: what reaches it (about 1.2 k tokens) goes to the first block, which
-//     sorts it; top-p and the draw happen on that list.
-//   * top-p alone: a histogram of weights over a, in steps of 2^(1/128), says to
-//     within 2^-13 where the running weight reaches its goal; the few tokens of that
-//     band go to the first block, which sorts them and has the exact end.
+//   * top-k: every thread's largest logit is known from the load.  A value that
+//     ceil(k / blocks) of each block's 512 reach, and few more, lies below the k-th
+//     logit, and little below it: what reaches it (1.2 to 2 k tokens) goes to the
+//     first block; top-p and the draw happen on that list.
+//   * top-p alone: a histogram of weights over a, in steps of 2^(1/8), says in which
+//     step the running weight reaches its goal; that step's tokens go to the first
+//     block, which has the exact end.
+//     A list is not sorted: with few tokens each counts those before it, with more
+//     the end is found digit by digit of their places.
 //   * what is too much for the list (thousands of ties, a large k, a goal in the
 //     far tail): borders digit by digit of the logits' order-keeping bits, from the
 //     top, a histogram of one digit over the tokens that share the digits before it.
@@ -41,11 +42,15 @@ constexpr int kNT = 512;
 constexpr int kWarps = kNT / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxParts = kMaxCluster * kWarps;
-constexpr int kCachedBytes = 190 * 1024;     // of a row's piece in a block's shared memory
-constexpr int kPairBytes = 72 * 1024;        // of that, where two blocks share an SM
-constexpr int kList = 2048;                  // tokens that the first block sorts
-constexpr int kBins = 4096;                  // of a in [0, 32)
-constexpr float kBinScale = 128.f;
+constexpr int kCachedBytes = 176 * 1024;     // of a row's piece in a block's shared memory
+constexpr int kPairBytes = 64 * 1024;        // of that, where two blocks share an SM
+constexpr int kList = 2048;                  // tokens that the first block looks through
+constexpr int kEach = kList / kNT;
+constexpr int kFew = 128;                    // of these, as many as are compared pair by pair
+constexpr int kBins = 256;                   // of a in [0, 32)
+constexpr float kBinScale = 8.f;
+constexpr int kCopies = 16;                  // of the histogram, two lanes each
+constexpr int kDigit = 1024;                 // values of a digit of a place
 
 struct Args {
   const void* logits;
@@ -68,6 +73,12 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t atom_cluster_add(uint32_t addr, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(addr), "r"(v) : "memory");
+  return r;
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -106,27 +117,35 @@ struct Shared {
   float top[kMaxCluster];           // of every block: its largest logit,
   float bound[kMaxCluster];         // and its bound for top-k
   float warp_top[kWarps];
+  float warp_low[kWarps];
   uint64_t sums[kMaxParts];         // of every warp of the cluster: weight (above the border),
   uint64_t kept[kMaxParts];         // that of tokens that min-p keeps,
+  uint64_t all[kMaxParts];          // that of all its tokens,
   uint32_t ties[kMaxParts];         // tokens at the border, or for the list
   uint32_t best[kMaxCluster];
-  uint64_t scan[kWarps + 1];
+  uint64_t scan[kWarps];
   uint32_t digit;
+  uint32_t listed;                  // tokens sent to this block's list
   uint64_t left;
   int found;                        // part that holds the goal
   uint64_t goal, before;
   uint64_t border;                  // place of the last kept token
-  uint32_t ties_before;
+  uint64_t total;
   uint32_t lo, hi;                  // bins of the band
+  uint64_t list[kList];             // places of tokens
   union {
     struct {
       uint32_t count[256], lo[256], hi[256];   // histogram of a digit: tokens, or weights as 64 bits in two words
     } digits;
-    uint32_t bins[kBins];           // histogram of weights over a
-    uint64_t list[kList];           // places of tokens, in the order of the indexes
-    float tops[kNT];                // the threads' largest logits
+    struct {
+      uint32_t mine[kBins][kCopies];           // histogram of weights over a
+      uint32_t all[kMaxCluster][kBins];        // every block's
+    } bins;
+    struct {
+      uint32_t count[kDigit], lo[kDigit], hi[kDigit];
+    } places;
+    uint64_t weights[kFew];
   } u;
-  uint64_t sorted[kList];
 };
 
 // A token's place in the order: larger is earlier.
@@ -391,139 +410,201 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t& total, Shar
   return (warp > 0 ? before : 0) + inc - v;
 }
 
-// The block's threads sort n2 (a power of two, at least 64) places in descending order.
-__device__ void sort_places(uint64_t* x, int n2) {
-  const int tid = threadIdx.x;
-  for (int k = 2; k <= n2; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int p = tid; p < n2 / 2; p += kNT) {
-        const int i = 2 * p - (p & (j - 1));
-        const uint64_t a = x[i], b = x[i + j];
-        const bool down = (i & k) == 0;
-        if (down ? a < b : a > b) x[i] = b, x[i + j] = a;
-      }
-      // a warp's pairs lie in 64 places of its own while j is at most 32
-      if (j > 32 || (j == 1 && k >= 64))
-        __syncthreads();
-      else
-        __syncwarp();
-    }
+// A value that at least j of the block's (one a thread) reach, and few more.  low, top: the least and the
+// largest of them, the same in all threads.
+__device__ float bound_of(float v, int j, float low, float top) {
+  if (__syncthreads_count(v >= low) < j) return -INFINITY;
+  float hi = top;
+  for (int i = 0; i < 20; ++i) {
+    const float mid = 0.5f * low + 0.5f * hi;
+    if (!(mid > low && mid < hi)) break;
+    const int n = __syncthreads_count(v >= mid);
+    if (n >= j)
+      low = mid;
+    else
+      hi = mid;
+    if (n >= j && n <= j + j / 4 + 1) break;
   }
-  __syncthreads();
+  return low;
 }
 
-// The j-th largest (j >= 1) of the block's values, one a thread.
-__device__ float nth_largest(float v, int j, Shared& sh) {
-  const int tid = threadIdx.x;
-  uint32_t mine = key_of(v);
-  uint32_t* x = reinterpret_cast<uint32_t*>(sh.u.tops);
-  for (int k = 2; k <= kNT; k <<= 1) {
-    for (int s = k >> 1; s > 0; s >>= 1) {
-      uint32_t other;
-      if (s >= 32) {
-        __syncthreads();
-        x[tid] = mine;
-        __syncthreads();
-        other = x[tid ^ s];
-      } else {
-        other = __shfl_xor_sync(~0u, mine, s);
-      }
-      const bool larger = ((tid & s) == 0) == ((tid & k) == 0);   // this thread keeps the larger of the two
-      mine = larger ? max(mine, other) : min(mine, other);
-    }
-  }
-  __syncthreads();
-  x[tid] = mine;
-  __syncthreads();
-  return logit_of(x[j - 1]);
-}
-
-// Each warp's tokens of the list, in the order of the indexes, to the first
-// block: `in(x)` says which.  Their number, or -1 if they are more than fit (then
-// nothing is sent).  All threads of the cluster; ends with its barrier.  extra(x):
-// called once with every vector's logits.
+// Each warp's tokens for the list, `in(x)` says which, to the first block's list in no order.  Their
+// number, or -1 if they are more than fit.  All threads of the cluster; ends with its barrier.
+// some: whether the lane has any.  extra(x): called with every vector's logits.
 template <typename R, typename In, typename Extra>
-__device__ int send_list(const R& row, int cluster, int rank, Shared& sh, const In& in, Extra& extra) {
+__device__ int send_list(const R& row, int cluster, int rank, Shared& sh, bool some, const In& in, Extra& extra) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int part = rank * kWarps + warp, parts = cluster * kWarps;
   uint32_t mine = 0;
-  for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
-    float x[R::VEC];
-    row.get(q0, lane, x);
-    extra(x);
-#pragma unroll
-    for (int i = 0; i < R::VEC; ++i) mine += in(x[i]);
-  }
-  mine = __reduce_add_sync(~0u, mine);
-  extra.send(part, cluster, lane, sh);
-  if (lane < cluster) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.ties[part]), lane), mine);
-  ptx::cluster_sync();
-  uint32_t before = 0, n = 0;
-  for (int i = lane; i < parts; i += 32) {
-    const uint32_t c = sh.ties[i];
-    n += c;
-    before += i < part ? c : 0;
-  }
-  n = __reduce_add_sync(~0u, n);
-  before = __reduce_add_sync(~0u, before);
-  if (n > kList) return -1;
-  if (mine) {
-    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(sh.u.list), 0);
+  if (__any_sync(~0u, some)) {
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
       row.get(q0, lane, x);
-      uint32_t c = 0;
+      extra(x);
 #pragma unroll
-      for (int i = 0; i < R::VEC; ++i) c += in(x[i]);
-      if (!__any_sync(~0u, c)) continue;
-      uint32_t inc = c;
+      for (int i = 0; i < R::VEC; ++i) mine += in(x[i]);
+    }
+  }
+  uint32_t inc = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o) inc += t;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += t;
+  }
+  const uint32_t all = __shfl_sync(~0u, inc, 31);
+  extra.send(part, cluster, lane, sh);
+  if (lane < cluster) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.ties[part]), lane), all);
+  if (all) {
+    uint32_t at = 0;
+    if (lane == 0) at = atom_cluster_add(ptx::mapa_shared(ptx::smem_u32(&sh.listed), 0), all);
+    at = __shfl_sync(~0u, at, 0) + inc - mine;
+    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(sh.list), 0);
+    for (int q0 = row.v0; q0 < row.v1 && __any_sync(~0u, mine); q0 += 32) {
+      float x[R::VEC];
+      row.get(q0, lane, x);
+#pragma unroll
+      for (int i = 0; i < R::VEC; ++i) {
+        if (in(x[i])) {
+          if (at < kList) st_cluster_u64(to + 8 * at, place_of(x[i], (q0 + lane) * R::VEC - row.off + i));
+          ++at, --mine;
+        }
       }
-      uint32_t at = before + inc - c;
-#pragma unroll
-      for (int i = 0; i < R::VEC; ++i)
-        if (in(x[i])) st_cluster_u64(to + 8 * at++, place_of(x[i], (q0 + lane) * R::VEC - row.off + i));
-      before += __shfl_sync(~0u, inc, 31);
     }
   }
   ptx::cluster_sync();
-  return static_cast<int>(n);
+  uint32_t n = 0;
+  for (int i = lane; i < parts; i += 32) n += sh.ties[i];
+  n = __reduce_add_sync(~0u, n);
+  return n > kList ? -1 : static_cast<int>(n);
 }
 
-// The first block: how many of the list's tokens, in their order, come before the
-// running weight (from `above` on) has reached its goal, at most `most`; sorts
-// the list's copy.  goal_of(weight of the first `most`): the goal.
-template <typename GoalOf>
-__device__ int list_end(int n, int most, uint64_t above, const Scale& s, Shared& sh, const GoalOf& goal_of) {
+// The block's threads: of tokens with these keys and weights (kEach a thread), the one whose weight takes the
+// running weight, from the largest key down, to `need` or more: its key, and the weight before it.
+// kCount: the need-th by number.  Digit by digit from the highest of `bits`, until the tokens that are left
+// are one.  Keys differ from one another; tokens with `in` false are left out.
+template <bool kCount>
+__device__ uint64_t pick(const uint64_t (&key)[kEach], const uint64_t (&w)[kEach], const bool (&in)[kEach], int bits,
+                         uint64_t need, Shared& sh, uint64_t& weight_before) {
   const int tid = threadIdx.x;
-  int n2 = 64;
-  while (n2 < n) n2 <<= 1;
-  for (int i = tid; i < n2; i += kNT) sh.sorted[i] = i < n ? sh.u.list[i] : 0;
+  uint64_t prefix = 0, before = 0;
+  int shift = bits;
+  while (true) {
+    const int low = max(shift - 10, 0), size = 1 << (shift - low);
+    for (int i = tid; i < kDigit; i += kNT) sh.u.places.count[i] = sh.u.places.lo[i] = sh.u.places.hi[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (!in[i] || (shift < 64 && key[i] >> shift != prefix)) continue;
+      const int d = static_cast<int>(key[i] >> low) & (size - 1);
+      atomicAdd(&sh.u.places.count[d], 1u);
+      const uint32_t lo = static_cast<uint32_t>(w[i]), was = atomicAdd(&sh.u.places.lo[d], lo);
+      const uint32_t hi = static_cast<uint32_t>(w[i] >> 32) + (was + lo < was);
+      if (hi) atomicAdd(&sh.u.places.hi[d], hi);
+    }
+    __syncthreads();
+    // two digits a thread, from the largest down
+    uint64_t c[2], v[2], total;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int d = kDigit - 1 - (2 * tid + i);
+      c[i] = sh.u.places.count[d];
+      v[i] = static_cast<uint64_t>(sh.u.places.hi[d]) << 32 | sh.u.places.lo[d];
+    }
+    uint64_t v_at = block_scan(v[0] + v[1], total, sh);
+    uint64_t c_at = kCount ? block_scan(c[0] + c[1], total, sh) : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t at = kCount ? c_at : v_at, size_here = kCount ? c[i] : v[i];
+      if (need > at && need <= at + size_here) {          // one thread, once
+        sh.digit = kDigit - 1 - (2 * tid + i);
+        sh.left = need - at;
+        sh.goal = v_at;
+        sh.before = c[i];
+      }
+      v_at += v[i];
+      c_at += c[i];
+    }
+    __syncthreads();
+    prefix = (shift < 64 ? prefix << (shift - low) : 0) | sh.digit;
+    need = sh.left;
+    before += sh.goal;
+    const bool one = sh.before == 1;
+    shift = low;
+    __syncthreads();
+    if (one || shift == 0) break;
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (in[i] && key[i] >> shift == prefix) sh.left = key[i];     // one
   __syncthreads();
-  sort_places(sh.sorted, n2);
-  constexpr int kEach = kList / kNT;
-  uint64_t w[kEach], sum = 0;
+  const uint64_t found = sh.left;
+  weight_before = before;
+  __syncthreads();
+  return found;
+}
+
+// The first block, over the list's n tokens (running weights begin at `above`): the place of the last token
+// that is kept: of the first `most` in their order, those before which the running weight has not
+// reached goal_of(weight of the first `most`).  All threads get it.
+template <typename GoalOf>
+__device__ uint64_t list_border(int n, int most, uint64_t above, const Scale& s, Shared& sh, const GoalOf& goal_of) {
+  const int tid = threadIdx.x;
+  if (n <= kFew) {
+    // four threads a token, each against a quarter of the others
+    static_assert(4 * kFew == kNT, "");
+    const int e = tid >> 2;
+    const uint64_t mine = e < n ? sh.list[e] : 0;
+    const uint64_t w = e < n ? weight_of(s, logit_at(mine)) : 0;
+    if ((tid & 3) == 0) sh.u.weights[e] = w;
+    __syncthreads();
+    uint64_t before = 0;
+    int rank = 0;
+    for (int j = tid & 3; j < n; j += 4) {
+      const bool earlier = sh.list[j] > mine;
+      before += earlier ? sh.u.weights[j] : 0;
+      rank += earlier;
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      before += __shfl_xor_sync(~0u, before, o);
+      rank += __shfl_xor_sync(~0u, rank, o);
+    }
+    if (e < n && rank == most - 1 && (tid & 3) == 0) {
+      sh.total = before + w;
+      sh.border = mine;
+    }
+    __syncthreads();
+    const uint64_t goal = goal_of(sh.total);
+    __syncthreads();
+    before += above;
+    if (e < n && rank < most && before < goal && before + w >= goal && (tid & 3) == 0) sh.border = mine;
+    __syncthreads();
+    const uint64_t border = sh.border;
+    return border;
+  }
+  uint64_t key[kEach], w[kEach];
+  bool in[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int at = tid * kEach + i;
-    w[i] = at < most ? weight_of(s, logit_at(sh.sorted[at])) : 0;
-    sum += w[i];
+    in[i] = i * kNT + tid < n;
+    key[i] = in[i] ? sh.list[i * kNT + tid] : 0;
+    w[i] = in[i] ? weight_of(s, logit_at(key[i])) : 0;
   }
-  uint64_t total;
-  uint64_t before = above + block_scan(sum, total, sh);
+  uint64_t border = 0, before, total;
+  if (most < n) {
+    border = pick<true>(key, w, in, 64, most, sh, before);
+    total = before + weight_of(s, logit_at(border));
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) in[i] = in[i] && key[i] >= border;
+  } else {
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) sum += w[i];
+    block_scan(sum, total, sh);
+  }
   const uint64_t goal = goal_of(total);
-  int mine = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    mine += tid * kEach + i < most && before < goal;
-    before += w[i];
-  }
-  uint64_t end;
-  block_scan(mine, end, sh);
-  return static_cast<int>(end);
+  if (goal > above + total) return border;              // all of them
+  return pick<false>(key, w, in, 64, goal - above, sh, before);
 }
 
 struct NoExtra {
@@ -728,15 +809,28 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
   const int sharing = max(1, min(a.cluster, (row.nv + chunk / 2) / chunk));
   const int each = (top_k + sharing - 1) / sharing;
   const bool listed = by_k && each <= kNT / 4;
-  float bound = INFINITY;
-  if (listed && rank < sharing) bound = nth_largest(top, each, sh);
+  const float mine = top;
+  float low = mine > -INFINITY ? mine : INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if (lane == 0) sh.warp_top[warp] = top;
+  for (int o = 16; o > 0; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    low = fminf(low, __shfl_xor_sync(~0u, low, o));
+  }
+  if (lane == 0) {
+    sh.warp_top[warp] = top;
+    sh.warp_low[warp] = low;
+    sh.listed = 0;
+  }
   __syncthreads();
   top = sh.warp_top[lane % kWarps];
+  low = sh.warp_low[lane % kWarps];
 #pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  for (int o = kWarps / 2; o > 0; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    low = fminf(low, __shfl_xor_sync(~0u, low, o));
+  }
+  float bound = INFINITY;
+  if (listed && rank < sharing) bound = bound_of(mine, each, low, top);
   ptx::cluster_wait();             // all blocks have started
   if (tid < a.cluster) {
     st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.top[rank]), tid), __float_as_uint(top));
@@ -801,35 +895,59 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
 
   if (listed) {
     NoExtra none;
-    const int n = send_list(row, a.cluster, rank, sh, [&](float x) { return x >= bound && x > -INFINITY; }, none);
+    const int n = send_list(row, a.cluster, rank, sh, mine >= bound && mine > -INFINITY,
+                            [&](float x) { return x >= bound && x > -INFINITY; }, none);
     if (n >= 0) {
       if (rank != 0) return;
       // fewer than top_k only where the row has no more above -inf
-      const int end = list_end(n, min(n, top_k), 0, scale, sh, [&](uint64_t total) { return by_p ? p_goal(total) : ~0ull; });
-      const uint64_t border = sh.sorted[end - 1];
-      constexpr int kEach = kList / kNT;
-      uint64_t w[kEach], sum = 0, total;
+      const uint64_t border = list_border(n, min(n, top_k), 0, scale, sh,
+                                          [&](uint64_t total) { return by_p ? p_goal(total) : ~0ull; });
+      if (n <= kFew) {
+        const int e = tid >> 2;
+        const uint64_t place = e < n ? sh.list[e] : 0;
+        uint64_t w = e < n && place >= border ? sh.u.weights[e] : 0;
+        if (w < least) w = 0;
+        __syncthreads();
+        if ((tid & 3) == 0) sh.u.weights[e] = w;
+        __syncthreads();
+        const uint32_t at = static_cast<uint32_t>(place);          // larger: an earlier index
+        uint64_t before = 0, total = 0;
+        for (int j = tid & 3; j < n; j += 4) {
+          const uint64_t v = sh.u.weights[j];
+          total += v;
+          before += static_cast<uint32_t>(sh.list[j]) > at ? v : 0;
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          before += __shfl_xor_sync(~0u, before, o);
+          total += __shfl_xor_sync(~0u, total, o);
+        }
+        const uint64_t goal = goal_of(u, total);
+        if (goal >= before && goal < before + w && (tid & 3) == 0) *token = index_at(place);
+        return;
+      }
+      uint64_t key[kEach], w[kEach], sum = 0, total;
+      bool in[kEach];
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int at = tid * kEach + i;
-        w[i] = 0;
-        if (at < n && sh.u.list[at] >= border) w[i] = weight_of(scale, logit_at(sh.u.list[at]));
+        const uint64_t place = i * kNT + tid < n ? sh.list[i * kNT + tid] : 0;
+        key[i] = static_cast<uint32_t>(place);                     // larger: an earlier index
+        w[i] = place >= border && place > 0 ? weight_of(scale, logit_at(place)) : 0;
         if (w[i] < least) w[i] = 0;
+        in[i] = w[i] > 0;
         sum += w[i];
       }
-      uint64_t upto = block_scan(sum, total, sh);
-      const uint64_t goal = goal_of(u, total);
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        if (goal >= upto && goal < upto + w[i]) *token = index_at(sh.u.list[tid * kEach + i]);
-        upto += w[i];
-      }
+      block_scan(sum, total, sh);
+      uint64_t before;
+      const uint64_t found = pick<false>(key, w, in, 32, goal_of(u, total) + 1, sh, before);
+      if (tid == 0) *token = index_at(found);
       return;
     }
   } else if (kCached && !by_k) {     // (a piece that fits has too few tokens for a bin to pass 32 bits)
-    // weights over a: each as 14 to 15 bits of the size that its bin has
-    for (int i = tid; i < kBins; i += kNT) sh.u.bins[i] = 0;
+    // weights over a: each as 14 to 15 bits of the size that its bin has, two lanes to a copy
+    for (int i = tid; i < kBins * kCopies; i += kNT) (&sh.u.bins.mine[0][0])[i] = 0;
     __syncthreads();
+    uint32_t* const copy = &sh.u.bins.mine[0][lane % kCopies];
     uint64_t sum = 0;
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
@@ -844,16 +962,16 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float at = h ? e[i].y : e[i].x, v = h ? y.y : y.x;
-            // the bin, from the low bits of at + 1.5 2^16 (steps of 2^-7) rounded down
-            const int bin = __float_as_uint(__fadd_rd(at, 98304.f)) & 0x3FFFu;
+            // the bin, from the low bits of at + 1.5 2^20 (steps of 2^-3) rounded down
+            const int bin = __float_as_uint(__fadd_rd(at, 1572864.f)) & 0x3FFu;
             if constexpr (decltype(small)::value) {
               const uint32_t w = whole_small(v);
               sum += w;
-              if (bin < kBins) atomicAdd(&sh.u.bins[bin], w >> max(23 - (bin >> 7), 0));
+              if (bin < kBins) atomicAdd(copy + bin * kCopies, w >> max(23 - (bin >> 3), 0));
             } else {
               const uint64_t w = whole(v);
               sum += w;
-              if (bin < kBins) atomicAdd(&sh.u.bins[bin], static_cast<uint32_t>(w >> max(23 - (bin >> 7), 0)));
+              if (bin < kBins) atomicAdd(copy + bin * kCopies, static_cast<uint32_t>(w >> max(23 - (bin >> 3), 0)));
             }
           }
         }
@@ -864,89 +982,56 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
         count(std::false_type());
     }
     sum = warp_sum(sum);
-    if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
+    if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.all[part]), lane), sum);
+    if (tid == 0) sh.lo = sh.hi = kBins;
+    __syncthreads();
+    // the copies together, to every block: two threads a bin
+    {
+      const int bin = tid >> 1;
+      uint32_t v = 0;
+#pragma unroll
+      for (int i = 0; i < kCopies / 2; ++i) v += sh.u.bins.mine[bin][(i * 2 + bin + tid) % kCopies];
+      v += __shfl_xor_sync(~0u, v, 1);
+      for (int c = tid & 1; c < a.cluster; c += 2)
+        st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.u.bins.all[rank][bin]), c), v);
+    }
     ptx::cluster_sync();
-    // every block has a share of the bins: its sums over the cluster, and (in the first block) all of them
-    const int share_bins = kBins / a.cluster;
-    uint64_t mine[kBins / kNT], all = 0;
     uint64_t goal;
     {
       uint64_t t = 0;
-      for (int i = lane; i < parts; i += 32) t += sh.sums[i];
+      for (int i = lane; i < parts; i += 32) t += sh.all[i];
       goal = p_goal(warp_sum(t));
     }
-    const int per = share_bins / kNT;        // 8 bins a thread with one block, 1 with eight
-#pragma unroll
-    for (int i = 0; i < kBins / kNT; ++i) {
-      mine[i] = 0;
-      if (i < per) {
-        const int bin = rank * share_bins + tid * per + i;
-        const uint32_t at = ptx::smem_u32(&sh.u.bins[bin]);
-        for (int c = 0; c < a.cluster; ++c) mine[i] += ld_cluster_u32(ptx::mapa_shared(at, c));
-        mine[i] <<= max(23 - (bin >> 7), 0);
-        all += mine[i];
-      }
-    }
-    uint64_t total;
-    uint64_t before = block_scan(all, total, sh);
-    if (tid < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.kept[rank]), tid), total);
-    if (tid == 0) sh.lo = sh.hi = kBins;
-    ptx::cluster_sync();
-    for (int c = 0; c < rank; ++c) before += sh.kept[c];
     // the running weight after a bin is between its sum and 1 + 2^-13 of it
-#pragma unroll
-    for (int i = 0; i < kBins / kNT; ++i) {
-      if (i < per) {
-        const uint64_t after = before + mine[i];
-        const uint32_t bin = rank * share_bins + tid * per + i;
-        auto most = [](uint64_t x) { return x + (x >> 13) + kBins; };
-        const bool first = most(after) >= goal && (bin == 0 || most(before) < goal);
-        const bool last = after >= goal && before < goal;
-        if (first || last) {
-          for (int c = 0; c < a.cluster; ++c) {
-            if (first) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.lo), c), bin);
-            if (last) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.hi), c), bin);
-          }
-        }
-        before = after;
-      }
+    uint64_t mine_bin = 0, all;
+    if (tid < kBins) {
+      for (int c = 0; c < a.cluster; ++c) mine_bin += sh.u.bins.all[c][tid];
+      mine_bin <<= max(23 - (tid >> 3), 0);
     }
-    ptx::cluster_sync();
+    const uint64_t before = block_scan(mine_bin, all, sh), after = before + mine_bin;
+    auto most = [](uint64_t x) { return x + (x >> 13) + kBins; };
+    if (tid < kBins && most(after) >= goal && (tid == 0 || most(before) < goal)) sh.lo = tid;
+    if (tid < kBins && after >= goal && before < goal) sh.hi = tid;
+    __syncthreads();
     if (sh.hi < kBins) {
       const float lo = static_cast<float>(sh.lo) * (1.f / kBinScale), hi = static_cast<float>(sh.hi + 1) * (1.f / kBinScale);
-      AboveBand above{scale, lo, least};
-      const int n = send_list(row, a.cluster, rank, sh, [&](float x) {
+      AboveBand band{scale, lo, least};
+      const int n = send_list(row, a.cluster, rank, sh, true, [&](float x) {
         const float e = exponents(scale, x, x).x;
         return e >= lo && e < hi;
-      }, above);
+      }, band);
       if (n >= 0) {
         if (rank == 0) {
-          uint64_t t = 0;
-          for (int i = lane; i < parts; i += 32) t += sh.sums[i];
-          const int end = list_end(n, n, warp_sum(t), scale, sh, [&](uint64_t) { return goal; });
-          const uint64_t border = sh.sorted[end - 1];
-          // the band's kept weights, summed over the list, are added to those of their warps
-          constexpr int kEach = kList / kNT;
-          uint64_t w[kEach], sum = 0, rest;
-#pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            const int at = tid * kEach + i;
-            w[i] = 0;
-            if (at < n && sh.u.list[at] >= border) w[i] = weight_of(scale, logit_at(sh.u.list[at]));
-            if (w[i] < least) w[i] = 0;
-            sum += w[i];
-          }
-          uint64_t upto = block_scan(sum, rest, sh);         // its barriers: the border has been read
-#pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            sh.sorted[tid * kEach + i] = upto;
-            upto += w[i];
-          }
-          uint64_t listed_all;
-          const uint64_t from = block_scan(tid < parts ? sh.ties[tid] : 0, listed_all, sh);
-          if (tid < parts) {
-            const uint64_t to = from + sh.ties[tid];
-            sh.kept[tid] += (to < kList ? sh.sorted[to] : rest) - (from < kList ? sh.sorted[from] : rest);
+          uint64_t above = 0;
+          for (int i = lane; i < parts; i += 32) above += sh.sums[i];
+          const uint64_t border = list_border(n, n, warp_sum(above), scale, sh, [&](uint64_t) { return goal; });
+          __syncthreads();
+          // the band's kept weights are added to those of their warps
+          for (int i = tid; i < n; i += kNT) {
+            const uint64_t place = sh.list[i];
+            const uint64_t w = place >= border ? weight_of(scale, logit_at(place)) : 0;
+            if (w >= least && w > 0)
+              atomicAdd(reinterpret_cast<unsigned long long*>(&sh.kept[(index_at(place) + row.off) / R::VEC / a.piece]), w);
           }
           __syncthreads();
           if (warp == 0) {
@@ -955,8 +1040,9 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
               st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.found), lane), sh.found);
               st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.goal), lane), sh.goal);
               st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.before), lane), sh.before);
+              st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.border), lane), border);
             }
-            if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.border), lane), border);
+            if (lane == 0) sh.border = border;
           }
         }
         ptx::cluster_sync();
