@@ -46,7 +46,7 @@ constexpr int kCachedBytes = 176 * 1024;     // of a row's piece in a block's sh
 constexpr int kPairBytes = 64 * 1024;        // of that, where two blocks share an SM
 constexpr int kList = 2048;                  // tokens that the first block looks through
 constexpr int kEach = kList / kNT;
-constexpr int kFew = 128;                    // of these, as many as are compared pair by pair
+constexpr int kFew = 256;                    // of these, as many as are compared pair by pair
 constexpr int kBins = 256;                   // of a in [0, 32)
 constexpr float kBinScale = 8.f;
 constexpr int kCopies = 16;                  // of the histogram, two lanes each
@@ -124,8 +124,11 @@ struct Shared {
   uint32_t ties[kMaxParts];         // tokens at the border, or for the list
   uint32_t best[kMaxCluster];
   uint64_t scan[kWarps];
+  uint32_t or_some[2], or_none[2];
   uint32_t digit;
+  uint32_t own, base;               // tokens that this block has for the list, and where they go
   uint32_t listed;                  // tokens sent to this block's list
+  uint32_t number[kMaxCluster];     // every block's
   uint64_t left;
   int found;                        // part that holds the goal
   uint64_t goal, before;
@@ -145,6 +148,7 @@ struct Shared {
       uint32_t count[kDigit], lo[kDigit], hi[kDigit];
     } places;
     uint64_t weights[kFew];
+    uint64_t own[kList];
   } u;
 };
 
@@ -194,15 +198,19 @@ struct Row {
     }
     return v;
   }
-  // Logits of the vector this lane has at step q0 (of v0, v0 + 32, ..); past the piece: -inf.
+  // Logits of the vector this lane has at step q0 (of v0, v0 + 32, .. below v1); past the piece: -inf.
   __device__ __forceinline__ void get(int q0, int lane, float (&x)[VEC]) const {
-    const int q = q0 + lane;
-    if (q >= v1) {
+    if constexpr (kCached) {
+      Elem<T>::get(kept[q0 + lane - v0], x);       // the load filled up the last step
+    } else {
+      const int q = q0 + lane;
+      if (q >= v1) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) x[i] = -INFINITY;
-      return;
+        for (int i = 0; i < VEC; ++i) x[i] = -INFINITY;
+        return;
+      }
+      Elem<T>::get(fetch(q), x);
     }
-    Elem<T>::get(kCached ? kept[q - v0] : fetch(q), x);
   }
 };
 
@@ -222,44 +230,43 @@ __device__ __forceinline__ float exponents(const Scale& s, const float (&x)[VEC]
 template <int VEC>
 __device__ __forceinline__ void weigh(const Scale& s, const float (&x)[VEC], uint64_t (&w)[VEC]) {
   float2 a[VEC / 2];
-  const float nearest = exponents(s, x, a);
-  if (nearest >= kNone) {
+  exponents(s, x, a);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] = 0;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) a[i] = weights38(a[i]);
-  if (nearest >= kSmall) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] = whole_small(i & 1 ? a[i / 2].y : a[i / 2].x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] = whole(i & 1 ? a[i / 2].y : a[i / 2].x);
+  for (int i = 0; i < VEC / 2; ++i) {
+    const Pair y = powers(a[i]);
+    w[2 * i] = whole(y.p.x, y.k.x);
+    w[2 * i + 1] = whole(y.p.y, y.k.y);
   }
 }
 
-// The sum of a vector's weights of at least `least`.
+// The sum of a vector's weights of at least `least`, from their a.
 template <int VEC>
-__device__ __forceinline__ uint64_t weight_sum(const Scale& s, const float (&x)[VEC], uint64_t least) {
-  float2 a[VEC / 2];
-  const float nearest = exponents(s, x, a);
-  if (nearest >= kNone) return 0;
+__device__ __forceinline__ uint64_t weight_sum(const float2 (&a)[VEC / 2], float nearest, uint64_t least) {
   uint64_t sum = 0;
-#pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) a[i] = weights38(a[i]);
+  if (nearest >= kNone) return 0;
   if (nearest >= kSmall) {
-    const uint32_t low = static_cast<uint32_t>(min(least, static_cast<uint64_t>(0xFFFFFFFFu)));    // such a weight is below 2^32 - 1
+    const uint32_t low = static_cast<uint32_t>(min(least, static_cast<uint64_t>(0xFFFFFFFFu)));
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const uint32_t w = whole_small(i & 1 ? a[i / 2].y : a[i / 2].x);
-      sum += w >= low ? w : 0;
+    for (int g = 0; g < VEC; g += 4) {           // four of them have 32 bits
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Pair y = powers(a[g / 2 + i]);
+        w[2 * i] = whole_small(y.p.x, y.k.x);
+        w[2 * i + 1] = whole_small(y.p.y, y.k.y);
+      }
+      if (low) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = w[i] >= low ? w[i] : 0;
+      }
+      sum += w[0] + w[1] + w[2] + w[3];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const uint64_t w = whole(i & 1 ? a[i / 2].y : a[i / 2].x);
-      sum += w >= least ? w : 0;
+    for (int i = 0; i < VEC / 2; ++i) {
+      const Pair y = powers(a[i]);
+      const uint64_t w0 = whole(y.p.x, y.k.x), w1 = whole(y.p.y, y.k.y);
+      sum += (w0 >= least ? w0 : 0) + (w1 >= least ? w1 : 0);
     }
   }
   return sum;
@@ -294,11 +301,6 @@ __device__ void part_sums(const R& row, const Scale& s, const Border& b, uint64_
     st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.ties[part]), lane), ties);
   }
   ptx::cluster_sync();
-}
-
-// The weight of one logit.
-__device__ __forceinline__ uint64_t weight_of(const Scale& s, float x) {
-  return whole(weights38(exponents(s, x, x)).x);
 }
 
 // Total of the parts: weight above the border and that of the ties that are kept.  All lanes of a warp.
@@ -428,67 +430,83 @@ __device__ float bound_of(float v, int j, float low, float top) {
   return low;
 }
 
-// Each warp's tokens for the list, `in(x)` says which, to the first block's list in no order.  Their
-// number, or -1 if they are more than fit.  All threads of the cluster; ends with its barrier.
-// some: whether the lane has any.  extra(x): called with every vector's logits.
-template <typename R, typename In, typename Extra>
-__device__ int send_list(const R& row, int cluster, int rank, Shared& sh, bool some, const In& in, Extra& extra) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = rank * kWarps + warp, parts = cluster * kWarps;
-  uint32_t mine = 0;
+// Each block's tokens for the list to the first block's, in no order.  Their number, or -1 if they are more
+// than fit.  All threads of the cluster; ends with its barrier.  some: whether the lane has any.
+// step(x, in): marks those of a vector's logits.
+template <typename R, typename Step>
+__device__ int send_list(const R& row, int cluster, int rank, Shared& sh, bool some, Step& step) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (__any_sync(~0u, some)) {
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
+      bool in[R::VEC];
       row.get(q0, lane, x);
-      extra(x);
+      step(x, in);
+      uint32_t mine = 0;
 #pragma unroll
-      for (int i = 0; i < R::VEC; ++i) mine += in(x[i]);
-    }
-  }
-  uint32_t inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t t = __shfl_up_sync(~0u, inc, o);
-    if (lane >= o) inc += t;
-  }
-  const uint32_t all = __shfl_sync(~0u, inc, 31);
-  extra.send(part, cluster, lane, sh);
-  if (lane < cluster) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.ties[part]), lane), all);
-  if (all) {
-    uint32_t at = 0;
-    if (lane == 0) at = atom_cluster_add(ptx::mapa_shared(ptx::smem_u32(&sh.listed), 0), all);
-    at = __shfl_sync(~0u, at, 0) + inc - mine;
-    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(sh.list), 0);
-    for (int q0 = row.v0; q0 < row.v1 && __any_sync(~0u, mine); q0 += 32) {
-      float x[R::VEC];
-      row.get(q0, lane, x);
+      for (int i = 0; i < R::VEC; ++i) mine += in[i];
+      if (mine == 0) continue;
+      uint32_t at = atomicAdd(&sh.own, mine);
 #pragma unroll
       for (int i = 0; i < R::VEC; ++i) {
-        if (in(x[i])) {
-          if (at < kList) st_cluster_u64(to + 8 * at, place_of(x[i], (q0 + lane) * R::VEC - row.off + i));
-          ++at, --mine;
-        }
+        if (in[i] && at < kList) sh.u.own[at] = place_of(x[i], (q0 + lane) * R::VEC - row.off + i);
+        at += in[i];
       }
     }
   }
+  step.send(rank * kWarps + warp, cluster, lane, sh);
+  __syncthreads();
+  const uint32_t mine = sh.own;
+  if (tid == 0) sh.base = mine ? atom_cluster_add(ptx::mapa_shared(ptx::smem_u32(&sh.listed), 0), mine) : 0;
+  if (tid < cluster) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.number[rank]), tid), mine);
+  __syncthreads();
+  const uint32_t base = sh.base;
+  if (mine <= kList && base + mine <= kList) {
+    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(sh.list + base), 0);
+    for (uint32_t i = tid; i < mine; i += kNT) st_cluster_u64(to + 8 * i, sh.u.own[i]);
+  }
   ptx::cluster_sync();
   uint32_t n = 0;
-  for (int i = lane; i < parts; i += 32) n += sh.ties[i];
-  n = __reduce_add_sync(~0u, n);
+  for (int c = 0; c < cluster; ++c) n += min(sh.number[c], static_cast<uint32_t>(kList + 1));
   return n > kList ? -1 : static_cast<int>(n);
 }
 
 // The block's threads: of tokens with these keys and weights (kEach a thread), the one whose weight takes the
 // running weight, from the largest key down, to `need` or more: its key, and the weight before it.
-// kCount: the need-th by number.  Digit by digit from the highest of `bits`, until the tokens that are left
-// are one.  Keys differ from one another; tokens with `in` false are left out.
+// kCount: the need-th by number.  Digit by digit from the highest of `bits` in which keys differ, until
+// the tokens that are left are one.  Keys differ from one another; tokens with `in` false are left out.
 template <bool kCount>
 __device__ uint64_t pick(const uint64_t (&key)[kEach], const uint64_t (&w)[kEach], const bool (&in)[kEach], int bits,
                          uint64_t need, Shared& sh, uint64_t& weight_before) {
   const int tid = threadIdx.x;
   uint64_t prefix = 0, before = 0;
   int shift = bits;
-  while (true) {
+  {
+    // the digits begin where keys differ: bits that are set in some and not in others
+    uint32_t some[2] = {0, 0}, none[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (!in[i]) continue;
+      some[0] |= static_cast<uint32_t>(key[i]), some[1] |= static_cast<uint32_t>(key[i] >> 32);
+      none[0] |= ~static_cast<uint32_t>(key[i]), none[1] |= ~static_cast<uint32_t>(key[i] >> 32);
+    }
+    if (tid == 0) sh.or_some[0] = sh.or_some[1] = sh.or_none[0] = sh.or_none[1] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a = __reduce_or_sync(~0u, some[h]), b = __reduce_or_sync(~0u, none[h]);
+      if ((tid & 31) == 0) {
+        atomicOr(&sh.or_some[h], a);
+        atomicOr(&sh.or_none[h], b);
+      }
+    }
+    __syncthreads();
+    const uint64_t all = static_cast<uint64_t>(sh.or_some[1]) << 32 | sh.or_some[0];
+    const uint64_t differ = all & (static_cast<uint64_t>(sh.or_none[1]) << 32 | sh.or_none[0]);
+    shift = min(bits, 64 - __clzll(static_cast<long long>(differ)));
+    if (shift < 64) prefix = all >> shift;
+  }
+  while (shift > 0) {
     const int low = max(shift - 10, 0), size = 1 << (shift - low);
     for (int i = tid; i < kDigit; i += kNT) sh.u.places.count[i] = sh.u.places.lo[i] = sh.u.places.hi[i] = 0;
     __syncthreads();
@@ -531,7 +549,7 @@ __device__ uint64_t pick(const uint64_t (&key)[kEach], const uint64_t (&w)[kEach
     const bool one = sh.before == 1;
     shift = low;
     __syncthreads();
-    if (one || shift == 0) break;
+    if (one) break;
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
@@ -550,26 +568,25 @@ template <typename GoalOf>
 __device__ uint64_t list_border(int n, int most, uint64_t above, const Scale& s, Shared& sh, const GoalOf& goal_of) {
   const int tid = threadIdx.x;
   if (n <= kFew) {
-    // four threads a token, each against a quarter of the others
-    static_assert(4 * kFew == kNT, "");
-    const int e = tid >> 2;
+    // 2 or 4 threads a token, each against a share of the others
+    const int log = n <= kNT / 4 ? 2 : 1, each = 1 << log, e = tid >> log;
     const uint64_t mine = e < n ? sh.list[e] : 0;
     const uint64_t w = e < n ? weight_of(s, logit_at(mine)) : 0;
-    if ((tid & 3) == 0) sh.u.weights[e] = w;
+    const bool first = (tid & (each - 1)) == 0;
+    if (first && e < kFew) sh.u.weights[e] = w;
     __syncthreads();
     uint64_t before = 0;
     int rank = 0;
-    for (int j = tid & 3; j < n; j += 4) {
+    for (int j = tid & (each - 1); j < n; j += each) {
       const bool earlier = sh.list[j] > mine;
       before += earlier ? sh.u.weights[j] : 0;
       rank += earlier;
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
+    for (int o = 1; o < each; o <<= 1) {
       before += __shfl_xor_sync(~0u, before, o);
       rank += __shfl_xor_sync(~0u, rank, o);
     }
-    if (e < n && rank == most - 1 && (tid & 3) == 0) {
+    if (e < n && rank == most - 1 && first) {
       sh.total = before + w;
       sh.border = mine;
     }
@@ -577,7 +594,7 @@ __device__ uint64_t list_border(int n, int most, uint64_t above, const Scale& s,
     const uint64_t goal = goal_of(sh.total);
     __syncthreads();
     before += above;
-    if (e < n && rank < most && before < goal && before + w >= goal && (tid & 3) == 0) sh.border = mine;
+    if (e < n && rank < most && before < goal && before + w >= goal && first) sh.border = mine;
     __syncthreads();
     const uint64_t border = sh.border;
     return border;
@@ -607,26 +624,37 @@ __device__ uint64_t list_border(int n, int most, uint64_t above, const Scale& s,
   return pick<false>(key, w, in, 64, goal - above, sh, before);
 }
 
-struct NoExtra {
+// The marks for send_list: logits of at least the bound.
+struct AboveBound {
+  float bound;
   template <int VEC>
-  __device__ __forceinline__ void operator()(const float (&)[VEC]) {}
+  __device__ __forceinline__ void operator()(const float (&x)[VEC], bool (&in)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) in[i] = x[i] >= bound && x[i] > -INFINITY;
+  }
   __device__ __forceinline__ void send(int, int, int, Shared&) {}
 };
 
-// Weights above the band, of each warp.
-struct AboveBand {
+// Those with a in [lo, hi); and the weights above, of each warp.
+struct InBand {
   Scale s;
-  float lo;            // a of the band's first bin
+  float lo, hi;
   uint64_t least;
   uint64_t sum = 0, kept = 0;
   template <int VEC>
-  __device__ __forceinline__ void operator()(const float (&x)[VEC]) {
+  __device__ __forceinline__ void operator()(const float (&x)[VEC], bool (&in)[VEC]) {
     float2 a[VEC / 2];
-    if (exponents(s, x, a) >= lo) return;
+    const float nearest = exponents(s, x, a);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float e = i & 1 ? a[i / 2].y : a[i / 2].x;
+      in[i] = e >= lo && e < hi;
+    }
+    if (nearest >= lo) return;
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) {
-      const float2 y = weights38(a[i]);
-      const uint64_t w0 = a[i].x < lo ? whole(y.x) : 0, w1 = a[i].y < lo ? whole(y.y) : 0;
+      const Pair y = powers(a[i]);
+      const uint64_t w0 = a[i].x < lo ? whole(y.p.x, y.k.x) : 0, w1 = a[i].y < lo ? whole(y.p.y, y.k.y) : 0;
       sum += w0 + w1;
       kept += (w0 >= least ? w0 : 0) + (w1 >= least ? w1 : 0);
     }
@@ -788,15 +816,18 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
   // the row, once, and its largest logit
   float top = -INFINITY;
   constexpr int kInFlight = 4;
-  for (int q0 = row.v0 + lane; q0 < row.v1; q0 += 32 * kInFlight) {
+  for (int q0 = row.v0; q0 < row.v1; q0 += 32 * kInFlight) {
     uint4 v[kInFlight];
 #pragma unroll
-    for (int i = 0; i < kInFlight; ++i)
-      if (q0 + i * 32 < row.v1) v[i] = row.fetch(q0 + i * 32);
+    for (int i = 0; i < kInFlight; ++i) {
+      const int q = q0 + i * 32 + lane;
+      v[i] = make_uint4(Elem<T>::kLowest, Elem<T>::kLowest, Elem<T>::kLowest, Elem<T>::kLowest);
+      if (q < row.v1) v[i] = row.fetch(q);
+    }
 #pragma unroll
     for (int i = 0; i < kInFlight; ++i) {
-      if (q0 + i * 32 >= row.v1) continue;
-      if (kCached) row.kept[q0 + i * 32 - row.v0] = v[i];
+      if (q0 + i * 32 >= row.v1) break;
+      if (kCached) row.kept[q0 + i * 32 + lane - row.v0] = v[i];
       float x[R::VEC];
       Elem<T>::get(v[i], x);
 #pragma unroll
@@ -819,7 +850,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
   if (lane == 0) {
     sh.warp_top[warp] = top;
     sh.warp_low[warp] = low;
-    sh.listed = 0;
+    sh.listed = sh.own = 0;
   }
   __syncthreads();
   top = sh.warp_top[lane % kWarps];
@@ -881,7 +912,9 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
       row.get(q0, lane, x);
-      sum += weight_sum(scale, x, least);
+      float2 e[R::VEC / 2];
+      const float nearest = exponents(scale, x, e);
+      sum += weight_sum<R::VEC>(e, nearest, least);
     }
     sum = warp_sum(sum);
     if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
@@ -894,36 +927,35 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
   }
 
   if (listed) {
-    NoExtra none;
-    const int n = send_list(row, a.cluster, rank, sh, mine >= bound && mine > -INFINITY,
-                            [&](float x) { return x >= bound && x > -INFINITY; }, none);
+    AboveBound above{bound};
+    const int n = send_list(row, a.cluster, rank, sh, mine >= bound && mine > -INFINITY, above);
     if (n >= 0) {
       if (rank != 0) return;
       // fewer than top_k only where the row has no more above -inf
       const uint64_t border = list_border(n, min(n, top_k), 0, scale, sh,
                                           [&](uint64_t total) { return by_p ? p_goal(total) : ~0ull; });
       if (n <= kFew) {
-        const int e = tid >> 2;
+        const int log = n <= kNT / 4 ? 2 : 1, part_of = 1 << log, e = tid >> log;
+        const bool first = (tid & (part_of - 1)) == 0;
         const uint64_t place = e < n ? sh.list[e] : 0;
         uint64_t w = e < n && place >= border ? sh.u.weights[e] : 0;
         if (w < least) w = 0;
         __syncthreads();
-        if ((tid & 3) == 0) sh.u.weights[e] = w;
+        if (first && e < kFew) sh.u.weights[e] = w;
         __syncthreads();
         const uint32_t at = static_cast<uint32_t>(place);          // larger: an earlier index
         uint64_t before = 0, total = 0;
-        for (int j = tid & 3; j < n; j += 4) {
+        for (int j = tid & (part_of - 1); j < n; j += part_of) {
           const uint64_t v = sh.u.weights[j];
           total += v;
           before += static_cast<uint32_t>(sh.list[j]) > at ? v : 0;
         }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
+        for (int o = 1; o < part_of; o <<= 1) {
           before += __shfl_xor_sync(~0u, before, o);
           total += __shfl_xor_sync(~0u, total, o);
         }
         const uint64_t goal = goal_of(u, total);
-        if (goal >= before && goal < before + w && (tid & 3) == 0) *token = index_at(place);
+        if (goal >= before && goal < before + w && first) *token = index_at(place);
         return;
       }
       uint64_t key[kEach], w[kEach], sum = 0, total;
@@ -958,18 +990,18 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
       auto count = [&](auto small) {
 #pragma unroll
         for (int i = 0; i < R::VEC / 2; ++i) {
-          const float2 y = weights38(e[i]);
+          const Pair y = powers(e[i]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float at = h ? e[i].y : e[i].x, v = h ? y.y : y.x;
+            const float at = h ? e[i].y : e[i].x, p = h ? y.p.y : y.p.x, k = h ? y.k.y : y.k.x;
             // the bin, from the low bits of at + 1.5 2^20 (steps of 2^-3) rounded down
             const int bin = __float_as_uint(__fadd_rd(at, 1572864.f)) & 0x3FFu;
             if constexpr (decltype(small)::value) {
-              const uint32_t w = whole_small(v);
+              const uint32_t w = whole_small(p, k);
               sum += w;
               if (bin < kBins) atomicAdd(copy + bin * kCopies, w >> max(23 - (bin >> 3), 0));
             } else {
-              const uint64_t w = whole(v);
+              const uint64_t w = whole(p, k);
               sum += w;
               if (bin < kBins) atomicAdd(copy + bin * kCopies, static_cast<uint32_t>(w >> max(23 - (bin >> 3), 0)));
             }
@@ -1015,11 +1047,8 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
     __syncthreads();
     if (sh.hi < kBins) {
       const float lo = static_cast<float>(sh.lo) * (1.f / kBinScale), hi = static_cast<float>(sh.hi + 1) * (1.f / kBinScale);
-      AboveBand band{scale, lo, least};
-      const int n = send_list(row, a.cluster, rank, sh, true, [&](float x) {
-        const float e = exponents(scale, x, x).x;
-        return e >= lo && e < hi;
-      }, band);
+      InBand band{scale, lo, hi, least};
+      const int n = send_list(row, a.cluster, rank, sh, true, band);
       if (n >= 0) {
         if (rank == 0) {
           uint64_t above = 0;
