@@ -51,64 +51,161 @@ __global__ void __launch_bounds__(kCopyNT) copy_pages_kernel(uint4* k, uint4* v,
 }
 
 // ---------------------------------------------------------------- rows moved together
+// Row i comes from path[i] >= i, and later rows from later places still: what the rows up
+// to i write no later row reads.  So rows move in ascending order, a group at a time, all of
+// a group read before any of it is written; the next group's reads may go out before.
+// Columns, heads, keys and values have nothing to do with one another.
 constexpr int kMoveNT = 256;
-constexpr int kMoveRows = 4;        // rows a thread has in flight
+constexpr int kMoveRows = 8;        // rows a thread has in flight, twice
+constexpr int kShort = 32;          // rows of a sequence that a block moves at once
 
-// Block (sequence, cache head, keys or values): rows move in ascending order, a
-// group of them at a time, all read before any is written.  Row i comes from
-// path[i] >= i, and later rows from later places still, so what a group writes
-// no later group reads.
-__global__ void __launch_bounds__(kMoveNT)
-    compact_kernel(uint4* k, uint4* v, int64_t pages, int heads_kv, int row_vecs, SeqArgs s, const int32_t* path,
-                   int width, const int32_t* count, uint32_t* err) {
+struct MoveArgs {
+  uint4* k;
+  uint4* v;
+  int64_t pages;
+  int heads_kv, row_vecs;
+  SeqArgs s;
+  const int32_t* path;
+  int width;
+  const int32_t* count;
+  uint32_t* err;
+};
+
+// The sequence and its rows; false (the same in all threads) if there is nothing to move.
+__device__ __forceinline__ bool move_begin(const MoveArgs& a, int b, bool tell, at::Seq& q, int& n) {
+  q = at::load_seq(a.s, b, tell ? a.err : nullptr);
+  n = ptx::ld_after_wait(a.count + b);
+  const int32_t* row = a.path + static_cast<int64_t>(b) * a.width;
+  bool bad = n < 0 || n > a.width || (n > 0 && q.len < q.n);
+  if (!bad) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kMoveNT) {
+      const int x = ptx::ld_after_wait(row + i), before = i > 0 ? ptx::ld_after_wait(row + i - 1) : -1;
+      bad = bad || x >= q.n || before >= x || x < 0;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tell && n != 0) atomicOr(a.err, kErrIndexRange);
+  return !bad && n > 0;
+}
+
+// The cache row of head 0 that slot `slot` of sequence b lies in, or -1.
+__device__ __forceinline__ int64_t move_row(const MoveArgs& a, int b, int slot) {
+  const int pid = ptx::ld_after_wait(a.s.table + static_cast<int64_t>(b) * a.s.table_pages + (slot >> a.s.page_shift));
+  if (pid < 0 || pid >= a.pages) {
+    atomicOr(a.err, kErrIndexRange);
+    return -1;
+  }
+  return (static_cast<int64_t>(pid) * a.heads_kv << a.s.page_shift) + (slot & ((1 << a.s.page_shift) - 1));
+}
+
+// Paths of at most kShort rows: a block has some heads of one sequence.
+__global__ void __launch_bounds__(kMoveNT) compact_short_kernel(const __grid_constant__ MoveArgs a, int splits) {
+  __shared__ int64_t from[kShort], to[kShort];
+  __shared__ int moving;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int tid = threadIdx.x;
-  const int b = blockIdx.x / (2 * heads_kv), part = blockIdx.x - b * (2 * heads_kv);
-  const int h = part % heads_kv;
-  uint4* cache = part < heads_kv ? k : v;
-  const at::Seq q = at::load_seq(s, b, tid == 0 ? err : nullptr);
-  const int n = ptx::ld_after_wait(count + b);
-  const int32_t* row = path + static_cast<int64_t>(b) * width;
-  bool bad = n < 0 || n > width || (n > 0 && q.len < q.n);
-  for (int i = tid; i < n && !bad; i += kMoveNT) {
-    const int x = ptx::ld_after_wait(row + i);
-    bad = x < 0 || x >= q.n || (i > 0 && ptx::ld_after_wait(row + i - 1) >= x);
-  }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0 && n != 0) atomicOr(err, kErrIndexRange);
-    return;
-  }
-  const int base = q.len - q.n, page = 1 << s.page_shift;
-  const int32_t* table = s.table + static_cast<int64_t>(b) * s.table_pages;
-  auto place = [&](int slot) -> uint4* {
-    const int pid = ptx::ld_after_wait(table + (slot >> s.page_shift));
-    if (pid < 0 || pid >= pages) {
-      atomicOr(err, kErrIndexRange);
-      return nullptr;
+  const int b = blockIdx.x / splits, split = blockIdx.x - b * splits;
+  at::Seq q;
+  int n;
+  if (!move_begin(a, b, tid == 0 && split == 0, q, n)) return;
+  if (tid < 32) {
+    const int x = tid < n ? ptx::ld_after_wait(a.path + static_cast<int64_t>(b) * a.width + tid) : tid;
+    const bool moves = x != tid;
+    const uint32_t all = __ballot_sync(~0u, moves);
+    if (moves) {
+      const int i = __popc(all & ((1u << tid) - 1));
+      const int64_t f = move_row(a, b, q.len - q.n + x), t = move_row(a, b, q.len - q.n + tid);
+      from[i] = t < 0 ? -1 : f;
+      to[i] = t;
     }
-    return cache + (((static_cast<int64_t>(pid) * heads_kv + h) << s.page_shift) + (slot & (page - 1))) * row_vecs;
-  };
-  const int lanes = kMoveNT / row_vecs, at = tid / row_vecs, vec = tid - at * row_vecs;    // row_vecs <= 64
-  for (int i0 = 0; i0 < n; i0 += lanes * kMoveRows) {
+    if (tid == 0) moving = __popc(all);
+  }
+  __syncthreads();
+  // units (a head's keys or values), each `each` vectors, as many as the registers hold at a time
+  const int units = 2 * a.heads_kv, each = moving * a.row_vecs;
+  if (each == 0) return;
+  const int u0 = units * split / splits, u1 = units * (split + 1) / splits;
+  const int step = max(1, kMoveNT * kMoveRows / each);       // 32 rows of 64 vectors are 2048: one unit fits
+  for (int u = u0; u < u1; u += step) {
+    const int items = min(step, u1 - u) * each;
     uint4 x[kMoveRows];
-    uint4* to[kMoveRows];
+    uint4* out[kMoveRows];
 #pragma unroll
     for (int r = 0; r < kMoveRows; ++r) {
-      const int i = i0 + r * lanes + at;
-      to[r] = nullptr;
-      if (at >= lanes || i >= n) continue;
-      const int from = ptx::ld_after_wait(row + i);
-      if (from == i) continue;
-      const uint4* p = place(base + from);
-      to[r] = place(base + i);
-      if (!p) to[r] = nullptr;
-      if (to[r]) x[r] = ptx::ld_after_wait(p + vec);
+      const int item = r * kMoveNT + tid;
+      out[r] = nullptr;
+      if (item >= items) continue;
+      const int unit = item / each, in = item - unit * each, row = in / a.row_vecs, vec = in - row * a.row_vecs;
+      if (from[row] < 0) continue;
+      const int h = (u + unit) % a.heads_kv;
+      uint4* cache = u + unit < a.heads_kv ? a.k : a.v;
+      const int64_t head = static_cast<int64_t>(h) << a.s.page_shift;
+      x[r] = ptx::ld_after_wait(cache + (from[row] + head) * a.row_vecs + vec);
+      out[r] = cache + (to[row] + head) * a.row_vecs + vec;
     }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kMoveRows; ++r)
-      if (to[r]) to[r][vec] = x[r];
+      if (out[r]) *out[r] = x[r];
+  }
+}
+
+// Longer ones: a block has `strip` vectors of every row of one head's keys or values.
+__global__ void __launch_bounds__(kMoveNT) compact_kernel(const __grid_constant__ MoveArgs a, int strip, int strips) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int tid = threadIdx.x;
+  const int unit = blockIdx.x / strips, col = (blockIdx.x - unit * strips) * strip;
+  const int b = unit / (2 * a.heads_kv), part = unit - b * (2 * a.heads_kv);
+  at::Seq q;
+  int n;
+  if (!move_begin(a, b, tid == 0 && col == 0, q, n)) return;
+  uint4* cache = part < a.heads_kv ? a.k : a.v;
+  const int64_t head = static_cast<int64_t>(part % a.heads_kv) << a.s.page_shift;
+  const int32_t* path = a.path + static_cast<int64_t>(b) * a.width;
+  const int base = q.len - q.n;
+  const int lanes = kMoveNT / strip, at = tid / strip, vec = col + tid - at * strip;
+  const bool live = at < lanes && vec < a.row_vecs;
+  const int group = lanes * kMoveRows;
+  // the rows of a group that this thread moves: what they are, and where they go (null: nowhere)
+  auto load = [&](int i0, uint4 (&x)[kMoveRows], uint4* (&to)[kMoveRows]) {
+    int from[kMoveRows];
+#pragma unroll
+    for (int r = 0; r < kMoveRows; ++r) {
+      const int i = i0 + r * lanes + at;
+      from[r] = live && i < n ? ptx::ld_after_wait(path + i) : i;
+      if (from[r] == i) from[r] = -1;
+    }
+    int64_t f[kMoveRows], t[kMoveRows];
+#pragma unroll
+    for (int r = 0; r < kMoveRows; ++r) {
+      f[r] = from[r] < 0 ? -1 : move_row(a, b, base + from[r]);
+      t[r] = from[r] < 0 ? -1 : move_row(a, b, base + i0 + r * lanes + at);
+    }
+#pragma unroll
+    for (int r = 0; r < kMoveRows; ++r) {
+      to[r] = nullptr;
+      if (f[r] < 0 || t[r] < 0) continue;
+      to[r] = cache + (t[r] + head) * a.row_vecs + vec;
+      x[r] = ptx::ld_after_wait(cache + (f[r] + head) * a.row_vecs + vec);
+    }
+  };
+  uint4 x[2][kMoveRows];
+  uint4* to[2][kMoveRows];
+  load(0, x[0], to[0]);
+  for (int i0 = 0; i0 < n; i0 += 2 * group) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at0 = i0 + h * group;
+      if (at0 >= n) break;
+      load(at0 + group, x[h ^ 1], to[h ^ 1]);
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kMoveRows; ++r)
+        if (to[h][r]) *to[h][r] = x[h][r];
+    }
   }
 }
 
@@ -325,9 +422,23 @@ cudaError_t launch_copy_pages(const engram_kv_cache* c, const int32_t* pairs, in
 cudaError_t launch_compact(const engram_kv_cache* c, const SeqArgs& seq, const int32_t* path, int width,
                            const int32_t* count, cudaStream_t s) {
   const engram_attn_config_t& g = c->plan->cfg;
-  const int vecs = g.head_dim * (g.dtype == ENGRAM_F32 ? 4 : 2) / 16;
-  return launch_pdl(compact_kernel, dim3(static_cast<unsigned>(seq.B) * 2 * g.heads_kv), dim3(kMoveNT), 0, s, static_cast<uint4*>(c->k),
-                    static_cast<uint4*>(c->v), c->pages, g.heads_kv, vecs, seq, path, width, count, c->plan->err);
+  const int vecs = g.head_dim * (g.dtype == ENGRAM_F32 ? 4 : 2) / 16, sms = c->plan->num_sms;
+  const MoveArgs a{static_cast<uint4*>(c->k), static_cast<uint4*>(c->v), c->pages, g.heads_kv, vecs, seq, path, width,
+                   count, c->plan->err};
+  if (width <= kShort) {
+    // few sequences: their heads over more blocks
+    int splits = 1;
+    while (splits < g.heads_kv && static_cast<int64_t>(seq.B) * splits * 2 <= sms) splits *= 2;
+    return launch_pdl(compact_short_kernel, dim3(static_cast<unsigned>(seq.B) * splits), dim3(kMoveNT), 0, s, a, splits);
+  }
+  // columns apart, 32 bytes at least (a sector), until there are four blocks an SM
+  int strip = vecs, strips = 1;
+  while (strip > 2 && static_cast<int64_t>(seq.B) * 2 * g.heads_kv * strips < 4 * sms) {
+    strip = (strip + 1) / 2 + ((strip + 1) / 2 & 1);
+    strips = (vecs + strip - 1) / strip;
+  }
+  return launch_pdl(compact_kernel, dim3(static_cast<unsigned>(seq.B) * 2 * g.heads_kv * strips), dim3(kMoveNT), 0, s, a,
+                    strip, strips);
 }
 
 cudaError_t launch_pool_free(const engram_attn_plan* plan, const engram_pool_t& p, const int32_t* rows,

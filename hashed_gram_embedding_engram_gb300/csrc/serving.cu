@@ -78,7 +78,7 @@ engram_status_t engram_kv_compact(engram_kv_cache_t* cache, const engram_sequenc
   if (!seq || seq->B < 0 || !table_pages_ok(plan, seq->table_pages) || width < 1) return ENGRAM_ERR_INVALID_ARG;
   if (seq->B == 0) return ENGRAM_OK;
   if (!seq->start || !seq->length || !seq->table || !path || !count) return ENGRAM_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(seq->B) * 2 * plan->cfg.heads_kv > INT32_MAX) return ENGRAM_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(seq->B) * 2 * plan->cfg.heads_kv > INT32_MAX / 64) return ENGRAM_ERR_UNSUPPORTED;
   if (engram_status_t e = device_ok(plan)) return e;
   SeqArgs s = seq_of(plan, seq);
   s.tokens = INT32_MAX;           // the packed rows are not touched
