@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kCopyNT) copy_pages_kernel(uint4* k, uint4* v,
 // a group read before any of it is written; the next group's reads may go out before.
 // Columns, heads, keys and values have nothing to do with one another.
 constexpr int kMoveNT = 256;
-constexpr int kMoveRows = 8;        // rows a thread has in flight, twice
+constexpr int kMoveRows = 4;        // rows a thread has in flight, twice
+constexpr int kShortRows = 8;       // the same for short paths, once
 constexpr int kShort = 32;          // rows of a sequence that a block moves at once
 
 struct MoveArgs {
@@ -127,13 +128,13 @@ __global__ void __launch_bounds__(kMoveNT) compact_short_kernel(const __grid_con
   const int units = 2 * a.heads_kv, each = moving * a.row_vecs;
   if (each == 0) return;
   const int u0 = units * split / splits, u1 = units * (split + 1) / splits;
-  const int step = max(1, kMoveNT * kMoveRows / each);       // 32 rows of 64 vectors are 2048: one unit fits
+  const int step = max(1, kMoveNT * kShortRows / each);       // 32 rows of 64 vectors are 2048: one unit fits
   for (int u = u0; u < u1; u += step) {
     const int items = min(step, u1 - u) * each;
-    uint4 x[kMoveRows];
-    uint4* out[kMoveRows];
+    uint4 x[kShortRows];
+    uint4* out[kShortRows];
 #pragma unroll
-    for (int r = 0; r < kMoveRows; ++r) {
+    for (int r = 0; r < kShortRows; ++r) {
       const int item = r * kMoveNT + tid;
       out[r] = nullptr;
       if (item >= items) continue;
@@ -147,13 +148,13 @@ __global__ void __launch_bounds__(kMoveNT) compact_short_kernel(const __grid_con
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kMoveRows; ++r)
+    for (int r = 0; r < kShortRows; ++r)
       if (out[r]) *out[r] = x[r];
   }
 }
 
 // Longer ones: a block has `strip` vectors of every row of one head's keys or values.
-__global__ void __launch_bounds__(kMoveNT) compact_kernel(const __grid_constant__ MoveArgs a, int strip, int strips) {
+__global__ void __launch_bounds__(kMoveNT, 4) compact_kernel(const __grid_constant__ MoveArgs a, int strip, int strips) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int tid = threadIdx.x;
