@@ -77,6 +77,7 @@ inline AttnArgs attn_args(const engram_kv_cache* cache, const engram_sequences_t
   a.scale_log2 = static_cast<float>(plan->scale * 1.4426950408889634);
   a.counters = static_cast<uint32_t*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounters * 4);
+  a.splits = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kAttnCounters * 4 + attn_parts_bytes(plan));
   a.err = plan->err;
   return a;
 }
@@ -88,7 +89,7 @@ inline cudaError_t launch_attention(const engram_kv_cache* cache, const AttnArgs
   if (max_new > seq->tokens) max_new = seq->tokens;
   const int64_t rows = max_new * cache->plan->group;
   if (attention_rows_applies(cache, rows)) return launch_attention_rows(cache, a, rows, s);
-  if (cache->maps) return launch_attention_tiles(cache, a, s);
+  if (cache->maps) return launch_attention_tiles(cache, a, static_cast<int>(max_new), s);
   return launch_attention_simt(cache->plan, a, static_cast<int>(max_new), s);
 }
 

@@ -87,6 +87,7 @@ struct AttnArgs {
   const uint32_t* mask;       // trees of drafts: [tokens, words] who sees whom, and [tokens] positions
   const int32_t* positions;
   int words;
+  int32_t* splits;            // of the tiles kernel: kSplitWords for each block, or null (trees: joined after it)
 };
 
 // Which keys a new token sees: all, those up to its own, or the cached ones and its row of the mask.
@@ -96,9 +97,13 @@ constexpr int kTreeWords = 8;            // of a row of the mask, at most (32 ne
 constexpr int kAttnCounters = 4096;      // at least the blocks of any attention grid (16384 bytes, as the header says)
 constexpr int kAttnPartRows = 256;       // rows of partial tiles per SM, twice (workspace bound)
 
+constexpr int kSplitWords = 8;           // what a block of the tiles kernel leaves for the joins of a tree's tiles
+
+inline size_t attn_parts_bytes(const engram_attn_plan* p) {
+  return static_cast<size_t>(p->num_sms) * 2 * kAttnPartRows * (static_cast<size_t>(p->cfg.head_dim) + 2) * 4;
+}
 inline size_t attn_workspace_bytes(const engram_attn_plan* p) {
-  return kAttnCounters * 4 +
-         static_cast<size_t>(p->num_sms) * 2 * kAttnPartRows * (static_cast<size_t>(p->cfg.head_dim) + 2) * 4;
+  return kAttnCounters * 4 + attn_parts_bytes(p) + static_cast<size_t>(p->num_sms) * kSplitWords * 4;
 }
 
 // bf16 with heads of 64 or 128: tensor maps, the rows and the tiles kernel; else the CUDA cores.
@@ -124,7 +129,7 @@ cudaError_t launch_attention_simt(const engram_attn_plan* p, const AttnArgs& a, 
 bool attention_rows_applies(const engram_kv_cache* c, int64_t rows);
 cudaError_t launch_attention_rows(const engram_kv_cache* c, const AttnArgs& a, int64_t rows, cudaStream_t s);
 // Attention of longer chunks on the tensor cores, 256 rows a tile.
-cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, int max_new, cudaStream_t s);
 // csrc/tree.cu, pages.cu, sample.cu
 cudaError_t launch_tree_build(const SeqArgs& s, const int32_t* parent, const engram_tree_t& t, uint32_t* err,
                               cudaStream_t stream);

@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kNT, 2)
   __shared__ Shared sh;
   __shared__ float s_max[2][kWarps][RT];
   __shared__ float s_sum[kWarps][RT];
+  __shared__ float s_stats[kTree ? 2 * RT : 1];
   __shared__ __align__(16) __nv_bfloat16 s_p[2][RT * kPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -348,8 +349,13 @@ __global__ void __launch_bounds__(kNT, 2)
         }
       if (!whole) {
         const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
-        if (arrive_last<kWarps * 32>(a, cf, cl, &sh.flag, tid, 1))
-          join_tile<__nv_bfloat16, kWarps * 32, RT, true>(a, w, cf, cl, tid, 1);
+        if (arrive_last<kWarps * 32>(a, cf, cl, &sh.flag, tid, 1)) {
+          if constexpr (kTree)
+            join_tree<__nv_bfloat16, kWarps * 32, RT, 2, 4, true, false>(a, {w.q.row0, w.h, w.r}, cf, cl, 0, tile_rows(a, w, RT), tid, 1,
+                                               s_stats, nullptr);
+          else
+            join_tile<__nv_bfloat16, kWarps * 32, RT, true>(a, w, cf, cl, tid, 1);
+        }
       } else {
         ptx::named_barrier(1, kWarps * 32);          // s_sum is free for the next tile
       }

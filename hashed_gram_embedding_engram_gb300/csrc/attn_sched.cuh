@@ -529,5 +529,132 @@ __device__ void join_tile(const AttnArgs& a, const Walk& w, int cf, int cl, int 
     join_sums<T, NT, RT, kByRow ? 2 : 4, kByRow ? 8 : 2, kByRow>(a, first, n, rows, tid, place);
 }
 
+// A tile, as its join needs it: the sequence's first row, the cache head, the tile's number in the sequence.
+struct TileOf {
+  int row0, h, r;
+};
+
+__device__ __forceinline__ int tile_rows(const AttnArgs& a, const Walk& w, int RT) {
+  return min(RT, w.q.n * a.group - w.r * RT);
+}
+
+// Loads of parts: from L2 (another block wrote them), and issued where they stand, so that several are in
+// flight (as ordinary loads under a condition each was waited for: 20 parts took 58 us).
+__device__ __forceinline__ float load_part(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_part4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+// join_tile for trees of drafts, whose tiles are cut into many parts of many rows: the rows' maxima and
+// totals are found by all threads at once (a warp a row took 33K clocks for 256 rows of 20 parts, three
+// dependent loads a row), and the factors are made where they are used.  Rows [begin, end) of the tile;
+// stats: [2][RT] floats of shared memory.  stage: kEach kParts NT vectors of shared memory, through which
+// each thread fetches its own (as registers the compiler keeps half as many in flight), or null.
+template <typename T, int NT, int RT, int kEach, int kParts, bool kByRow, bool kStage>
+__device__ void join_tree(const AttnArgs& a, const TileOf& w, int cf, int cl, int begin, int end, int tid, uint32_t bar,
+                          float* stats, float4* stage) {
+  const int rows = end - begin, n = cl - cf + 1;
+  const int64_t slot = RT * (a.D + 2);
+  const float* const first = part_slot<RT>(a, 2 * cf + 1);       // then the slots 2c of the later blocks
+  auto part = [&](int c) { return first + (c == 0 ? 0 : (2 * c - 1) * slot); };
+  auto place = [&](int row) {
+    const int rr = w.r * RT + row;
+    return (static_cast<int64_t>(w.row0) + rr / a.group) * a.heads + w.h * a.group + rr % a.group;
+  };
+  int log = 0;                    // threads of a row: at most a warp's
+  while (log < 5 && (rows << (log + 1)) <= NT) ++log;
+  const int each = 1 << log, sub = tid & (each - 1);
+  constexpr int kAhead = 4;
+  for (int row0 = 0; row0 < rows; row0 += NT >> log) {
+    const int row = row0 + (tid >> log);
+    float top = -INFINITY, total = 0.f;
+    for (int c0 = sub; c0 < n; c0 += each * kAhead) {
+      float m[kAhead], l[kAhead], high = top;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float* p = part(min(c0 + i * each, n - 1)) + RT * a.D + begin + min(row, rows - 1);
+        m[i] = load_part(p);
+        l[i] = load_part(p + RT);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (c0 + i * each >= n) m[i] = -INFINITY, l[i] = 0.f;
+        high = fmaxf(high, m[i]);
+      }
+      const float base = high == -INFINITY ? 0.f : high;
+      total *= exp2f(top - base);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) total = fmaf(exp2f(m[i] - base), l[i], total);
+      top = high;
+    }
+    for (int o = 1; o < each; o <<= 1) {
+      const float t2 = __shfl_xor_sync(~0u, top, o), l2 = __shfl_xor_sync(~0u, total, o);
+      const float high = fmaxf(top, t2), base = high == -INFINITY ? 0.f : high;
+      total = exp2f(top - base) * total + exp2f(t2 - base) * l2;
+      top = high;
+    }
+    if (sub == 0 && row < rows) {
+      stats[row] = top == -INFINITY ? 0.f : top;
+      stats[RT + row] = total == 0.f ? 0.f : 1.f / total;
+      if (a.lse) a.lse[place(begin + row)] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+    }
+  }
+  ptx::named_barrier(bar, NT);
+  // items of kEach neighbouring 4-element vectors of a row
+  const int groups = a.D / (4 * kEach), items = rows * groups;
+  for (int x = tid; x < items; x += NT) {
+    const int row = kByRow ? x / groups : x % rows, g = kByRow ? x % groups : x / rows;
+    const float base = stats[row], inv = stats[RT + row];
+    float4 o[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < n; c0 += kParts) {
+      float f[kParts];
+      float4 v[kStage ? 1 : kParts][kEach];
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) {
+        if (kStage && c0 + c >= n) break;
+        const float* s = part(min(c0 + c, n - 1));
+        f[c] = load_part(s + RT * a.D + begin + row);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const float* p = s + (kByRow ? (begin + row) * a.D + (g * kEach + i) * 4 : ((g * kEach + i) * RT + begin + row) * 4);
+          if constexpr (kStage)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(stage + (c * kEach + i) * NT + tid)),
+                         "l"(p)
+                         : "memory");
+          else
+            v[c][i] = load_part4(p);
+        }
+      }
+      if constexpr (kStage) asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) {
+        if (kStage && c0 + c >= n) break;
+        const float e = c0 + c < n ? exp2f(f[c] - base) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const float4 x = kStage ? stage[(c * kEach + i) * NT + tid] : v[kStage ? 0 : c][i];
+          o[i].x = fmaf(e, x.x, o[i].x);
+          o[i].y = fmaf(e, x.y, o[i].y);
+          o[i].z = fmaf(e, x.z, o[i].z);
+          o[i].w = fmaf(e, x.w, o[i].w);
+        }
+      }
+    }
+    T* to = static_cast<T*>(a.out) + place(begin + row) * a.D + g * kEach * 4;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      store4(to + i * 4, make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv));
+  }
+  ptx::named_barrier(bar, NT);     // stats may be written again
+}
+
 }  // namespace at
 }  // namespace engram

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
   float* Ps = Vs + kKT * DP;
   __shared__ Range range;
   __shared__ int flag;
+  __shared__ float stats[kTree ? 2 * RT : 1];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -273,7 +274,13 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
           }
         }
         const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
-        if (arrive_last<kNT>(a, cf, cl, &flag, tid, 1)) join_tile<T, kNT, RT, true>(a, w, cf, cl, tid, 1);
+        if (arrive_last<kNT>(a, cf, cl, &flag, tid, 1)) {
+          if constexpr (kTree)
+            join_tree<T, kNT, RT, 2, 4, true, false>(a, {w.q.row0, w.h, w.r}, cf, cl, 0, tile_rows(a, w, RT), tid, 1,
+                                                     stats, nullptr);
+          else
+            join_tile<T, kNT, RT, true>(a, w, cf, cl, tid, 1);
+        }
       }
     }
     u = piece.next;

@@ -72,6 +72,7 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int flag;
+  int split[kSplitWords];   // of a tree: the tile that the block begins and does not end (first word -1: none)
   Range range;
   // on a line of their own: a warp's 32 values in one access (4096-token chunk 313 us where they lay across two, 309)
   alignas(128) float top[2][2][128];   // [tile][half][row]: maxima of a step
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kNT, 1)
     }
     ptx::mbar_init(&sh.drain, 1);
     sh.abort = 0;
+    sh.split[0] = -1;
     ptx::fence_mbar_init();
     ptx::tma_prefetch_desc(&map_k);
     ptx::tma_prefetch_desc(&map_v);
@@ -366,8 +368,18 @@ __global__ void __launch_bounds__(kNT, 1)
           }
           if (!whole) {
             const int cf = first_block<kCost>(range, at), cl = last_block<kCost>(range, at, w);
-            if (arrive_last<kSoft>(a, cf, cl, &sh.flag, tid, 1))
+            if (kTree && a.splits) {    // joined by the kernel after this one
+              if (tid == 0 && ua == 0) {
+                sh.split[0] = cl;
+                sh.split[1] = cf;
+                sh.split[2] = w.q.row0;
+                sh.split[3] = w.h;
+                sh.split[4] = w.r;
+                sh.split[5] = tile_rows(a, w, kRT);
+              }
+            } else if (arrive_last<kSoft>(a, cf, cl, &sh.flag, tid, 1)) {
               join_tile<__nv_bfloat16, kSoft, kRT, false>(a, w, cf, cl, tid, 1);
+            }
           }
         }
         u = piece.next;
@@ -503,16 +515,69 @@ __global__ void __launch_bounds__(kNT, 1)
   }
 
   __syncthreads();
+  if (kTree && a.splits && tid < kSplitWords) a.splits[blockIdx.x * kSplitWords + tid] = sh.split[tid];
   if (warp == 17) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
 }
 
+// The joins of a tree's tiles, over all SMs: a tile of 256 rows in 19 parts is 1.3 MB, which the block that
+// arrives last reads in 20 us, while the others have ended.  Each block of the kernel before has left what
+// it began and did not end; the blocks here share those tiles' rows.
+constexpr int kJoinNT = 256;
+constexpr int kJoinRows = 32;
+constexpr int kJoinSmem = 2 * 8 * kJoinNT * 16;
+
 template <int D>
-cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
+__global__ void __launch_bounds__(kJoinNT) attn_join_kernel(const __grid_constant__ AttnArgs a, int blocks) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int tiles[kJoinNT], before[kJoinNT / 32];
+  __shared__ float stats[2 * kRT];
+  const int tid = threadIdx.x;
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  // tasks: kJoinRows rows of a tile (a tile has up to kRT / kJoinRows)
+  constexpr int kTasks = kRT / kJoinRows;
+  for (int base = 0; base < blocks; base += kJoinNT) {
+    const int c = base + tid;
+    const bool split = c < blocks && ptx::ld_after_wait(a.splits + c * kSplitWords) >= 0;
+    // in the order of the blocks: the same list in every block here
+    const uint32_t all = __ballot_sync(~0u, split);
+    if ((tid & 31) == 0) before[tid >> 5] = __popc(all);
+    __syncthreads();
+    int at = __popc(all & ((1u << (tid & 31)) - 1)), total = 0;
+    for (int i = 0; i < kJoinNT / 32; ++i) {
+      at += i < tid >> 5 ? before[i] : 0;
+      total += before[i];
+    }
+    if (split) tiles[at] = c;
+    __syncthreads();
+    for (int task = blockIdx.x; task < total * kTasks; task += gridDim.x) {
+      const int32_t* s = a.splits + tiles[task / kTasks] * kSplitWords;
+      const int cl = ptx::ld_after_wait(s), cf = ptx::ld_after_wait(s + 1), row0 = ptx::ld_after_wait(s + 2),
+                h = ptx::ld_after_wait(s + 3), r = ptx::ld_after_wait(s + 4), rows = ptx::ld_after_wait(s + 5);
+      const int begin = task % kTasks * kJoinRows;
+      if (begin < rows)
+        join_tree<__nv_bfloat16, kJoinNT, kRT, 2, 8, false, true>(a, {row0, h, r}, cf, cl, begin,
+                                                                  min(rows, begin + kJoinRows), tid, 1, stats,
+                                                                  reinterpret_cast<float4*>(smem_raw));
+    }
+    __syncthreads();
+  }
+}
+
+template <int D>
+cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, AttnArgs a, int max_new, cudaStream_t s) {
+  // Trees of few tiles are cut into many parts: joined by a kernel of their own (2 trees of 64 tokens over 30k and
+  // 65k, 8 tiles: 51 us, in the tiles kernel 86).  With a tile for every block or more, a tile has two or three
+  // parts, and the joins run beside other tiles' steps (32 trees, 256 tiles: 159 us, with the other kernel 164).
+  const int64_t tiles = (static_cast<int64_t>(max_new) * a.group + kRT - 1) / kRT * a.seq.B * a.heads_kv;
+  if (a.causal != kSeesTree || tiles >= p->num_sms) a.splits = nullptr;
   auto* kernel = a.causal == kSeesTree ? attn_tiles_kernel<D, true> : attn_tiles_kernel<D, false>;
-  return launch_pdl(kernel, dim3(p->num_sms), dim3(kNT), Cfg<D>::kSmem, s, a, c->k128, c->v128);
+  const cudaError_t e = launch_pdl(kernel, dim3(p->num_sms), dim3(kNT), Cfg<D>::kSmem, s, a, c->k128, c->v128);
+  if (e != cudaSuccess || !a.splits) return e;
+  return launch_pdl(attn_join_kernel<D>, dim3(p->num_sms * 3), dim3(kJoinNT), kJoinSmem, s, a, p->num_sms);
 }
 
 template <int D>
@@ -521,7 +586,7 @@ cudaError_t prepare() {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  return cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmem);
 }
 
 }  // namespace
@@ -530,8 +595,8 @@ cudaError_t prepare_attention_tiles(const engram_attn_plan* p) {
   return p->cfg.head_dim == 64 ? prepare<64>() : prepare<128>();
 }
 
-cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, cudaStream_t s) {
-  return a.D == 64 ? run<64>(c->plan, c, a, s) : run<128>(c->plan, c, a, s);
+cudaError_t launch_attention_tiles(const engram_kv_cache* c, const AttnArgs& a, int max_new, cudaStream_t s) {
+  return a.D == 64 ? run<64>(c->plan, c, a, max_new, s) : run<128>(c->plan, c, a, max_new, s);
 }
 
 }  // namespace engram
