@@ -304,102 +304,129 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& total, int64_t
   return before + inc - v;
 }
 
-// One block, so that its barriers part the steps: count what each row needs,
-// find as many unused pages, hand them out, drop the counts of those replaced
-// (all rows look at the counts that the call began with).
-// first: [rows] of a row's place in the line of taken pages; taken, old: [pages].
+// What reserve keeps between its steps: [rows] a row's place in the line of written pages, [pages] what is
+// wanted and what is taken for it.
+struct Wanted {
+  int row, g, old, fresh;
+};
+
+constexpr int kFirstShared = 2048;    // rows whose places fit in shared memory
+constexpr int kLook = 8;              // pages a thread looks at together
+
+// One block, so that its barriers part the steps: put the pages that rows will write in a line (a thread a
+// row), see which of them need a page (a thread a page), find as many unused ones, hand them out and drop
+// the counts of those replaced.  All rows look at the counts that the call began with.  What bounds it is
+// the chain of loads of each step (before and after, table, count, counts of unused pages), a microsecond
+// each: 544 rows of 33 entries 8 us, where a warp a row took 39.
 __global__ void __launch_bounds__(kReserveNT)
     pool_reserve_kernel(engram_pool_t p, int page_shift, const int32_t* before, const int32_t* after, int32_t* pairs,
-                        int32_t* missing, int64_t* first, int32_t* taken, int32_t* old, uint32_t* err) {
+                        int32_t* missing, int64_t* first, Wanted* want, uint32_t* err) {
   __shared__ int64_t warp_sum[kReserveWarps];
+  __shared__ int64_t first_shared[kFirstShared];
+  __shared__ int found_in[kLook][kReserveWarps + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  // the pages [lo, hi) of row r that will be written
-  auto range = [&](int r, int& lo, int& hi, int& n0, bool tell) {
-    n0 = ptx::ld_after_wait(before + r);
-    const int n1 = ptx::ld_after_wait(after + r);
-    lo = hi = 0;
-    if (n1 <= n0) return;
-    if (n0 < 0 || n1 > static_cast<int64_t>(p.table_pages) << page_shift) {
-      if (tell) atomicOr(err, kErrIndexRange);
-      return;
+  int64_t* const at_row = p.rows <= kFirstShared ? first_shared : first;
+  int64_t line = 0;
+  for (int r0 = 0; r0 < p.rows; r0 += kReserveNT) {
+    const int r = r0 + tid;
+    int n = 0;
+    if (r < p.rows) {
+      const int n0 = ptx::ld_after_wait(before + r), n1 = ptx::ld_after_wait(after + r);
+      if (n1 > n0) {
+        if (n0 < 0 || n1 > static_cast<int64_t>(p.table_pages) << page_shift)
+          atomicOr(err, kErrIndexRange);
+        else
+          n = ((n1 - 1) >> page_shift) + 1 - (n0 >> page_shift);
+      }
+      pairs[2 * static_cast<int64_t>(r)] = pairs[2 * static_cast<int64_t>(r) + 1] = -1;
     }
-    lo = n0 >> page_shift;
-    hi = ((n1 - 1) >> page_shift) + 1;
-  };
-  // 0: the entry stays; 1: a page is taken; 2: in place of a shared one
-  auto needs = [&](int e, bool tell) {
-    if (e < 0) return 1;
-    if (e >= p.pages) {
-      if (tell) atomicOr(err, kErrIndexRange);
-      return 0;
-    }
-    return ptx::ld_after_wait(p.ref + e) > 1 ? 2 : 0;
-  };
-  for (int r = warp; r < p.rows; r += kReserveWarps) {
-    int lo, hi, n0, n = 0;
-    range(r, lo, hi, n0, lane == 0);
-    const int32_t* row = p.table + static_cast<int64_t>(r) * p.table_pages;
-    for (int g0 = lo; g0 < hi; g0 += 32) {
-      const int g = g0 + lane;
-      const bool need = g < hi && needs(ptx::ld_after_wait(row + min(g, hi - 1)), true) != 0;
-      n += __popc(__ballot_sync(~0u, need));
-    }
-    if (lane == 0) first[r] = n;
+    int64_t total;
+    const int64_t at = line + block_scan(n, total, warp_sum);
+    if (r < p.rows) at_row[r] = at;
+    line += total;
   }
   __syncthreads();
   int64_t wanted = 0;
-  for (int r0 = 0; r0 < p.rows; r0 += kReserveNT) {
-    const int r = r0 + tid;
+  for (int64_t x0 = 0; x0 < line; x0 += kReserveNT) {
+    const int64_t x = x0 + tid;
+    Wanted w{0, 0, -1, -1};
+    bool need = false;
+    if (x < line) {
+      int lo = 0, hi = p.rows - 1;            // the last row that begins at x or before it
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (at_row[mid] <= x)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      w.row = lo;
+      w.g = (ptx::ld_after_wait(before + lo) >> page_shift) + static_cast<int>(x - at_row[lo]);
+      const int e = ptx::ld_after_wait(p.table + static_cast<int64_t>(lo) * p.table_pages + w.g);
+      need = e < 0;
+      if (e >= p.pages) {
+        atomicOr(err, kErrIndexRange);
+      } else if (e >= 0 && ptx::ld_after_wait(p.ref + e) > 1) {
+        need = true;
+        w.old = e;
+      }
+    }
     int64_t total;
-    const int64_t n = r < p.rows ? first[r] : 0;
-    const int64_t at = wanted + block_scan(n, total, warp_sum);
-    if (r < p.rows) first[r] = at;
+    const int64_t at = wanted + block_scan(need, total, warp_sum);
+    if (need && at < p.pages) want[at] = w;
     wanted += total;
   }
   int64_t found = 0;
-  for (int64_t g0 = 0; g0 < p.pages && found < wanted; g0 += kReserveNT) {
-    const int64_t g = g0 + tid;
-    int64_t total;
-    const bool unused = g < p.pages && ptx::ld_after_wait(p.ref + g) <= 0;
-    const int64_t at = found + block_scan(unused, total, warp_sum);
-    if (unused) taken[at] = static_cast<int32_t>(g);
-    found += total;
+  for (int64_t g0 = 0; g0 < p.pages && found < wanted; g0 += kReserveNT * kLook) {
+    int ref[kLook];
+    uint32_t unused[kLook];
+#pragma unroll
+    for (int k = 0; k < kLook; ++k) {
+      const int64_t g = g0 + k * kReserveNT + tid;
+      ref[k] = g < p.pages ? ptx::ld_after_wait(p.ref + g) : 1;
+    }
+    __syncthreads();                          // the numbers before have been read
+#pragma unroll
+    for (int k = 0; k < kLook; ++k) {
+      unused[k] = __ballot_sync(~0u, ref[k] <= 0);
+      if (lane == 0) found_in[k][warp] = __popc(unused[k]);
+    }
+    __syncthreads();
+    if (warp < kLook) {
+      const int n = found_in[warp][lane];
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += t;
+      }
+      found_in[warp][lane] = inc - n;
+      if (lane == 31) found_in[warp][kReserveWarps] = inc;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kLook; ++k) {
+      const int64_t at = found + found_in[k][warp] + __popc(unused[k] & ((1u << lane) - 1));
+      if (ref[k] <= 0 && at < wanted) want[at].fresh = static_cast<int32_t>(g0 + k * kReserveNT + tid);   // at < pages
+      found += found_in[k][kReserveWarps];
+    }
   }
   const bool enough = found >= wanted;
   if (tid == 0) *missing = enough ? 0 : static_cast<int32_t>(min(wanted - found, static_cast<int64_t>(INT32_MAX)));
   __syncthreads();
-  for (int r = warp; r < p.rows; r += kReserveWarps) {
-    int lo, hi, n0;
-    range(r, lo, hi, n0, false);
-    int32_t* row = p.table + static_cast<int64_t>(r) * p.table_pages;
-    int from = -1, to = -1;
-    int64_t at = enough ? first[r] : 0;
-    for (int g0 = enough ? lo : hi; g0 < hi; g0 += 32) {
-      const int g = g0 + lane;
-      const int e = ptx::ld_after_wait(row + min(g, hi - 1));
-      const int need = g < hi ? needs(e, false) : 0;
-      const uint32_t some = __ballot_sync(~0u, need != 0);
-      if (need) {
-        const int64_t x = at + __popc(some & ((1u << lane) - 1));
-        const int fresh = taken[x];
-        old[x] = need == 2 ? e : -1;
-        row[g] = fresh;
-        if (need == 2 && (static_cast<int64_t>(g) << page_shift) < n0) from = e, to = fresh;   // lane 0 of the first turn
-      }
-      at += __popc(some);
-    }
-    if (lane == 0) {
-      pairs[2 * static_cast<int64_t>(r)] = from;
-      pairs[2 * static_cast<int64_t>(r) + 1] = to;
-    }
-  }
-  __syncthreads();
   if (!enough) return;
   for (int64_t x = tid; x < wanted; x += kReserveNT) {
-    atomicAdd(p.ref + taken[x], 1);
-    if (old[x] >= 0) atomicSub(p.ref + old[x], 1);
+    const Wanted w = want[x];
+    p.table[static_cast<int64_t>(w.row) * p.table_pages + w.g] = w.fresh;
+    atomicAdd(p.ref + w.fresh, 1);
+    if (w.old < 0) continue;
+    atomicSub(p.ref + w.old, 1);
+    if (static_cast<int64_t>(w.g) << page_shift < ptx::ld_after_wait(before + w.row)) {      // the row's first written page
+      pairs[2 * static_cast<int64_t>(w.row)] = w.old;
+      pairs[2 * static_cast<int64_t>(w.row) + 1] = w.fresh;
+    }
   }
 }
 
@@ -455,16 +482,16 @@ cudaError_t launch_pool_fork(const engram_attn_plan* plan, const engram_pool_t& 
 }
 
 size_t pool_workspace_bytes(const engram_pool_t& p) {
-  return static_cast<size_t>(p.rows) * 8 + static_cast<size_t>(p.pages) * 8;
+  return (static_cast<size_t>(p.rows) * 8 + 15) / 16 * 16 + static_cast<size_t>(p.pages) * sizeof(Wanted);
 }
 
 cudaError_t launch_pool_reserve(const engram_attn_plan* plan, const engram_pool_t& p, const int32_t* before,
                                 const int32_t* after, int32_t* pairs, int32_t* missing, void* workspace,
                                 cudaStream_t s) {
   int64_t* first = static_cast<int64_t*>(workspace);
-  int32_t* taken = reinterpret_cast<int32_t*>(first + p.rows);
+  Wanted* want = reinterpret_cast<Wanted*>(first + (p.rows + 1) / 2 * 2);
   return launch_pdl(pool_reserve_kernel, dim3(1), dim3(kReserveNT), 0, s, p, plan->page_shift, before, after, pairs,
-                    missing, first, taken, taken + p.pages, plan->err);
+                    missing, first, want, plan->err);
 }
 
 }  // namespace engram
