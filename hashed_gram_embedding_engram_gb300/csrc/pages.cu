@@ -153,8 +153,19 @@ __global__ void __launch_bounds__(kMoveNT) compact_short_kernel(const __grid_con
   }
 }
 
-// Longer ones: a block has `strip` vectors of every row of one head's keys or values.
-__global__ void __launch_bounds__(kMoveNT, 4) compact_kernel(const __grid_constant__ MoveArgs a, int strip, int strips) {
+// Longer ones: a block has `strip` vectors of every row of one head's keys or values.  Where up to kAhead rows
+// come from is looked up for all of them together (looked up group by group, each group waited for its path
+// and its page ids before its rows' loads went out), and kDepth groups of rows are on their way through shared
+// memory: what bounds the rows of few sequences is how many loads are in flight.  Four prompts of 9k to 16k
+// tokens to 45 % (187 MB): see kDepth.
+constexpr int kAhead = 8192;
+constexpr int kDepth = 4;           // 4 x 16 KB a block, two blocks an SM
+constexpr int kGroupBytes = kMoveRows * kMoveNT * 16;
+
+__global__ void __launch_bounds__(kMoveNT, 2) compact_kernel(const __grid_constant__ MoveArgs a, int strip, int strips) {
+  extern __shared__ uint4 ring[];                       // [kDepth][kMoveRows][kMoveNT], then from
+  int* const from = reinterpret_cast<int*>(ring + kDepth * kMoveRows * kMoveNT);   // rows of the cache (31 bits), -1: none
+  __shared__ int to_page[kAhead / 8 + 1];               // the first row of a page's head 0, -1: no page
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int tid = threadIdx.x;
@@ -164,48 +175,64 @@ __global__ void __launch_bounds__(kMoveNT, 4) compact_kernel(const __grid_consta
   int n;
   if (!move_begin(a, b, tid == 0 && col == 0, q, n)) return;
   uint4* cache = part < a.heads_kv ? a.k : a.v;
-  const int64_t head = static_cast<int64_t>(part % a.heads_kv) << a.s.page_shift;
+  const int shift = a.s.page_shift, page = 1 << shift, head = (part % a.heads_kv) << shift;
   const int32_t* path = a.path + static_cast<int64_t>(b) * a.width;
   const int base = q.len - q.n;
   const int lanes = kMoveNT / strip, at = tid / strip, vec = col + tid - at * strip;
   const bool live = at < lanes && vec < a.row_vecs;
   const int group = lanes * kMoveRows;
-  // the rows of a group that this thread moves: what they are, and where they go (null: nowhere)
-  auto load = [&](int i0, uint4 (&x)[kMoveRows], uint4* (&to)[kMoveRows]) {
-    int from[kMoveRows];
+  for (int begin = 0; begin < n; begin += kAhead) {
+    const int rows = min(n - begin, kAhead), first = base + begin;
+    __syncthreads();                                    // the rows before have been moved
+    for (int i = tid; i <= (first + rows - 1 >> shift) - (first >> shift); i += kMoveNT)
+      to_page[i] = static_cast<int>(move_row(a, b, ((first >> shift) + i) << shift));
+    constexpr int kLook = 8;
+    for (int i0 = tid; i0 < rows; i0 += kMoveNT * kLook) {
+      int x[kLook];
 #pragma unroll
-    for (int r = 0; r < kMoveRows; ++r) {
-      const int i = i0 + r * lanes + at;
-      from[r] = live && i < n ? ptx::ld_after_wait(path + i) : i;
-      if (from[r] == i) from[r] = -1;
+      for (int r = 0; r < kLook; ++r) {
+        const int i = i0 + r * kMoveNT;
+        x[r] = i < rows ? ptx::ld_after_wait(path + begin + i) : begin + i;
+      }
+#pragma unroll
+      for (int r = 0; r < kLook; ++r) {
+        const int i = i0 + r * kMoveNT;
+        if (i < rows) from[i] = x[r] == begin + i ? -1 : static_cast<int>(move_row(a, b, base + x[r]));
+      }
     }
-    int64_t f[kMoveRows], t[kMoveRows];
+    __syncthreads();
+    // row i's place, or null
+    auto place = [&](int i) -> uint4* {
+      const int p = to_page[(first + i >> shift) - (first >> shift)];
+      if (!live || i >= rows || from[i] < 0 || p < 0) return nullptr;
+      return cache + static_cast<int64_t>(p + (first + i & page - 1) + head) * a.row_vecs + vec;
+    };
+    auto load = [&](int g) {
+      uint4* slot = ring + g % kDepth * (kMoveRows * kMoveNT) + tid;
 #pragma unroll
-    for (int r = 0; r < kMoveRows; ++r) {
-      f[r] = from[r] < 0 ? -1 : move_row(a, b, base + from[r]);
-      t[r] = from[r] < 0 ? -1 : move_row(a, b, base + i0 + r * lanes + at);
-    }
+      for (int r = 0; r < kMoveRows; ++r) {
+        const int i = g * group + r * lanes + at;
+        if (place(min(i, rows - 1)) && i < rows) {
+          const uint4* p = cache + static_cast<int64_t>(from[i] + head) * a.row_vecs + vec;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(slot + r * kMoveNT)), "l"(p) : "memory");
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const int groups = (rows + group - 1) / group;
 #pragma unroll
-    for (int r = 0; r < kMoveRows; ++r) {
-      to[r] = nullptr;
-      if (f[r] < 0 || t[r] < 0) continue;
-      to[r] = cache + (t[r] + head) * a.row_vecs + vec;
-      x[r] = ptx::ld_after_wait(cache + (f[r] + head) * a.row_vecs + vec);
-    }
-  };
-  uint4 x[2][kMoveRows];
-  uint4* to[2][kMoveRows];
-  load(0, x[0], to[0]);
-  for (int i0 = 0; i0 < n; i0 += 2 * group) {
+    for (int g = 0; g < kDepth - 1; ++g) load(g);       // past the last: empty
+    for (int g = 0; g < groups; ++g) {
+      load(g + kDepth - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      __syncthreads();                                  // everyone's rows of this group have been read
+      const uint4* slot = ring + g % kDepth * (kMoveRows * kMoveNT) + tid;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at0 = i0 + h * group;
-      if (at0 >= n) break;
-      load(at0 + group, x[h ^ 1], to[h ^ 1]);
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < kMoveRows; ++r)
-        if (to[h][r]) *to[h][r] = x[h][r];
+      for (int r = 0; r < kMoveRows; ++r) {
+        const int i = g * group + r * lanes + at;
+        if (i >= rows) continue;
+        if (uint4* to = place(i)) *to = slot[r * kMoveNT];
+      }
     }
   }
 }
@@ -459,13 +486,17 @@ cudaError_t launch_compact(const engram_kv_cache* c, const SeqArgs& seq, const i
     while (splits < g.heads_kv && static_cast<int64_t>(seq.B) * splits * 2 <= sms) splits *= 2;
     return launch_pdl(compact_short_kernel, dim3(static_cast<unsigned>(seq.B) * splits), dim3(kMoveNT), 0, s, a, splits);
   }
-  // columns apart, 32 bytes at least (a sector), until there are four blocks an SM
+  // columns apart, 64 bytes at least (half a line), until there are two blocks an SM or nearly
   int strip = vecs, strips = 1;
-  while (strip > 2 && static_cast<int64_t>(seq.B) * 2 * g.heads_kv * strips < 4 * sms) {
+  while (strip > 4 && static_cast<int64_t>(seq.B) * 2 * g.heads_kv * strips < sms * 3 / 2) {
     strip = (strip + 1) / 2 + ((strip + 1) / 2 & 1);
     strips = (vecs + strip - 1) / strip;
   }
-  return launch_pdl(compact_kernel, dim3(static_cast<unsigned>(seq.B) * 2 * g.heads_kv * strips), dim3(kMoveNT), 0, s, a,
+  const int smem = kDepth * kGroupBytes + (width < kAhead ? width : kAhead) * 4;
+  const cudaError_t e = cudaFuncSetAttribute(compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kDepth * kGroupBytes + kAhead * 4);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(compact_kernel, dim3(static_cast<unsigned>(seq.B) * 2 * g.heads_kv * strips), dim3(kMoveNT), smem, s, a,
                     strip, strips);
 }
 
