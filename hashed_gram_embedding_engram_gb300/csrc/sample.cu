@@ -50,7 +50,11 @@ constexpr int kFew = 256;                    // of these, as many as are compare
 constexpr int kBins = 256;                   // of a in [0, 32)
 constexpr float kBinScale = 8.f;
 constexpr int kCopies = 16;                  // of the histogram, two lanes each
-constexpr int kDigit = 1024;                 // values of a digit of a place
+constexpr int kDigitBits = 9;                // of a digit of a place: a value for each thread
+constexpr int kLocal = 8192;                 // tokens of a block that top-p may keep
+constexpr int kBand = 1024;                  // of these, in the band
+constexpr int kSpan = 64;                    // neighbours whose weights are summed for the draw,
+constexpr int kSpans = 1024;                 // and how many such there are
 
 struct Args {
   const void* logits;
@@ -129,6 +133,7 @@ struct Shared {
   uint32_t own, base;               // tokens that this block has for the list, and where they go
   uint32_t listed;                  // tokens sent to this block's list
   uint32_t number[kMaxCluster];     // every block's
+  uint32_t in_band;
   uint64_t left;
   int found;                        // part that holds the goal
   uint64_t goal, before;
@@ -144,11 +149,20 @@ struct Shared {
       uint32_t mine[kBins][kCopies];           // histogram of weights over a
       uint32_t all[kMaxCluster][kBins];        // every block's
     } bins;
-    struct {
-      uint32_t count[kDigit], lo[kDigit], hi[kDigit];
-    } places;
-    uint64_t weights[kFew];
     uint64_t own[kList];
+    struct {
+      uint16_t at[kLocal];                     // the block's tokens that top-p may keep: where they lie in it
+      union {
+        uint64_t band[kBand];                  // places of those in the band
+        struct {
+          uint32_t lo[kSpans], hi[kSpans];     // weights of kSpan neighbours each
+        } spans;
+        struct {
+          uint32_t count[kNT], lo[kNT], hi[kNT];    // histogram of a digit of the list's places
+        } places;
+        uint64_t weights[kFew];
+      };
+    } local;
   } u;
 };
 
@@ -435,7 +449,7 @@ __device__ float bound_of(float v, int j, float low, float top) {
 // step(x, in): marks those of a vector's logits.
 template <typename R, typename Step>
 __device__ int send_list(const R& row, int cluster, int rank, Shared& sh, bool some, Step& step) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   if (__any_sync(~0u, some)) {
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
@@ -454,7 +468,6 @@ __device__ int send_list(const R& row, int cluster, int rank, Shared& sh, bool s
       }
     }
   }
-  step.send(rank * kWarps + warp, cluster, lane, sh);
   __syncthreads();
   const uint32_t mine = sh.own;
   if (tid == 0) sh.base = mine ? atom_cluster_add(ptx::mapa_shared(ptx::smem_u32(&sh.listed), 0), mine) : 0;
@@ -507,40 +520,32 @@ __device__ uint64_t pick(const uint64_t (&key)[kEach], const uint64_t (&w)[kEach
     if (shift < 64) prefix = all >> shift;
   }
   while (shift > 0) {
-    const int low = max(shift - 10, 0), size = 1 << (shift - low);
-    for (int i = tid; i < kDigit; i += kNT) sh.u.places.count[i] = sh.u.places.lo[i] = sh.u.places.hi[i] = 0;
+    const int low = max(shift - kDigitBits, 0), size = 1 << (shift - low);
+    static_assert(1 << kDigitBits == kNT, "");
+    sh.u.local.places.count[tid] = sh.u.local.places.lo[tid] = sh.u.local.places.hi[tid] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       if (!in[i] || (shift < 64 && key[i] >> shift != prefix)) continue;
       const int d = static_cast<int>(key[i] >> low) & (size - 1);
-      atomicAdd(&sh.u.places.count[d], 1u);
-      const uint32_t lo = static_cast<uint32_t>(w[i]), was = atomicAdd(&sh.u.places.lo[d], lo);
+      atomicAdd(&sh.u.local.places.count[d], 1u);
+      const uint32_t lo = static_cast<uint32_t>(w[i]), was = atomicAdd(&sh.u.local.places.lo[d], lo);
       const uint32_t hi = static_cast<uint32_t>(w[i] >> 32) + (was + lo < was);
-      if (hi) atomicAdd(&sh.u.places.hi[d], hi);
+      if (hi) atomicAdd(&sh.u.local.places.hi[d], hi);
     }
     __syncthreads();
-    // two digits a thread, from the largest down
-    uint64_t c[2], v[2], total;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int d = kDigit - 1 - (2 * tid + i);
-      c[i] = sh.u.places.count[d];
-      v[i] = static_cast<uint64_t>(sh.u.places.hi[d]) << 32 | sh.u.places.lo[d];
-    }
-    uint64_t v_at = block_scan(v[0] + v[1], total, sh);
-    uint64_t c_at = kCount ? block_scan(c[0] + c[1], total, sh) : 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint64_t at = kCount ? c_at : v_at, size_here = kCount ? c[i] : v[i];
-      if (need > at && need <= at + size_here) {          // one thread, once
-        sh.digit = kDigit - 1 - (2 * tid + i);
-        sh.left = need - at;
-        sh.goal = v_at;
-        sh.before = c[i];
-      }
-      v_at += v[i];
-      c_at += c[i];
+    // a digit a thread, from the largest down
+    const int d = kNT - 1 - tid;
+    const uint64_t c = sh.u.local.places.count[d];
+    const uint64_t v = static_cast<uint64_t>(sh.u.local.places.hi[d]) << 32 | sh.u.local.places.lo[d];
+    uint64_t total;
+    const uint64_t v_at = block_scan(v, total, sh), c_at = kCount ? block_scan(c, total, sh) : 0;
+    const uint64_t at = kCount ? c_at : v_at, here = kCount ? c : v;
+    if (need > at && need <= at + here) {                 // one thread
+      sh.digit = d;
+      sh.left = need - at;
+      sh.goal = v_at;
+      sh.before = c;
     }
     __syncthreads();
     prefix = (shift < 64 ? prefix << (shift - low) : 0) | sh.digit;
@@ -573,13 +578,13 @@ __device__ uint64_t list_border(int n, int most, uint64_t above, const Scale& s,
     const uint64_t mine = e < n ? sh.list[e] : 0;
     const uint64_t w = e < n ? weight_of(s, logit_at(mine)) : 0;
     const bool first = (tid & (each - 1)) == 0;
-    if (first && e < kFew) sh.u.weights[e] = w;
+    if (first && e < kFew) sh.u.local.weights[e] = w;
     __syncthreads();
     uint64_t before = 0;
     int rank = 0;
     for (int j = tid & (each - 1); j < n; j += each) {
       const bool earlier = sh.list[j] > mine;
-      before += earlier ? sh.u.weights[j] : 0;
+      before += earlier ? sh.u.local.weights[j] : 0;
       rank += earlier;
     }
     for (int o = 1; o < each; o <<= 1) {
@@ -632,41 +637,6 @@ struct AboveBound {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) in[i] = x[i] >= bound && x[i] > -INFINITY;
   }
-  __device__ __forceinline__ void send(int, int, int, Shared&) {}
-};
-
-// Those with a in [lo, hi); and the weights above, of each warp.
-struct InBand {
-  Scale s;
-  float lo, hi;
-  uint64_t least;
-  uint64_t sum = 0, kept = 0;
-  template <int VEC>
-  __device__ __forceinline__ void operator()(const float (&x)[VEC], bool (&in)[VEC]) {
-    float2 a[VEC / 2];
-    const float nearest = exponents(s, x, a);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float e = i & 1 ? a[i / 2].y : a[i / 2].x;
-      in[i] = e >= lo && e < hi;
-    }
-    if (nearest >= lo) return;
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
-      const Pair y = powers(a[i]);
-      const uint64_t w0 = a[i].x < lo ? whole(y.p.x, y.k.x) : 0, w1 = a[i].y < lo ? whole(y.p.y, y.k.y) : 0;
-      sum += w0 + w1;
-      kept += (w0 >= least ? w0 : 0) + (w1 >= least ? w1 : 0);
-    }
-  }
-  __device__ __forceinline__ void send(int part, int cluster, int lane, Shared& sh) {
-    sum = warp_sum(sum);
-    kept = warp_sum(kept);
-    if (lane < cluster) {
-      st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
-      st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.kept[part]), lane), kept);
-    }
-  }
 };
 
 // The warp whose piece holds the goal finds the index.  keep(x, j, w): the token's weight, or 0.
@@ -712,14 +682,6 @@ struct KeepLeast {       // of at least `least`
   __device__ __forceinline__ void operator()(const float (&)[VEC], int, uint64_t (&w)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) w[i] = w[i] >= least ? w[i] : 0;
-  }
-};
-struct KeepPlaces {      // and not after the border
-  uint64_t least, border;
-  template <int VEC>
-  __device__ __forceinline__ void operator()(const float (&x)[VEC], int j, uint64_t (&w)[VEC]) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] = w[i] >= least && place_of(x[i], j + i) >= border ? w[i] : 0;
   }
 };
 struct KeepTies {        // above the border, and the first ties at it
@@ -815,21 +777,26 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
 
   // the row, once, and its largest logit
   float top = -INFINITY;
-  constexpr int kInFlight = 4;
-  for (int q0 = row.v0; q0 < row.v1; q0 += 32 * kInFlight) {
-    uint4 v[kInFlight];
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i) {
-      const int q = q0 + i * 32 + lane;
-      v[i] = make_uint4(Elem<T>::kLowest, Elem<T>::kLowest, Elem<T>::kLowest, Elem<T>::kLowest);
-      if (q < row.v1) v[i] = row.fetch(q);
+  if constexpr (kCached) {
+    for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+      const int q = q0 + lane, j = q * R::VEC - row.off;
+      uint4* to = row.kept + (q - row.v0);
+      if (q < row.v1 && j >= 0 && j + R::VEC <= a.V)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(to)), "l"(row.p + j) : "memory");
+      else
+        *to = q < row.v1 ? row.fetch(q) : make_uint4(Elem<T>::kLowest, Elem<T>::kLowest, Elem<T>::kLowest, Elem<T>::kLowest);
     }
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i) {
-      if (q0 + i * 32 >= row.v1) break;
-      if (kCached) row.kept[q0 + i * 32 + lane - row.v0] = v[i];
+    asm volatile("cp.async.wait_all;" ::: "memory");      // a lane reads what it fetched itself
+    for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
-      Elem<T>::get(v[i], x);
+      row.get(q0, lane, x);
+#pragma unroll
+      for (int e = 0; e < R::VEC; ++e) top = fmaxf(top, x[e]);
+    }
+  } else {
+    for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+      float x[R::VEC];
+      row.get(q0, lane, x);
 #pragma unroll
       for (int e = 0; e < R::VEC; ++e) top = fmaxf(top, x[e]);
     }
@@ -850,7 +817,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
   if (lane == 0) {
     sh.warp_top[warp] = top;
     sh.warp_low[warp] = low;
-    sh.listed = sh.own = 0;
+    sh.listed = sh.own = sh.in_band = 0;
   }
   __syncthreads();
   top = sh.warp_top[lane % kWarps];
@@ -938,15 +905,15 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
         const int log = n <= kNT / 4 ? 2 : 1, part_of = 1 << log, e = tid >> log;
         const bool first = (tid & (part_of - 1)) == 0;
         const uint64_t place = e < n ? sh.list[e] : 0;
-        uint64_t w = e < n && place >= border ? sh.u.weights[e] : 0;
+        uint64_t w = e < n && place >= border ? sh.u.local.weights[e] : 0;
         if (w < least) w = 0;
         __syncthreads();
-        if (first && e < kFew) sh.u.weights[e] = w;
+        if (first && e < kFew) sh.u.local.weights[e] = w;
         __syncthreads();
         const uint32_t at = static_cast<uint32_t>(place);          // larger: an earlier index
         uint64_t before = 0, total = 0;
         for (int j = tid & (part_of - 1); j < n; j += part_of) {
-          const uint64_t v = sh.u.weights[j];
+          const uint64_t v = sh.u.local.weights[j];
           total += v;
           before += static_cast<uint32_t>(sh.list[j]) > at ? v : 0;
         }
@@ -975,7 +942,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
       if (tid == 0) *token = index_at(found);
       return;
     }
-  } else if (kCached && !by_k) {     // (a piece that fits has too few tokens for a bin to pass 32 bits)
+  } else if (kCached && !by_k && chunk * R::VEC <= 65536) {
     // weights over a: each as 14 to 15 bits of the size that its bin has, two lanes to a copy
     for (int i = tid; i < kBins * kCopies; i += kNT) (&sh.u.bins.mine[0][0])[i] = 0;
     __syncthreads();
@@ -1046,37 +1013,141 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
     if (tid < kBins && after >= goal && before < goal) sh.hi = tid;
     __syncthreads();
     if (sh.hi < kBins) {
+      // the block's tokens up to the band's end, and the weights of those above it
       const float lo = static_cast<float>(sh.lo) * (1.f / kBinScale), hi = static_cast<float>(sh.hi + 1) * (1.f / kBinScale);
-      InBand band{scale, lo, hi, least};
-      const int n = send_list(row, a.cluster, rank, sh, true, band);
-      if (n >= 0) {
-        if (rank == 0) {
-          uint64_t above = 0;
-          for (int i = lane; i < parts; i += 32) above += sh.sums[i];
-          const uint64_t border = list_border(n, n, warp_sum(above), scale, sh, [&](uint64_t) { return goal; });
-          __syncthreads();
-          // the band's kept weights are added to those of their warps
-          for (int i = tid; i < n; i += kNT) {
-            const uint64_t place = sh.list[i];
-            const uint64_t w = place >= border ? weight_of(scale, logit_at(place)) : 0;
-            if (w >= least && w > 0)
-              atomicAdd(reinterpret_cast<unsigned long long*>(&sh.kept[(index_at(place) + row.off) / R::VEC / a.piece]), w);
-          }
-          __syncthreads();
-          if (warp == 0) {
-            find_part(parts, u, sh, [&](int i) { return sh.kept[i]; });
-            if (lane > 0 && lane < a.cluster) {
-              st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.found), lane), sh.found);
-              st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.goal), lane), sh.goal);
-              st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.before), lane), sh.before);
-              st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.border), lane), border);
-            }
-            if (lane == 0) sh.border = border;
+      const T* const mine_row = reinterpret_cast<const T*>(smem);
+      const int block_first = rank * chunk * R::VEC - row.off;      // index of the block's first element
+      __syncthreads();                                              // the bins have been read
+      for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
+        float x[R::VEC];
+        float2 e[R::VEC / 2];
+        row.get(q0, lane, x);
+        if (!__any_sync(~0u, exponents(scale, x, e) < hi)) continue;
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < R::VEC; ++i) n += (i & 1 ? e[i / 2].y : e[i / 2].x) < hi;
+        uint32_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t t = __shfl_up_sync(~0u, inc, o);
+          if (lane >= o) inc += t;
+        }
+        uint32_t at = 0;
+        if (lane == 31) at = atomicAdd(&sh.own, inc);
+        at = __shfl_sync(~0u, at, 31) + inc - n;
+        const int o = (warp * a.piece + q0 + lane - row.v0) * R::VEC;
+#pragma unroll
+        for (int i = 0; i < R::VEC; ++i) {
+          if ((i & 1 ? e[i / 2].y : e[i / 2].x) < hi) {
+            if (at < kLocal) sh.u.local.at[at] = static_cast<uint16_t>(o + i);
+            ++at;
           }
         }
+      }
+      __syncthreads();
+      const int n_local = static_cast<int>(sh.own);
+      uint64_t above = 0;
+      for (int i = tid; i < min(n_local, kLocal); i += kNT) {
+        const int o = sh.u.local.at[i];
+        const float x = static_cast<float>(mine_row[o]);
+        const float2 e = exponents(scale, x, x);
+        if (e.x < lo) {
+          const Pair y = powers(e);
+          above += whole(y.p.x, y.k.x);
+        } else {
+          const uint32_t at = atomicAdd(&sh.in_band, 1u);
+          if (at < kBand) sh.u.local.band[at] = place_of(x, block_first + o);
+        }
+      }
+      uint64_t block_above;
+      block_scan(above, block_above, sh);
+      const uint32_t n_band = sh.in_band;
+      const bool fits = n_local <= kLocal && n_band <= kBand;
+      if (tid == 0 && fits && n_band) sh.base = atom_cluster_add(ptx::mapa_shared(ptx::smem_u32(&sh.listed), 0), n_band);
+      if (tid < a.cluster) {
+        st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.number[rank]), tid), fits ? n_band : kList + 1u);
+        st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[rank]), tid), block_above);
+      }
+      __syncthreads();
+      if (fits && n_band && sh.base + n_band <= kList) {
+        const uint32_t to = ptx::mapa_shared(ptx::smem_u32(sh.list + sh.base), 0);
+        for (uint32_t i = tid; i < n_band; i += kNT) st_cluster_u64(to + 8 * i, sh.u.local.band[i]);
+      }
+      ptx::cluster_sync();
+      uint32_t n = 0;
+      uint64_t all_above = 0;
+      for (int c = 0; c < a.cluster; ++c) {
+        n += sh.number[c];
+        all_above += sh.sums[c];
+      }
+      if (n <= kList) {
+        if (rank == 0) {
+          const uint64_t border = list_border(static_cast<int>(n), static_cast<int>(n), all_above, scale, sh,
+                                                     [&](uint64_t) { return goal; });
+          if (tid < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.border), tid), border);
+        }
         ptx::cluster_sync();
-        KeepPlaces keep{least, sh.border};
-        if (sh.found == part) draw(row, scale, sh.before, sh.goal, token, keep);
+        const uint64_t border = sh.border;
+        // what is kept, summed over neighbours
+        for (int i = tid; i < kSpans; i += kNT) sh.u.local.spans.lo[i] = sh.u.local.spans.hi[i] = 0;
+        __syncthreads();
+        uint64_t kept = 0;
+        for (int i = tid; i < n_local; i += kNT) {
+          const int o = sh.u.local.at[i];
+          const float x = static_cast<float>(mine_row[o]);
+          const uint64_t w = place_of(x, block_first + o) >= border ? weight_of(scale, x) : 0;
+          if (w == 0 || w < least) continue;
+          kept += w;
+          const uint32_t low = static_cast<uint32_t>(w), was = atomicAdd(&sh.u.local.spans.lo[o / kSpan], low);
+          const uint32_t high = static_cast<uint32_t>(w >> 32) + (was + low < was);
+          if (high) atomicAdd(&sh.u.local.spans.hi[o / kSpan], high);
+        }
+        uint64_t block_kept;
+        block_scan(kept, block_kept, sh);
+        if (tid < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.kept[rank]), tid), block_kept);
+        ptx::cluster_sync();
+        if (warp == 0) find_part(a.cluster, u, sh, [&](int i) { return sh.kept[i]; });
+        __syncthreads();
+        if (sh.found != rank) return;
+        // this block has the token: the span, then the token in it
+        uint64_t w[2], upto, ignored;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w[i] = static_cast<uint64_t>(sh.u.local.spans.hi[2 * tid + i]) << 32 | sh.u.local.spans.lo[2 * tid + i];
+        upto = sh.before + block_scan(w[0] + w[1], ignored, sh);
+        const uint64_t want = sh.goal;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (want >= upto && want < upto + w[i]) {      // one thread, once
+            sh.digit = 2 * tid + i;
+            sh.before = upto;
+          }
+          upto += w[i];
+        }
+        __syncthreads();
+        if (warp != 0) return;
+        uint64_t v[kSpan / 32], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kSpan / 32; ++i) {
+          const int o = sh.digit * kSpan + lane * (kSpan / 32) + i;
+          const float x = o < chunk * R::VEC ? static_cast<float>(mine_row[o]) : -INFINITY;
+          v[i] = place_of(x, block_first + o) >= border ? weight_of(scale, x) : 0;
+          if (v[i] < least || x == -INFINITY) v[i] = 0;
+          sum += v[i];
+        }
+        uint64_t inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t t = __shfl_up_sync(~0u, inc, o);
+          if (lane >= o) inc += t;
+        }
+        uint64_t at = sh.before + inc - sum;
+#pragma unroll
+        for (int i = 0; i < kSpan / 32; ++i) {
+          if (want >= at && want < at + v[i]) *token = block_first + static_cast<int>(sh.digit) * kSpan + lane * (kSpan / 32) + i;
+          at += v[i];
+        }
         return;
       }
     }
