@@ -876,6 +876,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
 
   if (!by_k && !by_p) {
     uint64_t sum = 0;
+#pragma unroll 2
     for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
       float x[R::VEC];
       row.get(q0, lane, x);
@@ -1018,14 +1019,23 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
       const T* const mine_row = reinterpret_cast<const T*>(smem);
       const int block_first = rank * chunk * R::VEC - row.off;      // index of the block's first element
       __syncthreads();                                              // the bins have been read
-      for (int q0 = row.v0; q0 < row.v1; q0 += 32) {
-        float x[R::VEC];
-        float2 e[R::VEC / 2];
-        row.get(q0, lane, x);
-        if (!__any_sync(~0u, exponents(scale, x, e) < hi)) continue;
-        uint32_t n = 0;
+      // eight steps together: a bit for each of a lane's tokens, one place in the list for all
+      constexpr int kSteps = 64 / R::VEC < 8 ? 64 / R::VEC : 8;
+      for (int q0 = row.v0; q0 < row.v1; q0 += 32 * kSteps) {
+        uint64_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < R::VEC; ++i) n += (i & 1 ? e[i / 2].y : e[i / 2].x) < hi;
+        for (int k = 0; k < kSteps; ++k) {
+          if (q0 + 32 * k >= row.v1) break;
+          float x[R::VEC];
+          float2 e[R::VEC / 2];
+          row.get(q0 + 32 * k, lane, x);
+          if (exponents(scale, x, e) >= hi) continue;
+          uint32_t in = 0;
+#pragma unroll
+          for (int i = 0; i < R::VEC; ++i) in |= ((i & 1 ? e[i / 2].y : e[i / 2].x) < hi ? 1u : 0u) << i;
+          bits |= static_cast<uint64_t>(in) << (k * R::VEC);
+        }
+        const uint32_t n = __popcll(bits);
         uint32_t inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1033,15 +1043,12 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
           if (lane >= o) inc += t;
         }
         uint32_t at = 0;
-        if (lane == 31) at = atomicAdd(&sh.own, inc);
+        if (lane == 31 && inc) at = atomicAdd(&sh.own, inc);
         at = __shfl_sync(~0u, at, 31) + inc - n;
         const int o = (warp * a.piece + q0 + lane - row.v0) * R::VEC;
-#pragma unroll
-        for (int i = 0; i < R::VEC; ++i) {
-          if ((i & 1 ? e[i / 2].y : e[i / 2].x) < hi) {
-            if (at < kLocal) sh.u.local.at[at] = static_cast<uint16_t>(o + i);
-            ++at;
-          }
+        for (; bits; bits &= bits - 1, ++at) {
+          const int k = __ffsll(static_cast<long long>(bits)) - 1;
+          if (at < kLocal) sh.u.local.at[at] = static_cast<uint16_t>(o + k / R::VEC * (32 * R::VEC) + k % R::VEC);
         }
       }
       __syncthreads();
