@@ -52,6 +52,17 @@ def test_large_vocabularies_and_settings_of_each_row(V, dtype):
           top_p=torch.tensor([1.0, 0.9, 0.5, 0.99, 1.0, 1.0]).cuda(), min_p=(torch.rand(R, generator=g) * 0.01).cuda())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("settings", [dict(temperature=3.0, top_p=0.5), dict(temperature=3.0, top_p=0.97),
+                                      dict(temperature=30.0, top_p=0.8), dict(temperature=2.0, top_p=1 - 2.0 ** -20),
+                                      dict(top_k=1100), dict(top_k=5000, top_p=0.7), dict(temperature=0.2, top_p=0.9999)],
+                         ids=[str(i) for i in range(7)])
+def test_more_tokens_than_a_blocks_lists_hold(settings, dtype):
+    """Lists that just fit and that do not: flat distributions, large top_k, borders in the far tail."""
+    check(*normal(3, 50001, 12, dtype=dtype), **settings)
+    check(*normal(2, 129280, 13, dtype=dtype), min_p=1e-4, **settings)
+
+
 @pytest.mark.parametrize("R", [1, 19, 20, 37, 38, 39, 75, 77, 150, 155, 400])
 def test_batches_around_the_sizes_at_which_rows_get_fewer_blocks(R):
     logits, u = normal(R, 9000, R)

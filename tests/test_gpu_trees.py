@@ -129,6 +129,20 @@ def test_layout_and_attention_match_float64(shape, dtype):
     c.check_tree(*c.attend())
 
 
+@pytest.mark.parametrize("new,window", [(9, 0), (40, 0), (40, 90)])
+def test_a_tile_for_every_block_and_more(new, window):
+    """160 and more tiles, which the tiles kernel joins itself (fewer have a kernel of their own for that)."""
+    r = np.random.RandomState(new)
+    n = r.randint(1, new + 1, 41).tolist()
+    c = TreeCase(seed=new, heads=16, heads_kv=4, D=64, page=16, new=n, length=[x + int(m) for x, m in zip(n, r.randint(0, 400, 41))],
+                 window=window)
+    assert 41 * 4 >= 160 and max(n) * 4 > 32
+    a = c.attend()
+    c.check_tree(*a)
+    b = c.attend()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("shape", [dict(new=(5, 3), length=(80, 40)), dict(new=(60, 40), length=(300, 77), D=128, heads=8)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_chain_is_the_causal_mask(shape, dtype):
