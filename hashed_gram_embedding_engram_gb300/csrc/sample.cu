@@ -85,6 +85,14 @@ __device__ __forceinline__ uint32_t atom_cluster_add(uint32_t addr, uint32_t v) 
   return r;
 }
 
+// All threads of the row's blocks.
+__device__ __forceinline__ void sync_row(int cluster) {
+  if (cluster == 1)
+    __syncthreads();
+  else
+    ptx::cluster_sync();
+}
+
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
@@ -308,13 +316,13 @@ __device__ void part_sums(const R& row, const Scale& s, const Border& b, uint64_
   }
   sum = warp_sum(sum);
   ties = __reduce_add_sync(~0u, ties);
-  ptx::cluster_sync();             // what was there has been read
+  sync_row(cluster);             // what was there has been read
   const int part = rank * kWarps + warp;
   if (lane < cluster) {
     st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
     st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.ties[part]), lane), ties);
   }
-  ptx::cluster_sync();
+  sync_row(cluster);
 }
 
 // Total of the parts: weight above the border and that of the ties that are kept.  All lanes of a warp.
@@ -367,7 +375,7 @@ __device__ uint32_t descend(const R& row, const Scale& s, uint32_t floor, uint64
         }
       }
     }
-    ptx::cluster_sync();
+    sync_row(cluster);
     uint64_t mine = 0;
     if (tid < 256) {
       for (int c = 0; c < cluster; ++c) {
@@ -394,7 +402,7 @@ __device__ uint32_t descend(const R& row, const Scale& s, uint32_t floor, uint64
         sh.left = need - (upto - mine);
       }
     }
-    ptx::cluster_sync();                             // the histograms have been read
+    sync_row(cluster);                             // the histograms have been read
     prefix = prefix << 8 | sh.digit;
     need = sh.left;
     __syncthreads();
@@ -478,7 +486,7 @@ __device__ int send_list(const R& row, int cluster, int rank, Shared& sh, bool s
     const uint32_t to = ptx::mapa_shared(ptx::smem_u32(sh.list + base), 0);
     for (uint32_t i = tid; i < mine; i += kNT) st_cluster_u64(to + 8 * i, sh.u.own[i]);
   }
-  ptx::cluster_sync();
+  sync_row(cluster);
   uint32_t n = 0;
   for (int c = 0; c < cluster; ++c) n += min(sh.number[c], static_cast<uint32_t>(kList + 1));
   return n > kList ? -1 : static_cast<int>(n);
@@ -834,7 +842,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
     st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.top[rank]), tid), __float_as_uint(top));
     st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.bound[rank]), tid), __float_as_uint(bound));
   }
-  ptx::cluster_sync();
+  sync_row(a.cluster);
   for (int c = 0; c < a.cluster; ++c) {
     top = fmaxf(top, sh.top[c]);
     bound = fminf(bound, sh.bound[c]);
@@ -861,7 +869,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
     __syncthreads();
     best = __reduce_min_sync(~0u, sh.ties[lane % kWarps]);
     if (tid == 0) st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.best[rank]), 0), best);
-    ptx::cluster_sync();
+    sync_row(a.cluster);
     if (rank == 0 && tid == 0) {
       for (int c = 0; c < a.cluster; ++c) best = min(best, sh.best[c]);
       *token = static_cast<int32_t>(best);
@@ -886,7 +894,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
     }
     sum = warp_sum(sum);
     if (lane < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.sums[part]), lane), sum);
-    ptx::cluster_sync();
+    sync_row(a.cluster);
     if (warp == 0) find_part(parts, u, sh, [&](int i) { return sh.sums[i]; });
     __syncthreads();
     KeepLeast keep{least};
@@ -995,7 +1003,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
       for (int c = tid & 1; c < a.cluster; c += 2)
         st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.u.bins.all[rank][bin]), c), v);
     }
-    ptx::cluster_sync();
+    sync_row(a.cluster);
     uint64_t goal;
     {
       uint64_t t = 0;
@@ -1080,7 +1088,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
         const uint32_t to = ptx::mapa_shared(ptx::smem_u32(sh.list + sh.base), 0);
         for (uint32_t i = tid; i < n_band; i += kNT) st_cluster_u64(to + 8 * i, sh.u.local.band[i]);
       }
-      ptx::cluster_sync();
+      sync_row(a.cluster);
       uint32_t n = 0;
       uint64_t all_above = 0;
       for (int c = 0; c < a.cluster; ++c) {
@@ -1093,7 +1101,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
                                                      [&](uint64_t) { return goal; });
           if (tid < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.border), tid), border);
         }
-        ptx::cluster_sync();
+        sync_row(a.cluster);
         const uint64_t border = sh.border;
         // what is kept, summed over neighbours
         for (int i = tid; i < kSpans; i += kNT) sh.u.local.spans.lo[i] = sh.u.local.spans.hi[i] = 0;
@@ -1112,7 +1120,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
         uint64_t block_kept;
         block_scan(kept, block_kept, sh);
         if (tid < a.cluster) st_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sh.kept[rank]), tid), block_kept);
-        ptx::cluster_sync();
+        sync_row(a.cluster);
         if (warp == 0) find_part(a.cluster, u, sh, [&](int i) { return sh.kept[i]; });
         __syncthreads();
         if (sh.found != rank) return;
