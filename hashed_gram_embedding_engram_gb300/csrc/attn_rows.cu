@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kNT, 2)
           for (int e = 0; e < 2; ++e) {
             float x = -INFINITY;
             uint32_t sees = 0;
-            if constexpr (kTree) sees = tree_sees(tree[t][e], j0 + warp * 16) >> qc;
+            if constexpr (kTree) sees = tree_sees(a, w.q, tree[t][e], j0 + warp * 16) >> qc;
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll

@@ -75,38 +75,37 @@ __device__ __forceinline__ int row_tiles(const Seq& q, int G) {
   return static_cast<int>((static_cast<int64_t>(q.n) * G + RT - 1) / RT);
 }
 
-// What new token i of a tree sees: cached keys [lo, base), and base + j for the set
-// bits j of its row of the mask (none of either if it does not see itself).
+// What a new token of a tree sees: cached keys [lo, len - n), and len - n + j for the set bits j of its row of
+// the mask (none of either if it does not see itself).  Two registers; the rest is the sequence's.
 struct TreeRow {
-  const uint32_t* bits;
-  int lo, base, end;  // end: one past the sequence's last key
-  int words;          // 0: no key
+  int row;      // of the mask, -1: no key
+  int lo;
 };
 
 __device__ __forceinline__ TreeRow tree_row(const AttnArgs& a, const Seq& q, int i, bool live) {
-  TreeRow t{a.mask, 0, 0, 0, 0};
+  TreeRow t{-1, 0};
   if (!live || q.len < q.n || q.n > 32 * a.words) return t;
-  const int64_t row = static_cast<int64_t>(q.row0) + i;
-  t.bits = a.mask + row * a.words;
-  if (!(ptx::ld_after_wait(reinterpret_cast<const int32_t*>(t.bits) + (i >> 5)) >> (i & 31) & 1)) return t;
-  t.words = a.words;
-  t.base = q.len - q.n;
-  t.end = q.len;
+  const int row = q.row0 + i;
+  const int32_t* bits = reinterpret_cast<const int32_t*>(a.mask) + static_cast<int64_t>(row) * a.words;
+  if (!(ptx::ld_after_wait(bits + (i >> 5)) >> (i & 31) & 1)) return t;
+  t.row = row;
   // positions below the cached text's end are taken for it: the tile's keys begin where those see
-  if (a.window > 0) t.lo = max(0, max(ptx::ld_after_wait(a.positions + row), t.base) - a.window + 1);
+  if (a.window > 0) t.lo = max(0, max(ptx::ld_after_wait(a.positions + row), q.len - q.n) - a.window + 1);
   return t;
 }
 
 // Bit k, k < 32: whether the token sees key j0 + k.
-__device__ __forceinline__ uint32_t tree_sees(const TreeRow& t, int j0) {
-  const int from = min(max(t.lo - j0, 0), 32), to = min(max(t.base - j0, 0), 32);
+__device__ __forceinline__ uint32_t tree_sees(const AttnArgs& a, const Seq& q, const TreeRow& t, int j0) {
+  if (t.row < 0) return 0;
+  const int bit = j0 - (q.len - q.n);                // of the mask's row
+  const int from = min(max(t.lo - j0, 0), 32), to = min(max(-bit, 0), 32);
   uint32_t m = to > from ? (to == 32 ? ~0u : (1u << to) - 1) & (~0u << from) : 0u;
-  const int bit = j0 - t.base, w = bit >> 5;       // of the mask's row; words before the first and after the last are 0
   if (bit > -32) {
-    const int32_t* bits = reinterpret_cast<const int32_t*>(t.bits);
-    const uint32_t lo = w >= 0 && w < t.words ? ptx::ld_after_wait(bits + w) : 0;
-    const uint32_t hi = (bit & 31) && w + 1 < t.words ? ptx::ld_after_wait(bits + w + 1) : 0;
-    const int left = min(max(t.end - j0, 0), 32);
+    // words before the first and after the last are 0, bits after the last token are not looked at
+    const int w = bit >> 5, left = min(max(q.len - j0, 0), 32);
+    const int32_t* bits = reinterpret_cast<const int32_t*>(a.mask) + static_cast<int64_t>(t.row) * a.words;
+    const uint32_t lo = w >= 0 && w < a.words ? ptx::ld_after_wait(bits + w) : 0;
+    const uint32_t hi = (bit & 31) && w + 1 < a.words ? ptx::ld_after_wait(bits + w + 1) : 0;
     m |= __funnelshift_r(lo, hi, bit & 31) & (left == 32 ? ~0u : (1u << left) - 1);
   }
   return m;

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kNT, DP == 64 || (DP == 128 && RT == 16) ? 2 :
           if constexpr (kTree) {
 #pragma unroll
             for (int i = 0; i < K; i += 2) {
-              sees[i] = tree_sees(tree[k], j0 + 16 * i) >> tx;
+              sees[i] = tree_sees(a, w.q, tree[k], j0 + 16 * i) >> tx;
               sees[i + 1] = sees[i] >> 16;
             }
           }

@@ -225,10 +225,10 @@ __global__ void __launch_bounds__(kNT, 1)
               ptx::tmem_ld_wait();
               const int j1 = j0 + half * 64;
               if constexpr (kTree) {
-                if (__any_sync(~0u, live && (j1 < tree.lo || j1 + 64 > tree.base))) {
+                if (__any_sync(~0u, live && (j1 < tree.lo || j1 + 64 > w.q.len - w.q.n || tree.row < 0))) {
 #pragma unroll
                   for (int c = 0; c < 2; ++c) {
-                    const uint32_t sees = live ? tree_sees(tree, j1 + c * 32) : ~0u;
+                    const uint32_t sees = live ? tree_sees(a, w.q, tree, j1 + c * 32) : ~0u;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                       if (!(sees >> i & 1)) s[c][i] = 0xFF800000u;     // -inf
