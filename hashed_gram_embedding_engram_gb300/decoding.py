@@ -34,6 +34,14 @@ _pack_settings = struct.Struct("@PPPPfiff").pack
 _F32, _I32 = torch.float32, torch.int32
 
 
+def _output(t: Optional[torch.Tensor], name: str, shape: tuple, like: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    """An int32 output and its address: the caller's, checked, or a new one beside `like`."""
+    if t is None:
+        t = torch.empty(shape, dtype=_I32, device=like.device)
+        return t, t.data_ptr()
+    return t, _ptr(t, name, _I32, shape, like.get_device())
+
+
 def _plan_handle(plan: AttentionPlan):
     if not plan._h:
         raise ValueError("plan: it is closed")
@@ -60,14 +68,11 @@ class DraftTree:
             raise ValueError("window: must not be negative")
         h, dev, T = _plan_handle(plan), plan.device, parent.shape[0]
         parent_ptr = _ptr(parent, "parent", _I32, (T,), dev)
-        if mask is None:
-            mask = torch.empty(T, words, dtype=_I32, device=parent.device)
-        if positions is None:
-            positions = torch.empty(T, dtype=_I32, device=parent.device)
+        mask, mask_ptr = _output(mask, "mask", (T, words), parent)
+        positions, at_ptr = _output(positions, "positions", (T,), parent)
         self.plan, self.batch, self.parent, self.mask, self.positions = plan, batch, parent, mask, positions
         self.tokens, self.window = T, min(int(window), _INT_MAX)
-        self._packed = _pack_tree(_ptr(mask, "mask", _I32, (T, words), dev),
-                                  _ptr(positions, "positions", _I32, (T,), dev), words, self.window)
+        self._packed = _pack_tree(mask_ptr, at_ptr, words, self.window)
         _lib.check(plan._lib.engram_tree_build(h, batch._struct(T, dev), parent_ptr, self._packed,
                                                _a._current_stream(dev)), "engram_tree_build")
 
@@ -89,20 +94,15 @@ class DraftTree:
         h, dev, width = _plan_handle(plan), plan.device, int(width)
         if not 1 <= width <= 32 * _MAX_WORDS:
             raise ValueError(f"width: {width}, expected 1 to {32 * _MAX_WORDS}")
-        device = self.parent.device
-        if path is None:
-            path = torch.empty(B, width, dtype=_I32, device=device)
-        if count is None:
-            count = torch.empty(B, dtype=_I32, device=device)
-        if emitted is None:
-            emitted = torch.empty(B, width, dtype=_I32, device=device)
-        if length is None:
-            length = torch.empty(B, dtype=_I32, device=device)
+        parent = self.parent
+        path, path_ptr = _output(path, "path", (B, width), parent)
+        count, count_ptr = _output(count, "count", (B,), parent)
+        emitted, emitted_ptr = _output(emitted, "emitted", (B, width), parent)
+        length, length_ptr = _output(length, "length", (B,), parent)
         _lib.check(plan._lib.engram_tree_accept(
-            h, self.batch._struct(T, dev), self.parent.data_ptr(), _ptr(tokens, "tokens", _I32, (T,), dev),
-            _ptr(sampled, "sampled", _I32, (T,), dev), width, _ptr(path, "path", _I32, (B, width), dev),
-            _ptr(count, "count", _I32, (B,), dev), _ptr(emitted, "emitted", _I32, (B, width), dev),
-            _ptr(length, "length", _I32, (B,), dev), _a._current_stream(dev)), "engram_tree_accept")
+            h, self.batch._struct(T, dev), parent.data_ptr(), _ptr(tokens, "tokens", _I32, (T,), dev),
+            _ptr(sampled, "sampled", _I32, (T,), dev), width, path_ptr, count_ptr, emitted_ptr, length_ptr,
+            _a._current_stream(dev)), "engram_tree_accept")
         return path, count, emitted, length
 
 
@@ -157,14 +157,11 @@ class PagePool:
         that row's alone (engram_pool_reserve).  Returns (pairs int32 [rows, 2] for
         ``PagedCache.copy_pages``, missing int32 [1]: pages that were too few; then nothing changed)."""
         dev, n = self.plan.device, self.table.shape[0]
-        if pairs is None:
-            pairs = torch.empty(n, 2, dtype=_I32, device=self.table.device)
-        if missing is None:
-            missing = torch.empty(1, dtype=_I32, device=self.table.device)
+        pairs, pairs_ptr = _output(pairs, "pairs", (n, 2), self.table)
+        missing, missing_ptr = _output(missing, "missing", (1,), self.table)
         _lib.check(self.plan._lib.engram_pool_reserve(
             _plan_handle(self.plan), self._packed, _ptr(before, "before", _I32, (n,), dev), _ptr(after, "after", _I32, (n,), dev),
-            _ptr(pairs, "pairs", _I32, (n, 2), dev), _ptr(missing, "missing", _I32, (1,), dev),
-            self._workspace.data_ptr(), self.workspace_bytes, _a._current_stream(dev)), "engram_pool_reserve")
+            pairs_ptr, missing_ptr, self._workspace.data_ptr(), self.workspace_bytes, _a._current_stream(dev)), "engram_pool_reserve")
         return pairs, missing
 
 
@@ -203,10 +200,9 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, *, temperature: Union[f
         else:
             ptrs.append(0)
             values.append(min(max(int(x), -1), _INT_MAX) if dtype is _I32 else float(x))
-    if tokens is None:
-        tokens = torch.empty(R, dtype=_I32, device=logits.device)
+    tokens, tokens_ptr = _output(tokens, "tokens", (R,), logits)
     _lib.check(_lib._lib().engram_sample_tokens(
         logits.data_ptr(), _lib.F32 if logits.dtype is _F32 else _lib.BF16, s0, _ptr(u, "u", _F32, (R,), dev),
-        _pack_settings(*ptrs, *values), R, V, _ptr(tokens, "tokens", _I32, (R,), dev), _a._current_stream(dev)),
+        _pack_settings(*ptrs, *values), R, V, tokens_ptr, _a._current_stream(dev)),
         "engram_sample_tokens")
     return tokens
