@@ -37,10 +37,13 @@ __device__ __forceinline__ Scale make_scale(float top, float temperature) {
 }
 
 // a of two logits, as (l - m) times -c: the same roundings.  Of NaN: the minimum with it is 64.
-__device__ __forceinline__ float2 exponents(const Scale& s, float x0, float x1) {
-  if (s.odd) return make_float2(x0 == s.top ? 0.f : kFar, x1 == s.top ? 0.f : kFar);
+__device__ __forceinline__ float2 finite_exponents(const Scale& s, float x0, float x1) {
   const float2 a = unpack2(mul2(add2(pack2(x0, x1), pack2(-s.top, -s.top)), pack2(s.c, s.c)));
   return make_float2(fminf(a.x, kFar), fminf(a.y, kFar));
+}
+__device__ __forceinline__ float2 exponents(const Scale& s, float x0, float x1) {
+  if (s.odd) return make_float2(x0 == s.top ? 0.f : kFar, x1 == s.top ? 0.f : kFar);
+  return finite_exponents(s, x0, x1);
 }
 
 // Two weights 2^38 p 2^-n as the numbers p (0.7 to 1.42) and n + kRound.
