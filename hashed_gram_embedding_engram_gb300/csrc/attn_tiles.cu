@@ -33,6 +33,9 @@
 // its full rate beside the copies that fill it.  16 and 4 heads of 64, the same
 // tokens: 136 us (0.76 PFLOP/s): half the products a step, the same exponentials.
 // 16 x 24 tokens over 16384 keys 192 us (5.6 TB/s).
+// Trees of drafts (kTree): what a row sees comes from its row of the mask, looked at only in steps that
+// reach the new tokens.  32 trees of 8 to 64 tokens (32 to 256 rows) over 100 to 8192: 157 us (3.5 TB/s;
+// tensor pipe 36 %: tiles of 256 rows are 56 % full), one of 26 over 517 17 to 19 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

