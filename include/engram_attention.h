@@ -90,7 +90,7 @@ engram_status_t engram_attn_plan_destroy(engram_attn_plan_t* plan);
 /* Synchronise `stream`, read and clear the plan's error word (as engram_get_error). */
 engram_status_t engram_attn_get_error(const engram_attn_plan_t* plan, engram_stream_t stream, uint32_t* flags_out);
 
-/* Bytes of device workspace engram_paged_attention needs.  The caller zero-fills
+/* Bytes of device workspace engram_paged_attention and engram_tree_attention need.  The caller zero-fills
  * its first 16384 bytes (counters) once when new; the calls leave them ready for
  * the next one.  Calls that may run at the same time need a workspace each. */
 engram_status_t engram_attn_workspace_bytes(const engram_attn_plan_t* plan, size_t* bytes);
@@ -165,8 +165,8 @@ engram_status_t engram_verify_drafts(const void* target, const void* draft_probs
  * token parent[i] < i of its sequence, or the cached text (parent -1).  It sees
  * the cached tokens, the tokens it descends from and itself, and its position
  * is length[b] - n_b + its depth, the number of new tokens before it.  A
- * sequence with length[b] < n_b is idle: its tokens have position 0 and see no
- * key.  A step: engram_tree_build; for each layer engram_qk_norm_rope at
+ * sequence with length[b] < n_b is idle (length 0: engram_kv_append leaves its
+ * tokens out too): its tokens have position 0 and see no key.  A step: engram_tree_build; for each layer engram_qk_norm_rope at
  * `positions`, engram_kv_append without a rope table, engram_tree_attention;
  * then engram_sample_tokens at every new token, engram_tree_accept, and for
  * each layer engram_kv_compact. */

@@ -148,6 +148,16 @@ def test_rows_apart_and_at_any_element(dtype):
     check(flat.view(-1)[:5000].expand(1, 5000), torch.rand(1).cuda())
 
 
+@pytest.mark.parametrize("V,dtype", [(300001, torch.float32), (360000, torch.float32), (300003, torch.bfloat16),
+                                     (600001, torch.bfloat16), (720001, torch.bfloat16)])
+def test_rows_that_just_fit_shared_memory(V, dtype):
+    """Pieces of more than 64 KB (one block an SM), of more than 65536 tokens (whose places take 17 bits), and the
+    longest that are kept."""
+    logits, u = normal(2, V, 14, dtype=dtype)
+    for settings in (dict(top_p=0.9), dict(temperature=2.0, top_p=0.7), dict(top_k=60, top_p=0.8), dict(min_p=0.01)):
+        check(logits, u, **settings)
+
+
 def test_rows_too_long_for_shared_memory():
     """Longer than a cluster's shared memory holds: read again from device memory."""
     for V, dtype in ((600001, torch.float32), (1100003, torch.bfloat16)):
