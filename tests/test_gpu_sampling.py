@@ -195,6 +195,20 @@ def test_weights_are_exponentials():
         assert (near <= want * (1.01e-7 + 3 * 2.0 ** -24 * a * math.log(2)) + 1).all()
 
 
+def test_two_streams_give_the_same_tokens():
+    inputs = [normal(40, 30000, i, dtype=t) for i, t in enumerate((torch.float32, torch.bfloat16))]
+    kw = dict(temperature=1.1, top_p=0.9)
+    want = [sample_tokens(*x, **kw) for x in inputs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in inputs], []
+    for _ in range(20):
+        for i, (x, s) in enumerate(zip(inputs, streams)):
+            with torch.cuda.stream(s):
+                got.append((i, sample_tokens(*x, **kw)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want[i]) for i, t in got)
+
+
 def test_graph_replay():
     logits, u = normal(4, 3000, 11)
     k = torch.tensor([0, 1, 20, 300], dtype=torch.int32, device="cuda")

@@ -275,6 +275,33 @@ def test_graph_replay_reads_the_trees_of_the_day():
         c.check_tree(out, lse)
 
 
+def test_calls_on_two_streams_and_replays_beside_them():
+    """Tiles cut into parts on each of two streams, and a captured call replayed on a third: a workspace each."""
+    cases = [TreeCase(seed=20 + i, new=(40, 64), length=(3000, 2500), heads=8, heads_kv=2, D=128, page=32) for i in range(3)]
+    for c in cases[1:]:                                 # one plan, three caches
+        c.plan = cases[0].plan
+        c.cache = type(c.cache)(c.plan, c.kd, c.vd)
+        c.tree = c.build()
+    want = [c.attend() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(streams[2]):
+        with torch.cuda.graph(graph, stream=streams[2]):
+            replayed = cases[2].cache.attend_tree(cases[2].tree, cases[2].q)
+    got = []
+    for _ in range(20):
+        for c, s in zip(cases[:2], streams):
+            with torch.cuda.stream(s):
+                got.append((c, c.cache.attend_tree(c.tree, c.q)))
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+    torch.cuda.synchronize()
+    for c, (out, lse) in got + [(cases[2], replayed)]:
+        o, l = want[cases.index(c)]
+        assert torch.equal(out, o) and torch.equal(lse, l)
+
+
 # ---------------------------------------------------------------- accepted paths
 def accept_case(seed, B, most, vocab, width):
     rng = random.Random(seed)
