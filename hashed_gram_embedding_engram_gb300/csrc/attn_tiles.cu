@@ -34,7 +34,7 @@
 // tokens: 136 us (0.76 PFLOP/s): half the products a step, the same exponentials.
 // 16 x 24 tokens over 16384 keys 192 us (5.6 TB/s).
 // Trees of drafts (kTree): what a row sees comes from its row of the mask, looked at only in steps that
-// reach the new tokens.  32 trees of 8 to 64 tokens (32 to 256 rows) over 100 to 8192: 157 us (3.5 TB/s;
+// reach the new tokens.  32 trees of 8 to 64 tokens (32 to 256 rows) over 100 to 8192: 148 us (3.7 TB/s;
 // tensor pipe 36 %: tiles of 256 rows are 56 % full), one of 26 over 517 17 to 19 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -53,7 +53,10 @@ using namespace at;
 
 constexpr int kRT = 256;
 constexpr int kKT = 128;
-constexpr int kCost = 5;           // steps that a tile's queries, output and joins are worth
+// Steps that a tile's queries, output and joins are worth.  Trees: 32 of 8 to 64 tokens took 164 us with 3, 157
+// with 5, 148 with 8, 152 with 12 and 157 with 18.  (Steps of tiles with one half counted as half of one: 171.)
+constexpr int kChunkCost = 5;
+constexpr int kTreeCost = 8;
 constexpr int kSoft = 512;         // softmax threads
 constexpr int kNT = kSoft + 128;   // warps 18 and 19 only round the last warpgroup up
 constexpr float kSlack = 8.f;      // powers of two a row's maximum may grow before O is rescaled
@@ -137,6 +140,7 @@ __global__ void __launch_bounds__(kNT, 1)
                       const __grid_constant__ CUtensorMap map_v) {
   constexpr int kStages = Cfg<D>::kStages;
   constexpr int kTile = Cfg<D>::kTile;
+  constexpr int kCost = kTree ? kTreeCost : kChunkCost;
   constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, kKT);
   constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(128, D) | (1u << 16);   // B (the values) MN-major
   extern __shared__ uint8_t smem_raw[];
@@ -574,7 +578,8 @@ template <int D>
 cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, AttnArgs a, int max_new, cudaStream_t s) {
   // Trees of few tiles are cut into many parts: joined by a kernel of their own (2 trees of 64 tokens over 30k and
   // 65k, 8 tiles: 51 us, in the tiles kernel 86).  With a tile for every block or more, a tile has two or three
-  // parts, and the joins run beside other tiles' steps (32 trees, 256 tiles: 159 us, with the other kernel 164).
+  // parts, and the joins run beside other tiles' steps (32 trees, 256 tiles: 159 us, with the other kernel 164; both
+  // before their costs were set).
   const int64_t tiles = (static_cast<int64_t>(max_new) * a.group + kRT - 1) / kRT * a.seq.B * a.heads_kv;
   if (a.causal != kSeesTree || tiles >= p->num_sms) a.splits = nullptr;
   auto* kernel = a.causal == kSeesTree ? attn_tiles_kernel<D, true> : attn_tiles_kernel<D, false>;
