@@ -110,7 +110,8 @@ class PagePool:
     """Pages shared among the rows of a page table: ``table`` int32 [rows, table_pages] (below 0: no
     page) and ``ref`` int32 [pages], how many entries name each page; both are the caller's and updated
     in place.  The table's rows serve SequenceBatch, one table all layers' caches.  Calls on one pool
-    run one after another: it has one workspace."""
+    run one after another, whatever their streams: they update the same two tensors, which like the
+    plan have to outlive what is queued or captured on them (the pool itself may go)."""
 
     def __init__(self, plan: AttentionPlan, table: torch.Tensor, ref: torch.Tensor):
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
@@ -127,7 +128,6 @@ class PagePool:
         _lib.check(plan._lib.engram_pool_workspace_bytes(self._packed, _lib.ctypes.byref(n)),
                    "engram_pool_workspace_bytes")
         self.workspace_bytes = n.value
-        self._workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=table.device)
 
     @classmethod
     def empty(cls, plan: AttentionPlan, rows: int, table_pages: int, pages: int) -> "PagePool":
@@ -159,9 +159,12 @@ class PagePool:
         dev, n = self.plan.device, self.table.shape[0]
         pairs, pairs_ptr = _output(pairs, "pairs", (n, 2), self.table)
         missing, missing_ptr = _output(missing, "missing", (1,), self.table)
+        # of the call's own stream, and in a graph's memory under capture: what is given back here is used
+        # again only behind this call, and stays the graph's as long as that may be replayed
+        workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.table.device)
         _lib.check(self.plan._lib.engram_pool_reserve(
             _plan_handle(self.plan), self._packed, _ptr(before, "before", _I32, (n,), dev), _ptr(after, "after", _I32, (n,), dev),
-            pairs_ptr, missing_ptr, self._workspace.data_ptr(), self.workspace_bytes, _a._current_stream(dev)), "engram_pool_reserve")
+            pairs_ptr, missing_ptr, workspace.data_ptr(), self.workspace_bytes, _a._current_stream(dev)), "engram_pool_reserve")
         return pairs, missing
 
 
