@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kRowNT) pool_free_kernel(engram_pool_t p, int 
 }
 
 // One block a pair.  What makes a pair good is read from src, dst and its own row alone, so no
-// block's answer depends on how far another is.
+// block's answer depends on how far another is: a row that any pair reads is written by none.
 __global__ void __launch_bounds__(kRowNT) pool_fork_kernel(engram_pool_t p, int page_shift, const int32_t* src,
                                                            const int32_t* dst, const int32_t* length, int n,
                                                            uint32_t* err) {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kRowNT) pool_fork_kernel(engram_pool_t p, int 
              len > static_cast<int64_t>(p.table_pages) << page_shift;
   for (int j = tid; j < n; j += kRowNT) {
     const int x = ptx::ld_after_wait(src + j), y = ptx::ld_after_wait(dst + j);
-    bad = bad || x == d || y == a || (j != i && y == d);
+    bad = bad || x == d || (j != i && y == d);
   }
   if (__syncthreads_or(bad)) {
     if (tid == 0) atomicOr(err, kErrIndexRange);

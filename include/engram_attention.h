@@ -254,7 +254,8 @@ engram_status_t engram_pool_free(const engram_attn_plan_t* plan, const engram_po
  * page's count rises by one.  Row dst[i] has to be without pages.  INDEX_RANGE,
  * and the pair is left out: a row outside the table, dst[i] named by any other
  * dst or any src, a dst with an entry, a length outside [0, table_pages * page]
- * or past src's pages, or an entry past the pool. */
+ * or past src's pages, or an entry past the pool.  What a pair that is left out
+ * would have written does not keep others from reading that row as it is. */
 engram_status_t engram_pool_fork(const engram_attn_plan_t* plan, const engram_pool_t* pool, const int32_t* src,
                                  const int32_t* dst, const int32_t* length, int64_t n, engram_stream_t stream);
 

@@ -117,7 +117,7 @@ class Pool:
         good = []
         for i, (a, d, n) in enumerate(zip(src, dst, length)):
             ok = 0 <= a < len(self.table) and 0 <= d < len(self.table) and 0 <= n <= len(self.table[0]) * self.page
-            ok = ok and d not in src and a not in dst and list(dst).count(d) == 1
+            ok = ok and d not in src and list(dst).count(d) == 1
             ok = ok and all(e < 0 for e in self.table[d])
             ok = ok and all(0 <= e < len(self.ref) for e in self.table[a][:self.pages_of(n)])
             good.append(ok)
