@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kNT, kCached ? 2 : 1) sample_kernel(const __gr
   // the blocks whose threads nearly all have logits share top-k's bound (the last ones may have few, or none)
   const int chunk = kWarps * a.piece;
   const int sharing = max(1, min(a.cluster, (row.nv + chunk / 2) / chunk));
-  const int each = (top_k + sharing - 1) / sharing;
+  const int each = top_k_share(top_k, a.V, sharing);
   // (random logits of which 3 / (3 + blocks) of the threads' largest reach the bound are 950 to 1500 tokens)
   const bool listed = by_k && each <= kNT * 3 / (3 + a.cluster);
   const float mine = top;

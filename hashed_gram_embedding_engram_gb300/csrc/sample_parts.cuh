@@ -101,5 +101,12 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
+// How many of the largest logits each of `blocks` blocks names, so that together they have the first top_k of
+// V.  top_k is any number: from V on (2^31 - 1 among them) it is off, and not added to.
+__host__ __device__ __forceinline__ int top_k_share(int top_k, int V, int blocks) {
+  const int kept = top_k < 0 ? 0 : (top_k < V ? top_k : V);
+  return (kept + blocks - 1) / blocks;
+}
+
 }  // namespace sample
 }  // namespace engram
