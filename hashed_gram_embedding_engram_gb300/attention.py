@@ -322,10 +322,10 @@ class PagedCache:
         p = self.plan
         if not p._h:
             raise ValueError("cache: its plan is closed")
+        D, dt, dev, T = p.head_dim, p.torch_dtype, p.device, tree.tokens
+        vq = _view(q, "q", dt, p.heads, D, dev, T)
         if _grad_mode() and q.requires_grad:
             _forward_only(q=q)
-        D, dt, dev, T = p.head_dim, p.torch_dtype, p.device, q.shape[0]
-        vq = _view(q, "q", dt, p.heads, D, dev, tree.tokens)
         packed = tree._struct(dev)
         if out is None:
             out = torch.empty(T, p.heads, D, dtype=dt, device=q.device)

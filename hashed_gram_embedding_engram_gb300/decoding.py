@@ -42,6 +42,12 @@ def _output(t: Optional[torch.Tensor], name: str, shape: tuple, like: torch.Tens
     return t, _ptr(t, name, _I32, shape, like.get_device())
 
 
+def _rows_of(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name}: expected int32 [n]")
+    return t.shape[0]
+
+
 def _plan_handle(plan: AttentionPlan):
     if not plan._h:
         raise ValueError("plan: it is closed")
@@ -138,7 +144,7 @@ class PagePool:
 
     def free(self, rows: torch.Tensor, keep: torch.Tensor) -> None:
         """Rows int32 [n] keep the pages of their first ``keep`` int32 [n] tokens (engram_pool_free)."""
-        dev, n = self.plan.device, rows.shape[0]
+        dev, n = self.plan.device, _rows_of(rows, "rows")
         _lib.check(self.plan._lib.engram_pool_free(
             _plan_handle(self.plan), self._packed, _ptr(rows, "rows", _I32, (n,), dev), _ptr(keep, "keep", _I32, (n,), dev), n,
             _a._current_stream(dev)), "engram_pool_free")
@@ -146,7 +152,7 @@ class PagePool:
     def fork(self, src: torch.Tensor, dst: torch.Tensor, length: torch.Tensor) -> None:
         """Rows ``dst`` int32 [n], which have no pages, share those of the first ``length`` int32 [n]
         tokens of rows ``src`` int32 [n] (engram_pool_fork)."""
-        dev, n = self.plan.device, src.shape[0]
+        dev, n = self.plan.device, _rows_of(src, "src")
         _lib.check(self.plan._lib.engram_pool_fork(
             _plan_handle(self.plan), self._packed, _ptr(src, "src", _I32, (n,), dev), _ptr(dst, "dst", _I32, (n,), dev),
             _ptr(length, "length", _I32, (n,), dev), n, _a._current_stream(dev)), "engram_pool_fork")
@@ -177,6 +183,8 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, *, temperature: Union[f
     ``top_k`` (0: off), ``top_p`` (1: off), ``min_p`` (0: off).  Returns int32 [R]."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (_F32, torch.bfloat16) or logits.dim() != 2:
         raise ValueError("logits: expected float32 or bfloat16 [R, V]")
+    if not isinstance(u, torch.Tensor):
+        raise TypeError("u: expected a torch.Tensor")
     if _a._grad_mode() and (logits.requires_grad or u.requires_grad):
         _a._forward_only(logits=logits, u=u)
     R, V = logits.shape
@@ -202,7 +210,10 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, *, temperature: Union[f
             values.append(0)
         else:
             ptrs.append(0)
-            values.append(min(max(int(x), -1), _INT_MAX) if dtype is _I32 else float(x))
+            try:
+                values.append(min(max(int(x), -1), _INT_MAX) if dtype is _I32 else float(x))
+            except (TypeError, ValueError, OverflowError):
+                raise ValueError(f"{name}: {x!r}, expected a number or a tensor of one for each row") from None
     tokens, tokens_ptr = _output(tokens, "tokens", (R,), logits)
     _lib.check(_lib._lib().engram_sample_tokens(
         logits.data_ptr(), _lib.F32 if logits.dtype is _F32 else _lib.BF16, s0, _ptr(u, "u", _F32, (R,), dev),
