@@ -26,6 +26,7 @@ from . import attention as _a
 from .attention import _INT_MAX, AttentionPlan, SequenceBatch, _off_device, _ptr
 
 _MAX_WORDS = 8              # of a row of a tree's mask (32 tokens each)
+_MAX_ROWS = 65536           # of a table that reserve extends, and that a call of free or fork names
 
 _pack_tree = struct.Struct("@PPii").pack
 _pack_pool = struct.Struct("@PPiiq").pack
@@ -45,6 +46,8 @@ def _output(t: Optional[torch.Tensor], name: str, shape: tuple, like: torch.Tens
 def _rows_of(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or t.dim() != 1:
         raise ValueError(f"{name}: expected int32 [n]")
+    if t.shape[0] > _MAX_ROWS:
+        raise ValueError(f"{name}: {t.shape[0]} rows, at most {_MAX_ROWS} a call")
     return t.shape[0]
 
 
@@ -115,7 +118,8 @@ class DraftTree:
 class PagePool:
     """Pages shared among the rows of a page table: ``table`` int32 [rows, table_pages] (below 0: no
     page) and ``ref`` int32 [pages], how many entries name each page; both are the caller's and updated
-    in place.  The table's rows serve SequenceBatch, one table all layers' caches.  Calls on one pool
+    in place.  The table's rows serve SequenceBatch, one table all layers' caches.  ``reserve`` takes
+    tables of up to 65536 rows, ``free`` and ``fork`` up to 65536 rows a call.  Calls on one pool
     run one after another, whatever their streams: they update the same two tensors, which like the
     plan have to outlive what is queued or captured on them (the pool itself may go)."""
 
@@ -163,6 +167,8 @@ class PagePool:
         that row's alone (engram_pool_reserve).  Returns (pairs int32 [rows, 2] for
         ``PagedCache.copy_pages``, missing int32 [1]: pages that were too few; then nothing changed)."""
         dev, n = self.plan.device, self.table.shape[0]
+        if n > _MAX_ROWS:
+            raise ValueError(f"table: {n} rows, reserve extends tables of at most {_MAX_ROWS}")
         pairs, pairs_ptr = _output(pairs, "pairs", (n, 2), self.table)
         missing, missing_ptr = _output(missing, "missing", (1,), self.table)
         # of the call's own stream, and in a graph's memory under capture: what is given back here is used

@@ -237,7 +237,7 @@ engram_status_t engram_kv_copy_pages(engram_kv_cache_t* cache, const int32_t* pa
 typedef struct {
   int32_t* table;               /* [rows, table_pages] */
   int32_t* ref;                 /* [pages] */
-  int rows;                     /* >= 0 */
+  int rows;                     /* >= 0; engram_pool_reserve: at most 65536, else ENGRAM_ERR_UNSUPPORTED */
   int table_pages;              /* >= 1, table_pages * page <= 2^30 */
   int64_t pages;                /* 1 <= pages < 2^31 */
 } engram_pool_t;
@@ -246,7 +246,7 @@ typedef struct {
  * pages' counts drop by one.  rows, keep: int32 [n]; a row outside the table, a
  * negative keep and an entry past the pool set INDEX_RANGE and change nothing; a
  * page whose count is 0 already sets it and keeps that.  A row named twice keeps
- * the lesser. */
+ * the lesser.  n at most 65536 (more: ENGRAM_ERR_UNSUPPORTED). */
 engram_status_t engram_pool_free(const engram_attn_plan_t* plan, const engram_pool_t* pool, const int32_t* rows,
                                  const int32_t* keep, int64_t n, engram_stream_t stream);
 
@@ -255,7 +255,8 @@ engram_status_t engram_pool_free(const engram_attn_plan_t* plan, const engram_po
  * and the pair is left out: a row outside the table, dst[i] named by any other
  * dst or any src, a dst with an entry, a length outside [0, table_pages * page]
  * or past src's pages, or an entry past the pool.  What a pair that is left out
- * would have written does not keep others from reading that row as it is. */
+ * would have written does not keep others from reading that row as it is.  n at
+ * most 65536 (more: ENGRAM_ERR_UNSUPPORTED). */
 engram_status_t engram_pool_fork(const engram_attn_plan_t* plan, const engram_pool_t* pool, const int32_t* src,
                                  const int32_t* dst, const int32_t* length, int64_t n, engram_stream_t stream);
 

@@ -46,3 +46,22 @@ def test_queries_that_are_no_queries(lib, grad):  # noqa: F811
         with torch.set_grad_enabled(grad), pytest.raises((TypeError, ValueError), match="^q: "):
             cache(plan()).attend_tree(tree(), wrong)
     assert count(lib, "engram_tree_attention") == 0
+
+
+def test_more_rows_than_a_call_takes(lib):  # noqa: F811
+    n = 65536
+    for call in (lambda n: pool().free(i32(n), i32(n)), lambda n: pool().fork(i32(n), i32(n), i32(n))):
+        call(n)
+        with pytest.raises(ValueError, match="65536"):
+            call(n + 1)
+    assert (count(lib, "engram_pool_free"), count(lib, "engram_pool_fork")) == (1, 1)
+    for rows in (n, n + 1):
+        p = pool()
+        p.table = i32(rows, 2)
+        outputs = dict(pairs=i32(rows, 2), missing=i32(1))
+        if rows == n:
+            p.reserve(i32(rows), i32(rows), **outputs)
+        else:
+            with pytest.raises(ValueError, match="^table: 65537 rows"):
+                p.reserve(i32(rows), i32(rows), **outputs)
+    assert count(lib, "engram_pool_reserve") == 1
