@@ -345,7 +345,9 @@ class PagedCache:
     def compact(self, batch: SequenceBatch, path: torch.Tensor, count: torch.Tensor) -> None:
         """Move the kept rows of each sequence together, in place: the keys and values of new token
         ``path[b, i]`` (int32 [B, width], ascending) to the slot of new token i, for i < ``count[b]``
-        (int32 [B]) (engram_kv_compact)."""
+        (int32 [B]) (engram_kv_compact).  Keys keep their rotation: after a whole text was thinned out,
+        rotate what follows with ``qk_norm_rope`` at positions of your own, past the whole text's, and
+        append it without ``rope``."""
         p = self.plan
         if not p._h:
             raise ValueError("cache: its plan is closed")

@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(kCopyNT) copy_pages_kernel(uint4* k, uint4* v,
 // a group read before any of it is written; the next group's reads may go out before.
 // Columns, heads, keys and values have nothing to do with one another.
 constexpr int kMoveNT = 256;
-constexpr int kMoveRows = 4;        // rows a thread has in flight, twice
-constexpr int kShortRows = 8;       // the same for short paths, once
+constexpr int kMoveRows = 4;        // a thread's rows of a group (kDepth groups are in flight)
+constexpr int kShortRows = 8;       // of a short path: all that are in flight
 constexpr int kShort = 32;          // rows of a sequence that a block moves at once
 
 struct MoveArgs {

@@ -5,6 +5,7 @@ Argument marshalling only, as in attention.py: every step runs in the library's 
 current stream.  A step with trees of drafts:
 
     pairs, missing = pool.reserve(fed, fed + n)          # pages for the new tokens; copy on write
+    if int(missing): ...                                 # nothing has changed: free pages, or extend fewer rows
     cache.copy_pages(pairs)                              # in every layer's cache
     tree = DraftTree(plan, batch, parent, max_nodes=64)
     q, k = plan.qk_norm_rope(q, k, tree.positions, rope) # in every layer
@@ -13,6 +14,8 @@ current stream.  A step with trees of drafts:
     sampled = sample_tokens(logits, u, top_p=0.9)        # after every new token
     path, count, emitted, fed = tree.accept(tokens, sampled)
     cache.compact(batch, path, count)                    # in every layer's cache
+
+Appending after a reserve whose ``missing`` is not 0 would write into pages that other rows share.
 """
 from __future__ import annotations
 
@@ -64,7 +67,9 @@ class DraftTree:
 
     ``max_nodes``: the most new tokens of a sequence, at most 256.  ``window`` as in ``attend``.
     ``positions`` int32 [tokens] then holds each token's place in the text (for the rotation), ``mask``
-    int32 [tokens, words] the new tokens that it sees, bit by bit.  They are allocated unless given."""
+    int32 [tokens, words] the new tokens that it sees, bit by bit.  They are allocated unless given.
+    Rows of no sequence (past ``start[B]``) are not written: give zeroed ``positions`` where a batch is
+    padded with such rows and its queries are rotated."""
 
     def __init__(self, plan: AttentionPlan, batch: SequenceBatch, parent: torch.Tensor, *, max_nodes: int = 64,
                  window: int = 0, mask: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None):
@@ -165,7 +170,8 @@ class PagePool:
                 missing: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Pages for tokens ``before[r]`` .. ``after[r]`` - 1 of every row r (int32 [rows]) that are each
         that row's alone (engram_pool_reserve).  Returns (pairs int32 [rows, 2] for
-        ``PagedCache.copy_pages``, missing int32 [1]: pages that were too few; then nothing changed)."""
+        ``PagedCache.copy_pages``, missing int32 [1]: pages that were too few; then nothing changed, and
+        the tokens must not be appended: rows may still share the pages that they would be written to)."""
         dev, n = self.plan.device, self.table.shape[0]
         if n > _MAX_ROWS:
             raise ValueError(f"table: {n} rows, reserve extends tables of at most {_MAX_ROWS}")

@@ -216,8 +216,14 @@ engram_status_t engram_tree_accept(const engram_attn_plan_t* plan, const engram_
  * width], sets INDEX_RANGE and moves nothing of its sequence; a page id outside
  * the cache sets INDEX_RANGE and its tokens are left out.  Other slots are not
  * written.  Two sequences that share a written page give either's rows there.
- * With n_b = length[b] it is the whole sequence that is thinned out.  seq->tokens
- * and max_new are not looked at. */
+ * With n_b = length[b] it is the whole sequence that is thinned out.  Keys keep the
+ * rotation that they were appended with, while the positions that other calls count
+ * (engram_kv_append, engram_tree_build, causal masks and windows) are places in the
+ * cache, smaller than the kept keys' from then on.  What follows a thinned text is
+ * therefore rotated by engram_qk_norm_rope to positions of the caller's, which go on
+ * from the whole text's, and appended without a rope table; a window then counts kept
+ * tokens.  A path accepted from a tree needs none of this: its tokens end up at the
+ * positions they were rotated to.  seq->tokens and max_new are not looked at. */
 engram_status_t engram_kv_compact(engram_kv_cache_t* cache, const engram_sequences_t* seq, const int32_t* path,
                                   int width, const int32_t* count, engram_stream_t stream);
 
@@ -266,7 +272,10 @@ engram_status_t engram_pool_fork(const engram_attn_plan_t* plan, const engram_po
  * whose count was above 1 when the call began; if that page holds earlier tokens
  * of the row, pairs[r] is (its id, the new one) for engram_kv_copy_pages, else
  * (-1, -1).  pairs int32 [rows, 2].  missing int32 [1]: 0, or the pages that were
- * too few; then nothing else is changed and no pair is given.  A negative before
+ * too few; then nothing else is changed and no pair is given: rows may still name
+ * pages that other rows name too, or none, so look at it before the tokens are
+ * appended, which would write over the others' keys unreported (free pages, or
+ * extend fewer rows, and call again).  A negative before
  * or an after past the table's row sets INDEX_RANGE and leaves its row out; an
  * entry past the pool sets it and stays.  workspace: engram_pool_workspace_bytes,
  * 16-byte aligned, contents irrelevant. */
