@@ -20,7 +20,7 @@ Appending after a reserve whose ``missing`` is not 0 would write into pages that
 from __future__ import annotations
 
 import struct
-from typing import Optional, Tuple, Union
+from typing import Dict, Optional, Tuple, Union
 
 import torch
 
@@ -151,6 +151,23 @@ class PagePool:
         return cls(plan, torch.full((rows, table_pages), -1, dtype=_I32, device=device),
                    torch.zeros(pages, dtype=_I32, device=device))
 
+    _workspaces: Optional[Dict[int, torch.Tensor]] = None      # of each stream, from its first call on
+
+    def _workspace_on(self, stream: int) -> torch.Tensor:
+        """Memory for a call on a stream, which is the current one: allocated there, so that once the
+        pool is gone it is used again only behind what is queued.  A call under capture gets memory of its
+        graph, which stays that graph's.  (Allocated with each call it took 2 to 4 us of the host's time.)"""
+        kept = self._workspaces
+        if kept is None:
+            kept = self._workspaces = {}
+        captured = _a._capturing()
+        ws = None if captured else kept.get(stream)
+        if ws is None:
+            ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.table.device)
+            if not captured:
+                kept[stream] = ws
+        return ws
+
     def free(self, rows: torch.Tensor, keep: torch.Tensor) -> None:
         """Rows int32 [n] keep the pages of their first ``keep`` int32 [n] tokens (engram_pool_free)."""
         dev, n = self.plan.device, _rows_of(rows, "rows")
@@ -177,12 +194,11 @@ class PagePool:
             raise ValueError(f"table: {n} rows, reserve extends tables of at most {_MAX_ROWS}")
         pairs, pairs_ptr = _output(pairs, "pairs", (n, 2), self.table)
         missing, missing_ptr = _output(missing, "missing", (1,), self.table)
-        # of the call's own stream, and in a graph's memory under capture: what is given back here is used
-        # again only behind this call, and stays the graph's as long as that may be replayed
-        workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.table.device)
+        stream = _a._current_stream(dev)
+        workspace = self._workspace_on(stream)
         _lib.check(self.plan._lib.engram_pool_reserve(
             _plan_handle(self.plan), self._packed, _ptr(before, "before", _I32, (n,), dev), _ptr(after, "after", _I32, (n,), dev),
-            pairs_ptr, missing_ptr, workspace.data_ptr(), self.workspace_bytes, _a._current_stream(dev)), "engram_pool_reserve")
+            pairs_ptr, missing_ptr, workspace.data_ptr(), self.workspace_bytes, stream), "engram_pool_reserve")
         return pairs, missing
 
 
