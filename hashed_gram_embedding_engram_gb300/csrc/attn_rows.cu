@@ -11,7 +11,8 @@
 //   * the TMA warp copies steps of 64 keys (one box a page and 64 columns,
 //     128-byte swizzle) into a ring; keys and values have barriers of their own.
 //   * scores: warp w has keys 16w .. 16w + 15 of the step; the warps share each
-//     row's maximum and their weights (bf16) through shared memory.
+//     row's maximum and their weights through shared memory: rounded to bf16, as the
+//     product's operands are of one type; totals are of the weights before it.
 //   * output: warp w has a quarter of the columns for all 64 keys, so the
 //     accumulators need no join between the warps.
 // The products are mma.sync m16n8k16: a tcgen05 tile has 128 rows, of which
@@ -22,7 +23,9 @@
 // Measured (32 query heads, 8 cache heads, D 128): single tokens of 256
 // sequences over 1 to 4096 keys 325 us (6.5 TB/s, 0.96 of a plain copy's rate),
 // of three over 30k to 131k 155 us (6.4 TB/s); drafts of 4 to 24 rows over 100
-// to 8192 keys 102 us (5.3 TB/s: the ends of the many short tiles).
+// to 8192 keys 102 us (5.3 TB/s: the ends of the many short tiles).  Trees of 8 tokens
+// (32 rows): 32 over 4096 keys 113 us (4.7 TB/s); with 16 and 4 heads of 64 44 us; one
+// over 517 (8 and 2 heads of 128) 16.5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -23,7 +23,9 @@
 // the round trip of O through the registers is rare.
 // Weights come from ex2.approx.ftz: its error, 2^-22 of the value, is far below the
 // weights' rounding to bf16 for the second product, and what it flushes to zero
-// (below 2^-126) adds nothing.
+// (below 2^-126) adds nothing.  That rounding is the product's: its operands are of
+// one type, the values'.  Totals are of the weights before it.  With the output's own
+// rounding it makes 1.3 to 1.4 times the error of that alone.
 // Slots past a length hold anything: their scores are replaced by -inf, and
 // the issuing warp zeroes their values in shared memory (0 * NaN is NaN).
 // Measured (32 query heads, 8 cache heads, D 128): 4096 tokens behind 4096
@@ -35,7 +37,7 @@
 // 16 x 24 tokens over 16384 keys 192 us (5.6 TB/s).
 // Trees of drafts (kTree): what a row sees comes from its row of the mask, looked at only in steps that
 // reach the new tokens.  32 trees of 8 to 64 tokens (32 to 256 rows) over 100 to 8192: 148 us (3.7 TB/s;
-// tensor pipe 36 %: tiles of 256 rows are 56 % full), one of 26 over 517 17 to 19 us.
+// tensor pipe 36 %: tiles of 256 rows are 56 % full), one of 26 over 517 19 us with its join.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -53,8 +55,10 @@ using namespace at;
 
 constexpr int kRT = 256;
 constexpr int kKT = 128;
-// Steps that a tile's queries, output and joins are worth.  Trees: 32 of 8 to 64 tokens took 164 us with 3, 157
-// with 5, 148 with 8, 152 with 12 and 157 with 18.  (Steps of tiles with one half counted as half of one: 171.)
+// Steps that a tile's queries, output and joins are worth.  Trees, layout and attention: 32 of 8 to 64 tokens take
+// 160 us with 5, 152 with 8 and 157 with 12 (the attention alone 164 with 3, 148 with 8 and 157 with 18; steps of
+// tiles with one half counted as half of one: 171); one of 26 over 517 22 us with 5, 8 and 12, two over 30k and 65k
+// 56, 57 and 57.
 constexpr int kChunkCost = 5;
 constexpr int kTreeCost = 8;
 constexpr int kSoft = 512;         // softmax threads
@@ -576,10 +580,13 @@ __global__ void __launch_bounds__(kJoinNT) attn_join_kernel(const __grid_constan
 
 template <int D>
 cudaError_t run(const engram_attn_plan* p, const engram_kv_cache* c, AttnArgs a, int max_new, cudaStream_t s) {
-  // Trees of few tiles are cut into many parts: joined by a kernel of their own (2 trees of 64 tokens over 30k and
-  // 65k, 8 tiles: 51 us, in the tiles kernel 86).  With a tile for every block or more, a tile has two or three
-  // parts, and the joins run beside other tiles' steps (32 trees, 256 tiles: 159 us, with the other kernel 164; both
-  // before their costs were set).
+  // Trees of few tiles are cut into many parts: joined by a kernel of their own.  With a tile for every block or
+  // more, a tile has two or three parts, and the joins run beside other tiles' steps.  Trees of 26 tokens over 4000,
+  // 8 cache heads of 128, a tile each, joined by the kernel or in place: 8 tiles 28 and 54 us, 32 tiles 35 and 47,
+  // 64 tiles 54 and 49, 128 tiles 82 and 77, 160 tiles 94 and 90, 256 tiles 131 and 126, 512 tiles 229 and 224.  Over
+  // 600: 20 and 32, 23 and 23, 26 and 25, 33 and 38, 39 and 40, 44 and 41, 75 and 74.  So where the two are level
+  // depends on the length, at 40 to 60 tiles over long texts and beyond 128 over short ones; the rule gives away 5 to
+  // 10 % between. (two trees over 30k and 65k 56 and 92, one of 26 over 517 22 and 33)
   const int64_t tiles = (static_cast<int64_t>(max_new) * a.group + kRT - 1) / kRT * a.seq.B * a.heads_kv;
   if (a.causal != kSeesTree || tiles >= p->num_sms) a.splits = nullptr;
   auto* kernel = a.causal == kSeesTree ? attn_tiles_kernel<D, true> : attn_tiles_kernel<D, false>;
